@@ -64,6 +64,9 @@ typedef enum {
                                       give up after 2 s, or after the number of ns in
                                       the environment variable TQ_TEST_WAIT_NS (read
                                       at each call; for tests of this path). */
+#define TQ_DEV_BAD_BLOCK      0x8  /* a block table entry was outside the cache */
+#define TQ_DEV_BAD_LENGTH     0x10 /* a sequence's length did not fit its arrays */
+#define TQ_DEV_NONFINITE      0x20 /* a written value was NaN, infinite or beyond 2^127 */
 
 typedef enum { TQ_F32 = 0, TQ_BF16 = 1 } tq_dtype;
 
@@ -390,6 +393,167 @@ tq_status tq_search_merge_topk(int32_t n_queries, int32_t k,
 /* Scratch bytes tq_search_topk needs for one pass over min(n_queries, 16384)
  * queries (0 on invalid arguments). */
 size_t tq_search_workspace_bytes(const tq_layout* layout, int32_t n_queries, int64_t n_db, int32_t k);
+
+/* ------------------------------------------------------------------------
+ * tq_qk_norm_rope — RMS norm of every query and key head and the position
+ * rotation, in one pass (one launch; device).
+ *
+ * gist.science TurboESM section 2A: RoPE precedes everything else that happens
+ * to a key; models that norm their heads do so before it. Its outputs are what
+ * tq_quantize_kv / tq_append_kv (with positions NULL), tq_cache8_write and the
+ * two attentions take.
+ *   y      = x * rsqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
+ *   (y_i, y_{i+r/2}) turned by positions[t] * rope_base^(-2i/r), i < r/2,
+ *            r = rot_dim; elements r..d-1 are not turned (positions NULL: none)
+ * Arithmetic in fp32, the angle in fp64; one rounding to dtype.
+ *
+ *  d            multiple of 8 in [8, 256];  rot_dim multiple of 8 in [0, d]
+ *  q, k         device, head h of token t at q + t*token_stride + h*head_stride
+ *               (elements; slices of a fused projection are fine); hq or hkv
+ *               may be 0
+ *  q_out, k_out same indexing; each may be its own input, else the buffers
+ *               must not overlap
+ *  q_weight, k_weight   device float [d] or NULL (no norm)
+ *  positions    device int32 [n_tokens] or NULL (no rotation); a negative one
+ *               sets TQ_DEV_BAD_POSITION and is used as it is
+ * Bases and strides must keep four elements aligned (8 bytes in bf16, 16 in
+ * fp32), weights 16 bytes. Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+tq_status tq_qk_norm_rope(int32_t d, int32_t rot_dim, int64_t n_tokens, int32_t hq, int32_t hkv, tq_dtype dtype,
+                          const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                          const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                          void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                          void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+                          const float* q_weight, const float* k_weight, float eps,
+                          const int32_t* positions, float rope_base, int32_t* d_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit cache: pages of `block` tokens, one scale for each block and head.
+ *
+ * Beside the 2-4 bit rotated cache above this is the one to take when accuracy
+ * comes first: no rotation, 8 bits a coordinate, the scale amortised over
+ * block * d values.
+ *  codes   k, v        uint8 [n_blocks][heads][block][d]: e4m3 bytes or int8
+ *  scales  k_scale, v_scale  float [n_blocks][heads], powers of two;
+ *          a stored value is code * scale
+ * Token p of sequence b is row p % block of page block_table[b][p / block].
+ * block_table is device int32 [batch][table_stride]; NULL means the pages of
+ * sequence b are b*table_stride, b*table_stride + 1, ... Entries of blocks that
+ * a call does not touch may hold anything (-1, say). A page outside
+ * [0, n_blocks) that is touched sets TQ_DEV_BAD_BLOCK: nothing is written to
+ * it, it reads as zeros, and attention leaves its keys out.
+ * A scale is 2^e with the smallest e >= -100 such that the block's largest
+ * magnitude is at most 448 * 2^e (e4m3) or 127 * 2^e (int8). Being a power of
+ * two it divides exactly, so a code is its value's one rounding (nearest, ties
+ * to even), and reading back is exact in fp32 and bf16.
+ * ---------------------------------------------------------------------- */
+typedef enum { TQ_E4M3 = 0, TQ_INT8 = 1 } tq_code8;
+
+typedef struct {
+  int32_t d;          /* head dim, a multiple of 16 in [16, 256]              */
+  int32_t heads;      /* KV heads                                              */
+  int32_t block;      /* tokens per block: 16, 32, 64 or 128                   */
+  int32_t code;       /* tq_code8                                              */
+  int64_t n_blocks;   /* pages, below 2^31                                     */
+  uint8_t* k;         /* device, 128-byte aligned                              */
+  uint8_t* v;
+  float* k_scale;     /* device                                                */
+  float* v_scale;
+} tq_cache8;
+
+/* Bytes of a cache of n_blocks pages (codes and scales); -1 on invalid sizes. */
+int64_t tq_cache8_bytes(int32_t d, int32_t heads, int32_t block, int64_t n_blocks);
+
+/* ------------------------------------------------------------------------
+ * tq_cache8_write — quantise new tokens into their blocks (one launch; device).
+ *
+ * 7minutos.es Etapa 1: a token's codes are computed once, when it enters the
+ * cache. Sequence b's new tokens are rows cu_tokens[b] .. cu_tokens[b+1]-1 of
+ * k and v and take positions start[b], start[b]+1, ...: one token each in a
+ * decode step, whole prompts, or any ragged mix.
+ * Where a block holds tokens of its sequence already (start[b] % block of
+ * them), its scale only grows: to the larger of the old one and the one that
+ * the new tokens need. The held codes then follow it, each rounded once more
+ * (int8: a shift; e4m3: only values that become subnormal change). Otherwise
+ * the old scale is ignored, so a fresh cache needs no initialisation. Rows
+ * behind the last new token are left as they were.
+ * An infinite value, or one beyond 2^127, does not enter the scale and is
+ * stored as the largest code; NaN is stored as zero; both set
+ * TQ_DEV_NONFINITE.
+ *
+ *  k, v          device rows of dtype, head h of row t at
+ *                k + t*token_stride + h*head_stride (16-byte aligned, strides
+ *                multiples of 8 elements)
+ *  n_tokens      rows of k and v;  batch  sequences
+ *  cu_tokens     device int32 [batch + 1], not falling, within [0, n_tokens]
+ *  start         device int32 [batch], tokens the sequence holds before the call
+ *  table_stride  blocks of one sequence: a sequence holds at most
+ *                table_stride * block tokens
+ * Lengths the arrays do not allow set TQ_DEV_BAD_LENGTH; the tokens beyond are
+ * left out. No two sequences of a call may write to the same page.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+tq_status tq_cache8_write(const tq_cache8* cache, tq_dtype dtype,
+                          const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                          const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                          int64_t n_tokens, int32_t batch, const int32_t* cu_tokens, const int32_t* start,
+                          const int32_t* block_table, int64_t table_stride, int32_t* d_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * tq_cache8_read — tokens of the cache back as rows (one launch; device).
+ *
+ * The counterpart of tq_cache8_write with the same indexing: positions
+ * start[b] .. of sequence b become rows cu_tokens[b] .. cu_tokens[b+1]-1 of
+ * k_out and v_out (either may be NULL). code * scale, exact in fp32 and bf16.
+ * Rows of no sequence are left as they were.
+ * ---------------------------------------------------------------------- */
+tq_status tq_cache8_read(const tq_cache8* cache, tq_dtype dtype,
+                         void* k_out, int64_t k_token_stride, int64_t k_head_stride,
+                         void* v_out, int64_t v_token_stride, int64_t v_head_stride,
+                         int64_t n_tokens, int32_t batch, const int32_t* cu_tokens, const int32_t* start,
+                         const int32_t* block_table, int64_t table_stride, int32_t* d_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * tq_cache8_attention — attention of the newest queries of each sequence over
+ * the 8-bit cache (device).
+ *
+ * gist.science TurboESM section 2E: one pass over the packed cache with an
+ * online softmax and no dequantised intermediate in memory. Query row i of
+ * sequence b stands at position p = seq_lens[b] - nq + i (its own key is in
+ * the cache already); query head h reads KV head h / (hq / heads):
+ *   s_t = scale * <q, k_t>;  out = softmax(s) v;  lse = ln sum_t e^(s_t)
+ * over the keys t of [0, seq_lens[b]), with causal != 0 only t <= p, and with
+ * window > 0 (causal only) only t > p - window. A row that sees no key gets
+ * zeros and lse = -inf.
+ *
+ *  q             device [batch][hq][nq][d] of q_dtype by three strides
+ *                (elements), rows of d contiguous, 16-byte aligned
+ *  nq            query rows of every sequence: 1 to decode, a few to check
+ *                drafted tokens, many for a chunk of a prompt
+ *  seq_lens      device int32 [batch], keys in the cache (0 is fine); one that
+ *                is negative or beyond table_stride * block is cut and sets
+ *                TQ_DEV_BAD_LENGTH
+ *  out           device, as q, of out_dtype; rows must not overlap
+ *  lse_out       device float [batch][hq][nq] or NULL
+ *  workspace     device scratch of tq_cache8_attention_workspace_bytes()
+ *                bytes, 256-byte aligned; needs no initialisation. Calls that
+ *                overlap on the GPU need one each.
+ * Supported d: 64, 128, 256 (others: TQ_ERR_UNSUPPORTED). Errors:
+ * TQ_ERR_INVALID_ARG, TQ_ERR_WORKSPACE, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+tq_status tq_cache8_attention(const tq_cache8* cache,
+                              const void* q, tq_dtype q_dtype, int64_t q_batch_stride, int64_t q_head_stride,
+                              int64_t q_row_stride,
+                              int32_t batch, int32_t hq, int32_t nq, const int32_t* seq_lens,
+                              const int32_t* block_table, int64_t table_stride,
+                              int32_t causal, int32_t window, float scale,
+                              void* out, tq_dtype out_dtype, int64_t out_batch_stride, int64_t out_head_stride,
+                              int64_t out_row_stride,
+                              float* lse_out, void* workspace, size_t workspace_bytes,
+                              int32_t* d_status, void* stream);
+
+/* Scratch bytes tq_cache8_attention needs (0 on bad arguments). */
+size_t tq_cache8_attention_workspace_bytes(const tq_cache8* cache, int32_t batch, int32_t hq, int32_t nq);
 
 /* ------------------------------------------------------------------------
  * tq_fit_rotation — per-head rotation from calibration vectors (host only).

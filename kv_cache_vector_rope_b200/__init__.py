@@ -26,6 +26,8 @@ LIB_PATH = os.path.join(_PKG, "libtq.so")
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA, TQ_ERR_WORKSPACE = range(5)
 TQ_F32, TQ_BF16 = 0, 1
 TQ_DEV_BAD_CODEBOOK, TQ_DEV_BAD_POSITION, TQ_DEV_TIMEOUT = 0x1, 0x2, 0x4
+TQ_DEV_BAD_BLOCK, TQ_DEV_BAD_LENGTH, TQ_DEV_NONFINITE = 0x8, 0x10, 0x20
+TQ_E4M3, TQ_INT8 = 0, 1
 
 _STATUS = {1: "TQ_ERR_INVALID_ARG", 2: "TQ_ERR_UNSUPPORTED", 3: "TQ_ERR_CUDA", 4: "TQ_ERR_WORKSPACE"}
 
@@ -43,6 +45,12 @@ class Layout(ctypes.Structure):
 class _Planes(ctypes.Structure):
     _fields_ = [("idx", ctypes.c_void_p), ("sign", ctypes.c_void_p), ("norm", ctypes.c_void_p),
                 ("rnorm", ctypes.c_void_p)]
+
+
+class _Cache8(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("heads", ctypes.c_int32), ("block", ctypes.c_int32), ("code", ctypes.c_int32),
+                ("n_blocks", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -74,6 +82,17 @@ _SIGNATURES = {
                                       _P, _P, _P, _I32, _P, _P, _P, _SZ, _P]),
     "tq_search_merge_topk": (ctypes.c_int, [_I32, _I32, _P, _P, _I64, _P, _P, _I64, _P, _P, _P]),
     "tq_search_workspace_bytes": (_SZ, [ctypes.POINTER(Layout), _I32, _I64, _I32]),
+    "tq_qk_norm_rope": (ctypes.c_int, [_I32, _I32, _I64, _I32, _I32, ctypes.c_int, _P, _I64, _I64, _P, _I64, _I64, _P,
+                                       _I64, _I64, _P, _I64, _I64, _P, _P, _F32, _P, _F32, _P, _P]),
+    "tq_cache8_bytes": (_I64, [_I32, _I32, _I32, _I64]),
+    "tq_cache8_write": (ctypes.c_int, [ctypes.POINTER(_Cache8), ctypes.c_int, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32,
+                                       _P, _P, _P, _I64, _P, _P]),
+    "tq_cache8_read": (ctypes.c_int, [ctypes.POINTER(_Cache8), ctypes.c_int, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32,
+                                      _P, _P, _P, _I64, _P, _P]),
+    "tq_cache8_attention": (ctypes.c_int, [ctypes.POINTER(_Cache8), _P, ctypes.c_int, _I64, _I64, _I64, _I32, _I32, _I32,
+                                           _P, _P, _I64, _I32, _I32, _F32, _P, ctypes.c_int, _I64, _I64, _I64, _P, _P,
+                                           _SZ, _P, _P]),
+    "tq_cache8_attention_workspace_bytes": (_SZ, [ctypes.POINTER(_Cache8), _I32, _I32, _I32]),
     "tq_fit_rotation": (ctypes.c_int, [_I32, _P, _I64, _P, _P]),
     "tq_rotate_normalize": (ctypes.c_int, [_I32, _P, _I64, _P, _P, ctypes.POINTER(_I64)]),
     "tq_last_error_string": (ctypes.c_char_p, []),
@@ -298,6 +317,199 @@ def tq_dequantize_sign_mean(lay: Layout, is_key: bool, planes: Planes, n_vectors
                                         _dev(Pi, "Pi"), vectors_per_pi, pi_stride, _dev(centroids, "centroids"),
                                         float(e_bar), _dev(out, "out"), _dtype_code(out), out.stride(0),
                                         _stream(stream)))
+
+
+def _same_device(**tensors) -> None:
+    """Every given tensor is a CUDA tensor on the current device (the library launches there)."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:          # -1 for a CPU tensor
+            raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev}), not {t.device}")
+
+
+def _rows_ok(t: torch.Tensor) -> bool:
+    """Unit stride along the last dimension (a tensor without elements has no strides that matter)."""
+    return t.stride(-1) == 1 or t.numel() == 0
+
+
+def _strides(t) -> tuple:
+    """Element strides of all dimensions but the last; 0 where a dimension has one index, whose stride means nothing."""
+    return tuple(st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape))
+
+
+def _int32(t, name: str, *shape) -> None:
+    """An int32 tensor, contiguous, of the given shape."""
+    if t is None:
+        return
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _status_word(t) -> None:
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+        raise ValueError("d_status must be an int32 tensor with an element")
+
+
+def tq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None,
+                    k_out: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+                    k_weight: torch.Tensor | None = None, eps: float = 1e-6, positions: torch.Tensor | None = None,
+                    rope_base: float = 10000.0, rot_dim: int | None = None, d_status: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """Per-head RMS norm and position rotation of q ([tokens, hq, d]) and k ([tokens, hkv, d]) into q_out and k_out.
+
+    The tensors may be strided views (unit stride along d), an output its own input; a side that is None is left out,
+    as is the norm of a side without a weight ([d] float32) and the rotation without positions ([tokens] int32)."""
+    one = q if q is not None else k
+    if one is None or one.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, d] tensors, one of them at least")
+    n, _, d = one.shape
+    args, heads = [], []
+    for x, o, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if (x is None) != (o is None):
+            raise ValueError(f"{name} and {name}_out go together")
+        if x is None:
+            heads.append(0)
+            args.append((None, 0, 0, None, 0, 0))
+            continue
+        if x.shape != (n, x.shape[1], d) or o.shape != x.shape or not _rows_ok(x) or not _rows_ok(o):
+            raise ValueError(f"{name} and {name}_out must be [tokens, heads, d] with unit stride along d")
+        if x.dtype != one.dtype or o.dtype != one.dtype:
+            raise ValueError("q, k and their outputs must have one dtype")
+        heads.append(x.shape[1])
+        args.append((x.data_ptr(), *_strides(x), o.data_ptr(), *_strides(o)))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape [{d}]")
+    _int32(positions, "positions", n)
+    _status_word(d_status)
+    _same_device(q=q, k=k, q_out=q_out, k_out=k_out, q_weight=q_weight, k_weight=k_weight, positions=positions,
+                 d_status=d_status)
+    a, b = args
+    _check(_lib.tq_qk_norm_rope(d, d if rot_dim is None else rot_dim, n, heads[0], heads[1], _dtype_code(one), a[0], a[1],
+                                a[2], b[0], b[1], b[2], a[3], a[4], a[5], b[3], b[4], b[5], _ptr(q_weight),
+                                _ptr(k_weight), eps, _ptr(positions), rope_base, _ptr(d_status), _stream(stream)))
+
+
+@dataclasses.dataclass
+class Cache8:
+    """A paged 8-bit KV cache (torch tensors on one device): token p of a sequence is row p % block of the page that
+    its block table names for p // block; a stored value is code * scale."""
+    k: torch.Tensor              # uint8 [n_blocks, heads, block, d]
+    v: torch.Tensor
+    k_scale: torch.Tensor        # float32 [n_blocks, heads], powers of two
+    v_scale: torch.Tensor
+    code: str = "e4m3"           # or "int8"
+
+    def c(self) -> _Cache8:
+        n, h, b, d = self.k.shape
+        for t, shape, dtype in ((self.k, (n, h, b, d), torch.uint8), (self.v, (n, h, b, d), torch.uint8),
+                                (self.k_scale, (n, h), torch.float32), (self.v_scale, (n, h), torch.float32)):
+            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError("a Cache8 has contiguous uint8 [n_blocks, heads, block, d] codes and float32 "
+                                 "[n_blocks, heads] scales")
+        if self.code not in _CODE8:
+            raise ValueError(f"unknown code {self.code!r} (e4m3 or int8)")
+        _same_device(k=self.k, v=self.v, k_scale=self.k_scale, v_scale=self.v_scale)
+        return _Cache8(d, h, b, _CODE8[self.code], n, self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                       self.v_scale.data_ptr())
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale))
+
+
+_CODE8 = {"e4m3": TQ_E4M3, "int8": TQ_INT8}
+
+
+def tq_cache8_bytes(d: int, heads: int, block: int, n_blocks: int) -> int:
+    return int(_lib.tq_cache8_bytes(d, heads, block, n_blocks))
+
+
+def alloc_cache8(n_blocks: int, heads: int, block: int, d: int, code: str = "e4m3", device="cuda") -> Cache8:
+    """Allocates a cache of n_blocks pages (allocation is PyTorch's; it needs no initialisation)."""
+    codes = [torch.empty((n_blocks, heads, block, d), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.empty((n_blocks, heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return Cache8(*codes, *scales, code)
+
+
+def _table8(cache: Cache8, block_table, batch: int) -> int:
+    """Checks a block table and returns its stride (without one, every sequence has an equal share of the pages)."""
+    if block_table is None:
+        return cache.k.shape[0] // max(batch, 1)
+    _int32(block_table, "block_table", batch, block_table.shape[-1])
+    return block_table.shape[1]
+
+
+def _rows8(fn, cache: Cache8, k, v, cu_tokens, start, block_table, d_status, stream) -> None:
+    one = k if k is not None else v
+    h, d = cache.k.shape[1], cache.k.shape[3]
+    if one is None:
+        raise ValueError("k and v are both None")
+    n = one.shape[0]
+    for x in (k, v):
+        if x is not None and (x.shape != (n, h, d) or not _rows_ok(x) or x.dtype != one.dtype):
+            raise ValueError(f"k and v must be [tokens, {h}, {d}] tensors of one dtype with unit stride along d")
+    batch = start.shape[0]
+    _int32(cu_tokens, "cu_tokens", batch + 1)
+    _int32(start, "start", batch)
+    stride = _table8(cache, block_table, batch)
+    _status_word(d_status)
+    _same_device(k=k, v=v, cu_tokens=cu_tokens, start=start, block_table=block_table, d_status=d_status)
+    ks, vs = (_strides(x) if x is not None else (0, 0) for x in (k, v))
+    _check(fn(ctypes.byref(cache.c()), _dtype_code(one), _ptr(k), *ks, _ptr(v), *vs, n, batch, cu_tokens.data_ptr(),
+              start.data_ptr(), _ptr(block_table), stride, _ptr(d_status), _stream(stream)))
+
+
+def tq_cache8_write(cache: Cache8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
+                    block_table: torch.Tensor | None = None, d_status: torch.Tensor | None = None, stream=None) -> None:
+    """Quantises rows cu_tokens[b] .. cu_tokens[b+1]-1 of k and v ([tokens, heads, d]) into positions start[b], ...
+    of sequence b (cu_tokens int32 [batch+1], start int32 [batch], block_table int32 [batch, blocks])."""
+    if k is None or v is None:
+        raise ValueError("tq_cache8_write needs k and v")
+    _rows8(_lib.tq_cache8_write, cache, k, v, cu_tokens, start, block_table, d_status, stream)
+
+
+def tq_cache8_read(cache: Cache8, k_out: torch.Tensor | None, v_out: torch.Tensor | None, cu_tokens: torch.Tensor,
+                   start: torch.Tensor, block_table: torch.Tensor | None = None, d_status: torch.Tensor | None = None,
+                   stream=None) -> None:
+    """Reads positions start[b], ... of sequence b back into rows cu_tokens[b] .. cu_tokens[b+1]-1 of k_out and v_out."""
+    _rows8(_lib.tq_cache8_read, cache, k_out, v_out, cu_tokens, start, block_table, d_status, stream)
+
+
+def tq_cache8_attention_workspace_bytes(cache: Cache8, batch: int, hq: int, nq: int) -> int:
+    return int(_lib.tq_cache8_attention_workspace_bytes(ctypes.byref(cache.c()), batch, hq, nq))
+
+
+def cache8_attention_workspace(cache: Cache8, batch: int, hq: int, nq: int) -> torch.Tensor:
+    n = tq_cache8_attention_workspace_bytes(cache, batch, hq, nq)
+    return torch.empty((max(n, 256) + 255) // 256 * 256, dtype=torch.uint8, device=cache.k.device)
+
+
+def tq_cache8_attention(cache: Cache8, q: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor,
+                        workspace: torch.Tensor, block_table: torch.Tensor | None = None, causal: bool = True,
+                        window: int = 0, scale: float | None = None, lse_out: torch.Tensor | None = None,
+                        d_status: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of q ([batch, hq, nq, d], any strides with unit stride along d) over the first seq_lens[b] tokens of
+    each sequence; row i stands at position seq_lens[b] - nq + i. out is as q, lse_out float32 [batch, hq, nq]."""
+    if q.dim() != 4 or out.shape != q.shape or not _rows_ok(q) or not _rows_ok(out):
+        raise ValueError("q and out must be [batch, hq, nq, d] tensors with unit stride along d")
+    batch, hq, nq, d = q.shape
+    if d != cache.k.shape[3]:
+        raise ValueError(f"q has d = {d}, the cache {cache.k.shape[3]}")
+    _int32(seq_lens, "seq_lens", batch)
+    stride = _table8(cache, block_table, batch)
+    if lse_out is not None and (lse_out.dtype != torch.float32 or lse_out.shape != (batch, hq, nq)
+                                or not lse_out.is_contiguous()):
+        raise ValueError("lse_out must be a contiguous float32 [batch, hq, nq] tensor")
+    _status_word(d_status)
+    _same_device(q=q, seq_lens=seq_lens, out=out, workspace=workspace, block_table=block_table, lse_out=lse_out,
+                 d_status=d_status)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _check(_lib.tq_cache8_attention(
+        ctypes.byref(cache.c()), q.data_ptr(), _dtype_code(q), *_strides(q), batch, hq, nq,
+        seq_lens.data_ptr(), _ptr(block_table), stride, int(causal), window, scale, out.data_ptr(), _dtype_code(out),
+        *_strides(out), _ptr(lse_out), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _ptr(d_status), _stream(stream)))
 
 
 def tq_residual_mean(samples, centroids, boundaries, bits: int) -> float:

@@ -1,0 +1,117 @@
+// Internal interface of the 8-bit block-scaled cache (tq_cache8*.cu).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tq.h"
+#include "tq_internal.h"
+
+namespace tq {
+
+// Sequences one launch handles: their prefix sums live in shared memory. Calls
+// with more are split into launches over slices of the batch.
+constexpr int kC8Slice = 1024;
+
+// Validates a cache descriptor (host); `what` names the entry point.
+tq_status check_cache8(const tq_cache8* c, const char* what);
+// Validates a block table: stride, and that every token position fits int32.
+tq_status check_table8(const tq_cache8* c, int32_t batch, int64_t table_stride, const char* what);
+
+// Whether rows of d elements at i * si + j * sj (i < ni, j < nj) can overlap: the
+// smaller stride's rows must fit within the larger stride.
+inline bool rows_overlap(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t d) {
+  if (ni > 1 && nj > 1) {
+    const bool i_in = si <= sj;
+    const int64_t n = i_in ? ni : nj, s = i_in ? si : sj, S = i_in ? sj : si;
+    return s < d || S - d < 0 || (n - 1) > (S - d) / s;
+  }
+  return (ni > 1 && si < d) || (nj > 1 && sj < d);
+}
+
+namespace c8 {
+
+// Largest magnitude that takes part in a block's scale; what lies beyond
+// (infinities included) is stored as the largest code.
+constexpr float kMost = 1.7014118346046923e38f;      // 2^127
+
+// Scale of a block whose largest magnitude is amax <= 2^127: the smallest
+// power of two 2^e with amax <= M 2^e, M = 448 = 1.75 * 2^8 (e4m3) or
+// 127 = 1.984375 * 2^6 (int8), and e >= -100. From the bits of amax: its
+// exponent, and whether its mantissa is above M's.
+template <bool INT8>
+__device__ __forceinline__ float block_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int E = static_cast<int>(u >> 23) - 127;
+  const uint32_t frac = u & 0x7fffffu;
+  int e = INT8 ? E - 6 + (frac > 0x7e0000u ? 1 : 0) : E - 8 + (frac > 0x600000u ? 1 : 0);
+  e = max(e, -100);                                  // zero and tiny blocks (E = -127) too
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// 1 / scale for a scale that is a power of two in [2^-100, 2^121]: exact.
+__device__ __forceinline__ float inv_pow2(float s) {
+  return __uint_as_float((254u << 23) - (__float_as_uint(s) & 0x7f800000u));
+}
+
+// Code of a value already divided by the scale: nearest, ties to even,
+// saturating. NaN has no code of its own and is stored as zero.
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode(float y) {
+  if (!(y == y)) return 0u;
+  if (INT8) return static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(y, -127.f), 127.f))) & 0xffu;
+  return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+}
+
+template <bool INT8>
+__device__ __forceinline__ float decode(uint32_t code) {
+  if (INT8) return static_cast<float>(static_cast<int8_t>(code));
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
+}
+
+// Largest b in [0, n) with cum[b] <= u, for cum[0] = 0 <= u < cum[n].
+__device__ __forceinline__ int find_seq(const int* cum, int n, int u) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// cum[0..n] = exclusive prefix sums of count(b), b < n <= kC8Slice, by a CTA of
+// T threads (T a multiple of 32, T <= 1024). `part` holds T / 32 ints. A count
+// is below 2^26, so that a warp's 32 stay below 2^31.
+template <int T, typename F>
+__device__ __forceinline__ void scan_counts(int* cum, int* part, int n, F count) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  int base = 0;
+  for (int at = 0; at < n; at += T) {
+    const int b = at + tid;
+    int v = b < n ? count(b) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    if (lane == 31) part[w] = v;
+    __syncthreads();
+    long long before = base, all = base;
+    for (int k = 0; k < T / 32; ++k) {
+      const int x = part[k];
+      if (k < w) before += x;
+      all += x;
+    }
+    // Sums beyond int32 (malformed lengths only) stay at its top, so that cum never falls.
+    if (b < n) cum[b + 1] = static_cast<int>(min(before + v, 0x7fffffffll));
+    base = static_cast<int>(min(all, 0x7fffffffll));
+    __syncthreads();
+  }
+  if (tid == 0) cum[0] = 0;
+  __syncthreads();
+}
+
+}  // namespace c8
+}  // namespace tq

@@ -17,6 +17,7 @@ Modules:
   attention  scores over packed planes, softmax attention, dequantisation.
   calib      per-head SVD basis composed with the random rotation.
   search     estimated-score and exact top-k over a compressed corpus.
+  cache8     the 8-bit block-scaled paged cache: write, read, attention, q/k norm with RoPE.
 
 Every function is pinned by tests under ``tests/test_oracle_*.py`` against
 closed forms, printed worked examples, brute force or statistical identities.
