@@ -150,8 +150,8 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:                                       # the raw handle: a Stream object costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -319,35 +319,49 @@ def tq_dequantize_sign_mean(lay: Layout, is_key: bool, planes: Planes, n_vectors
                                         _stream(stream)))
 
 
-def _same_device(**tensors) -> None:
+# The checks below are written out flat: a call of a decode step takes the GPU 3 to 10 us, and these lines are most of
+# what it takes the host.
+def _on_device(*tensors) -> None:
     """Every given tensor is a CUDA tensor on the current device (the library launches there)."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+    for t in tensors:
         if t is not None and t.get_device() != dev:          # -1 for a CPU tensor
-            raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev}), not {t.device}")
+            raise ValueError(f"a {list(t.shape)} tensor is on {t.device}: all must be CUDA tensors on the current "
+                             f"device (cuda:{dev})")
 
 
-def _rows_ok(t: torch.Tensor) -> bool:
-    """Unit stride along the last dimension (a tensor without elements has no strides that matter)."""
-    return t.stride(-1) == 1 or t.numel() == 0
-
-
-def _strides(t) -> tuple:
-    """Element strides of all dimensions but the last; 0 where a dimension has one index, whose stride means nothing."""
-    return tuple(st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape))
-
-
-def _int32(t, name: str, *shape) -> None:
+def _int32(t, name: str, shape: tuple) -> None:
     """An int32 tensor, contiguous, of the given shape."""
-    if t is None:
-        return
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
 
 
-def _status_word(t) -> None:
-    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+def _status_word(t) -> int | None:
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.numel() < 1:
         raise ValueError("d_status must be an int32 tensor with an element")
+    return t.data_ptr()
+
+
+def _weight(w, name: str, d: int) -> int | None:
+    if w is None:
+        return None
+    if w.dtype is not torch.float32 or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape [{d}]")
+    return w.data_ptr()
+
+
+def _heads(x: torch.Tensor, o: torch.Tensor, one: torch.Tensor, name: str) -> tuple:
+    """Pointers and strides of [tokens, heads, d] rows and of the rows they become."""
+    xs, os_ = x.stride(), o.stride()
+    if x.dim() != 3 or x.shape[0] != one.shape[0] or x.shape[2] != one.shape[2] or o.shape != x.shape:
+        raise ValueError(f"{name} and {name}_out must be [tokens, heads, d] tensors of the same shape")
+    if x.numel() and (xs[2] != 1 or os_[2] != 1):
+        raise ValueError(f"{name} and {name}_out must have unit stride along d")
+    if x.dtype is not one.dtype or o.dtype is not one.dtype:
+        raise ValueError("q, k and their outputs must have one dtype")
+    return x.shape[1], x.data_ptr(), xs[0], xs[1], o.data_ptr(), os_[0], os_[1]
 
 
 def tq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None,
@@ -362,35 +376,28 @@ def tq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch
     one = q if q is not None else k
     if one is None or one.dim() != 3:
         raise ValueError("q and k must be [tokens, heads, d] tensors, one of them at least")
-    n, _, d = one.shape
-    args, heads = [], []
-    for x, o, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if (x is None) != (o is None):
-            raise ValueError(f"{name} and {name}_out go together")
-        if x is None:
-            heads.append(0)
-            args.append((None, 0, 0, None, 0, 0))
-            continue
-        if x.shape != (n, x.shape[1], d) or o.shape != x.shape or not _rows_ok(x) or not _rows_ok(o):
-            raise ValueError(f"{name} and {name}_out must be [tokens, heads, d] with unit stride along d")
-        if x.dtype != one.dtype or o.dtype != one.dtype:
-            raise ValueError("q, k and their outputs must have one dtype")
-        heads.append(x.shape[1])
-        args.append((x.data_ptr(), *_strides(x), o.data_ptr(), *_strides(o)))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape [{d}]")
-    _int32(positions, "positions", n)
-    _status_word(d_status)
-    _same_device(q=q, k=k, q_out=q_out, k_out=k_out, q_weight=q_weight, k_weight=k_weight, positions=positions,
-                 d_status=d_status)
-    a, b = args
-    _check(_lib.tq_qk_norm_rope(d, d if rot_dim is None else rot_dim, n, heads[0], heads[1], _dtype_code(one), a[0], a[1],
-                                a[2], b[0], b[1], b[2], a[3], a[4], a[5], b[3], b[4], b[5], _ptr(q_weight),
-                                _ptr(k_weight), eps, _ptr(positions), rope_base, _ptr(d_status), _stream(stream)))
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q and q_out, and k and k_out, go together")
+    n, d = one.shape[0], one.shape[2]
+    hq, qp, qt, qh, qop, qot, qoh = _heads(q, q_out, one, "q") if q is not None else (0, None, 0, 0, None, 0, 0)
+    hk, kp, kt, kh, kop, kot, koh = _heads(k, k_out, one, "k") if k is not None else (0, None, 0, 0, None, 0, 0)
+    pos = None
+    if positions is not None:
+        _int32(positions, "positions", (n,))
+        pos = positions.data_ptr()
+    _on_device(q, k, q_out, k_out, q_weight, k_weight, positions, d_status)
+    st = _lib.tq_qk_norm_rope(d, d if rot_dim is None else rot_dim, n, hq, hk, _dtype_code(one), qp, qt, qh, kp, kt, kh,
+                              qop, qot, qoh, kop, kot, koh, _weight(q_weight, "q_weight", d),
+                              _weight(k_weight, "k_weight", d), eps, pos, rope_base, _status_word(d_status),
+                              _stream(stream))
+    if st:
+        _check(st)
 
 
-@dataclasses.dataclass
+_CODE8 = {"e4m3": TQ_E4M3, "int8": TQ_INT8}
+
+
+@dataclasses.dataclass(slots=True)
 class Cache8:
     """A paged 8-bit KV cache (torch tensors on one device): token p of a sequence is row p % block of the page that
     its block table names for p // block; a stored value is code * scale."""
@@ -401,23 +408,22 @@ class Cache8:
     code: str = "e4m3"           # or "int8"
 
     def c(self) -> _Cache8:
-        n, h, b, d = self.k.shape
-        for t, shape, dtype in ((self.k, (n, h, b, d), torch.uint8), (self.v, (n, h, b, d), torch.uint8),
-                                (self.k_scale, (n, h), torch.float32), (self.v_scale, (n, h), torch.float32)):
-            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
-                raise ValueError("a Cache8 has contiguous uint8 [n_blocks, heads, block, d] codes and float32 "
-                                 "[n_blocks, heads] scales")
-        if self.code not in _CODE8:
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        if k.dim() != 4:
+            raise ValueError("codes must be [n_blocks, heads, block, d]")
+        n, h, b, d = k.shape
+        if (v.shape != k.shape or ks.shape != (n, h) or vs.shape != (n, h) or k.dtype is not torch.uint8
+                or v.dtype is not torch.uint8 or ks.dtype is not torch.float32 or vs.dtype is not torch.float32
+                or not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())):
+            raise ValueError("a Cache8 has contiguous uint8 [n_blocks, heads, block, d] codes and float32 "
+                             "[n_blocks, heads] scales")
+        code = _CODE8.get(self.code)
+        if code is None:
             raise ValueError(f"unknown code {self.code!r} (e4m3 or int8)")
-        _same_device(k=self.k, v=self.v, k_scale=self.k_scale, v_scale=self.v_scale)
-        return _Cache8(d, h, b, _CODE8[self.code], n, self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-                       self.v_scale.data_ptr())
+        return _Cache8(d, h, b, code, n, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale))
-
-
-_CODE8 = {"e4m3": TQ_E4M3, "int8": TQ_INT8}
 
 
 def tq_cache8_bytes(d: int, heads: int, block: int, n_blocks: int) -> int:
@@ -431,32 +437,35 @@ def alloc_cache8(n_blocks: int, heads: int, block: int, d: int, code: str = "e4m
     return Cache8(*codes, *scales, code)
 
 
-def _table8(cache: Cache8, block_table, batch: int) -> int:
-    """Checks a block table and returns its stride (without one, every sequence has an equal share of the pages)."""
-    if block_table is None:
-        return cache.k.shape[0] // max(batch, 1)
-    _int32(block_table, "block_table", batch, block_table.shape[-1])
-    return block_table.shape[1]
+def _table8(c: _Cache8, table, batch: int) -> tuple:
+    """Pointer and stride of a block table (without one, every sequence has an equal share of the pages)."""
+    if table is None:
+        return None, c.n_blocks // max(batch, 1)
+    if table.dim() != 2 or table.shape[0] != batch or table.dtype is not torch.int32 or not table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [batch, blocks] tensor")
+    return table.data_ptr(), table.shape[1]
 
 
 def _rows8(fn, cache: Cache8, k, v, cu_tokens, start, block_table, d_status, stream) -> None:
+    c = cache.c()
     one = k if k is not None else v
-    h, d = cache.k.shape[1], cache.k.shape[3]
     if one is None:
         raise ValueError("k and v are both None")
-    n = one.shape[0]
+    shape = (one.shape[0], c.heads, c.d)
     for x in (k, v):
-        if x is not None and (x.shape != (n, h, d) or not _rows_ok(x) or x.dtype != one.dtype):
-            raise ValueError(f"k and v must be [tokens, {h}, {d}] tensors of one dtype with unit stride along d")
+        if x is not None and (x.shape != shape or x.dtype is not one.dtype or (x.stride(2) != 1 and x.numel())):
+            raise ValueError(f"k and v must be [tokens, {c.heads}, {c.d}] tensors of one dtype with unit stride along d")
+    kp, kt, kh = (k.data_ptr(), k.stride(0), k.stride(1)) if k is not None else (None, 0, 0)
+    vp, vt, vh = (v.data_ptr(), v.stride(0), v.stride(1)) if v is not None else (None, 0, 0)
     batch = start.shape[0]
-    _int32(cu_tokens, "cu_tokens", batch + 1)
-    _int32(start, "start", batch)
-    stride = _table8(cache, block_table, batch)
-    _status_word(d_status)
-    _same_device(k=k, v=v, cu_tokens=cu_tokens, start=start, block_table=block_table, d_status=d_status)
-    ks, vs = (_strides(x) if x is not None else (0, 0) for x in (k, v))
-    _check(fn(ctypes.byref(cache.c()), _dtype_code(one), _ptr(k), *ks, _ptr(v), *vs, n, batch, cu_tokens.data_ptr(),
-              start.data_ptr(), _ptr(block_table), stride, _ptr(d_status), _stream(stream)))
+    _int32(cu_tokens, "cu_tokens", (batch + 1,))
+    _int32(start, "start", (batch,))
+    table, stride = _table8(c, block_table, batch)
+    _on_device(cache.k, cache.v, cache.k_scale, cache.v_scale, k, v, cu_tokens, start, block_table, d_status)
+    st = fn(c, _dtype_code(one), kp, kt, kh, vp, vt, vh, shape[0], batch, cu_tokens.data_ptr(), start.data_ptr(), table,
+            stride, _status_word(d_status), _stream(stream))
+    if st:
+        _check(st)
 
 
 def tq_cache8_write(cache: Cache8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
@@ -476,7 +485,7 @@ def tq_cache8_read(cache: Cache8, k_out: torch.Tensor | None, v_out: torch.Tenso
 
 
 def tq_cache8_attention_workspace_bytes(cache: Cache8, batch: int, hq: int, nq: int) -> int:
-    return int(_lib.tq_cache8_attention_workspace_bytes(ctypes.byref(cache.c()), batch, hq, nq))
+    return int(_lib.tq_cache8_attention_workspace_bytes(cache.c(), batch, hq, nq))
 
 
 def cache8_attention_workspace(cache: Cache8, batch: int, hq: int, nq: int) -> torch.Tensor:
@@ -490,26 +499,30 @@ def tq_cache8_attention(cache: Cache8, q: torch.Tensor, seq_lens: torch.Tensor, 
                         d_status: torch.Tensor | None = None, stream=None) -> None:
     """Attention of q ([batch, hq, nq, d], any strides with unit stride along d) over the first seq_lens[b] tokens of
     each sequence; row i stands at position seq_lens[b] - nq + i. out is as q, lse_out float32 [batch, hq, nq]."""
-    if q.dim() != 4 or out.shape != q.shape or not _rows_ok(q) or not _rows_ok(out):
-        raise ValueError("q and out must be [batch, hq, nq, d] tensors with unit stride along d")
+    c = cache.c()
+    if q.dim() != 4 or out.shape != q.shape:
+        raise ValueError("q and out must be [batch, hq, nq, d] tensors of the same shape")
     batch, hq, nq, d = q.shape
-    if d != cache.k.shape[3]:
-        raise ValueError(f"q has d = {d}, the cache {cache.k.shape[3]}")
-    _int32(seq_lens, "seq_lens", batch)
-    stride = _table8(cache, block_table, batch)
-    if lse_out is not None and (lse_out.dtype != torch.float32 or lse_out.shape != (batch, hq, nq)
-                                or not lse_out.is_contiguous()):
-        raise ValueError("lse_out must be a contiguous float32 [batch, hq, nq] tensor")
-    _status_word(d_status)
-    _same_device(q=q, seq_lens=seq_lens, out=out, workspace=workspace, block_table=block_table, lse_out=lse_out,
-                 d_status=d_status)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    _check(_lib.tq_cache8_attention(
-        ctypes.byref(cache.c()), q.data_ptr(), _dtype_code(q), *_strides(q), batch, hq, nq,
-        seq_lens.data_ptr(), _ptr(block_table), stride, int(causal), window, scale, out.data_ptr(), _dtype_code(out),
-        *_strides(out), _ptr(lse_out), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _ptr(d_status), _stream(stream)))
+    qb, qh, qr, qd = q.stride()
+    ob, oh, orow, od = out.stride()
+    if (qd != 1 or od != 1) and q.numel():
+        raise ValueError("q and out must have unit stride along d")
+    if d != c.d:
+        raise ValueError(f"q has d = {d}, the cache {c.d}")
+    _int32(seq_lens, "seq_lens", (batch,))
+    table, stride = _table8(c, block_table, batch)
+    lse = None
+    if lse_out is not None:
+        if lse_out.dtype is not torch.float32 or lse_out.shape != (batch, hq, nq) or not lse_out.is_contiguous():
+            raise ValueError("lse_out must be a contiguous float32 [batch, hq, nq] tensor")
+        lse = lse_out.data_ptr()
+    _on_device(cache.k, cache.v, cache.k_scale, cache.v_scale, q, out, seq_lens, workspace, block_table, lse_out, d_status)
+    st = _lib.tq_cache8_attention(c, q.data_ptr(), _dtype_code(q), qb, qh, qr, batch, hq, nq, seq_lens.data_ptr(), table,
+                                  stride, causal, window, 1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
+                                  _dtype_code(out), ob, oh, orow, lse, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _status_word(d_status), _stream(stream))
+    if st:
+        _check(st)
 
 
 def tq_residual_mean(samples, centroids, boundaries, bits: int) -> float:

@@ -278,7 +278,7 @@ tq_status rows_call(const char* what, const tq_cache8* cache, tq_dtype dtype, co
   if (n_tokens == 0 || batch == 0) return TQ_OK;
   if (!cu_tokens || !start) return fail(TQ_ERR_INVALID_ARG, "%s: NULL cu_tokens or start", what);
   if (WRITE ? (!k || !v) : (!k && !v)) return fail(TQ_ERR_INVALID_ARG, "%s: NULL rows", what);
-  st = check_table8(cache, batch, block_table ? table_stride : table_stride, what);
+  st = check_table8(cache, batch, table_stride, what);
   if (st != TQ_OK) return st;
   if (!block_table && table_stride * batch > cache->n_blocks)
     return fail(TQ_ERR_INVALID_ARG, "%s: without a block table the cache needs batch * table_stride blocks", what);
@@ -288,7 +288,7 @@ tq_status rows_call(const char* what, const tq_cache8* cache, tq_dtype dtype, co
   } side[2] = {{k, k_ts, k_hs}, {v, v_ts, v_hs}};
   for (const auto& s : side) {
     if (!s.p) continue;
-    if (!aligned(s.p, 16) || s.ts % 8 != 0 || s.hs % 8 != 0 || s.ts < 0 || s.hs < 0)
+    if (!aligned(s.p, 16) || !stride_ok(n_tokens, s.ts, 8) || !stride_ok(cache->heads, s.hs, 8))
       return fail(TQ_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned, strides multiples of 8 elements, not negative",
                   what);
     if (!WRITE && rows_overlap(n_tokens, s.ts, cache->heads, s.hs, cache->d))
@@ -303,6 +303,17 @@ tq_status rows_call(const char* what, const tq_cache8* cache, tq_dtype dtype, co
 }
 
 }  // namespace
+
+EncodeTiledFn encode_tiled_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool got = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                     q == cudaDriverEntryPointSuccess;
+    return got ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+  }();
+  return fn;
+}
 
 tq_status check_cache8(const tq_cache8* c, const char* what) {
   if (!c) return fail(TQ_ERR_INVALID_ARG, "%s: cache is NULL", what);

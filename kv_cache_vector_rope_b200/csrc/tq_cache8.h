@@ -1,6 +1,7 @@
 // Internal interface of the 8-bit block-scaled cache (tq_cache8*.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -20,6 +21,9 @@ tq_status check_cache8(const tq_cache8* c, const char* what);
 // Validates a block table: stride, and that every token position fits int32.
 tq_status check_table8(const tq_cache8* c, int32_t batch, int64_t table_stride, const char* what);
 
+// A stride's check passes where its dimension has one index: it is never used.
+inline bool stride_ok(int64_t n, int64_t stride, int64_t unit) { return n <= 1 || (stride >= 0 && stride % unit == 0); }
+
 // Whether rows of d elements at i * si + j * sj (i < ni, j < nj) can overlap: the
 // smaller stride's rows must fit within the larger stride.
 inline bool rows_overlap(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t d) {
@@ -30,6 +34,12 @@ inline bool rows_overlap(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t
   }
   return (ni > 1 && si < d) || (nj > 1 && sj < d);
 }
+
+// The driver's tensor-map encoder, looked up once; NULL where the driver lacks it.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled_fn();
 
 namespace c8 {
 

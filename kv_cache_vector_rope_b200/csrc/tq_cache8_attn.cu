@@ -16,7 +16,11 @@
 // at most two of them.
 //
 // Each warp takes groups of 16 keys of its CTA's range and keeps its own
-// running (m, l, sum). The products run on 16x8x16 half-precision matrix
+// running (m, l, sum). A group lies in one page; its keys and values come by two
+// TMA copies (128-byte swizzle, the cache seen as rows of 128 bytes) into the
+// warp's own ring in shared memory, several groups ahead, so the loads never
+// wait for the arithmetic and no warp waits for another until the range ends.
+// The products run on 16x8x16 half-precision matrix
 // instructions with the keys (then the value coordinates) as the 16 rows and
 // eight query rows as the columns, which suits the few rows of a step: every
 // 8-bit code is exactly a half, and a query row is scaled by a power of two
@@ -27,15 +31,17 @@
 
 #include "tq_cache8.h"
 #include "tq_device.cuh"
+#include "tq_sm100.cuh"
 
 namespace tq {
 namespace {
 
 using namespace c8;
+using namespace sm100;
 
 constexpr int kAtThreads = 256;
 constexpr int kAtWarps = kAtThreads / 32;
-constexpr int kAtGrid = 148 * 2;                     // two CTAs per SM
+constexpr int kAtGrid = 148 * 2;                     // at most two CTAs per SM
 constexpr int kUnit = 64;                            // keys per unit of the split
 constexpr int kMinUnits = 2;                         // a CTA takes at least this many units
 constexpr float kLog2e = 1.4426950408889634f;
@@ -68,6 +74,7 @@ struct AttnArgs {
   float* lse;                                        // [batch][hq][nq] or NULL
   float* rec;                                        // [grid][2][rows of a tile][2 + d]
   int* cum_out;                                      // [batch + 1], for the combine kernel
+  uint64_t wait_ns;
   int32_t* d_status;
 };
 
@@ -122,19 +129,45 @@ __device__ __forceinline__ uint32_t two_halves(uint32_t w) {
   return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
 }
 
+// Per head dim: 16-byte chunks a lane reads of each of its two keys, 4-byte
+// words it reads of each of its four values, ring stages per warp and CTAs per
+// SM (three stages of 4 KB for each of 16 warps are 192 KB at d = 128).
 template <int D>
-struct Chunk;                                        // bytes a lane loads of one key / value row
+struct Plan;
 template <>
-struct Chunk<64> {
-  static constexpr int kK = 1, kVWords = 2;
+struct Plan<64> {
+  static constexpr int kK = 1, kVWords = 2, kStages = 6, kCtas = 2;
 };
 template <>
-struct Chunk<128> {
-  static constexpr int kK = 2, kVWords = 4;
+struct Plan<128> {
+  static constexpr int kK = 2, kVWords = 4, kStages = 3, kCtas = 2;
 };
 template <>
-struct Chunk<256> {
-  static constexpr int kK = 4, kVWords = 8;
+struct Plan<256> {
+  static constexpr int kK = 4, kVWords = 8, kStages = 3, kCtas = 1;
+};
+
+// Dynamic shared memory: the warps' rings first (1024-byte aligned).
+template <int D, int NT, int QL>
+struct Smem {
+  static constexpr int kHalfStage = 16 * D;          // 16 keys (or values)
+  static constexpr int kStage = 2 * kHalfStage;
+  static constexpr int kRing = kStage * Plan<D>::kStages;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kKS = D / 16;
+  // uint2 [NT][QL][kKS][32], the query operands, while keys are walked; float4
+  // [warps][2][32], a piece of the value sums, while the warps are merged.
+  static constexpr int kOffQ = kAtWarps * kRing;
+  static constexpr int kOffAcc = kOffQ;
+  static constexpr int kQBytes = NT * QL * kKS * 32 * 8, kAccBytes = kAtWarps * 2 * 32 * 16;
+  static constexpr int kOffM = kOffQ + (kQBytes > kAccBytes ? kQBytes : kAccBytes);
+  static constexpr int kOffL = kOffM + 4 * kAtWarps * kRows;
+  static constexpr int kOffTop = kOffL + 4 * kAtWarps * kRows;   // float [2][kRows]: merged maximum and sum
+  static constexpr int kOffRow = kOffTop + 8 * kRows;            // per row: score factor, first key, end
+  static constexpr int kOffBar = kOffRow + 12 * kRows;
+  static constexpr int kOffPart = kOffBar + 8 * kAtWarps * Plan<D>::kStages;
+  static constexpr int kOffCum = kOffPart + 4 * kAtWarps;
+  static constexpr int kBytes = kOffCum + 4 * (kC8Slice + 1) + 1024;   // and room to align the base
 };
 
 // One (sequence, KV head, row tile, key range) of a CTA's range.
@@ -167,24 +200,66 @@ __device__ __forceinline__ int64_t page_of(const AttnArgs& a, int b, int blk) {
   return a.table ? static_cast<int64_t>(a.table[b * a.table_stride + blk]) : (a.first_seq + b) * a.table_stride + blk;
 }
 
-__device__ __forceinline__ float load_q(const void* p, bool f32, int64_t i) {
-  return f32 ? reinterpret_cast<const float*>(p)[i] : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+// Sixteen consecutive values of a query row.
+template <bool F32>
+__device__ __forceinline__ void load_q16(const void* p, int64_t i, float* x) {
+  if (F32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 y = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i)[k];
+      x[4 * k] = y.x;
+      x[4 * k + 1] = y.y;
+      x[4 * k + 2] = y.z;
+      x[4 * k + 3] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 y = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i)[k];
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        x[8 * k + 2 * h] = __uint_as_float(w[h] << 16);
+        x[8 * k + 2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
+      }
+    }
+  }
 }
+
+// Where byte `at` of a half stage lies: 16-byte chunk c of 128-byte row r sits at chunk c ^ (r % 8).
+__device__ __forceinline__ int swizzled(int at) { return at ^ ((at >> 3) & 0x70); }
 
 // NT: eight-row query tiles a CTA handles together. QF / OF: fp32 queries /
 // outputs, two half limbs each.
 template <int D, bool INT8, int NT, bool QF, bool OF>
-__global__ void __launch_bounds__(kAtThreads, 2) cache8_attn_kernel(AttnArgs a) {
-  constexpr int KC = Chunk<D>::kK, KS = KC * 4;      // 16-byte chunks, k-steps of the score product
-  constexpr int VW = Chunk<D>::kVWords, MT = VW * 2; // words per value row of a lane, 16-row tiles of the value product
+__global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
+    cache8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a) {
+  constexpr int KC = Plan<D>::kK, KS = KC * 4;       // 16-byte chunks, k-steps of the score product
+  constexpr int VW = Plan<D>::kVWords, MT = VW * 2;  // words per value row of a lane, 16-row tiles of the value product
+  constexpr int ST = Plan<D>::kStages;
   constexpr int QL = QF ? 2 : 1;
   constexpr int kRows = 8 * NT;
-  __shared__ int cum[kC8Slice + 1];
-  __shared__ int part[kAtWarps];
-  __shared__ float sm_m[kAtWarps][kRows], sm_l[kAtWarps][kRows];
-  __shared__ float4 sm_acc[kAtWarps][4][32];
+  constexpr bool kQRegs = NT * QL * KS <= 8;         // few enough to hold in registers
+  using L = Smem<D, NT, QL>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  uint2* sm_q = reinterpret_cast<uint2*>(smem + L::kOffQ);
+  float4* sm_acc = reinterpret_cast<float4*>(smem + L::kOffAcc);
+  float* sm_m = reinterpret_cast<float*>(smem + L::kOffM);
+  float* sm_l = reinterpret_cast<float*>(smem + L::kOffL);
+  float* sm_top = reinterpret_cast<float*>(smem + L::kOffTop);
+  float* sm_cq = reinterpret_cast<float*>(smem + L::kOffRow);
+  int* sm_lo = reinterpret_cast<int*>(sm_cq + kRows);
+  int* sm_hi = sm_lo + kRows;
+  int* cum = reinterpret_cast<int*>(smem + L::kOffCum);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  scan_counts<kAtThreads>(cum, part, a.batch, [&](int b) {
+  unsigned char* ring = smem + w * L::kRing;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar) + w * ST;
+  if (lane == 0) {
+    for (int s = 0; s < ST; ++s) mbar_init(bar + s, 1);
+    mbar_fence_init();
+  }
+  scan_counts<kAtThreads>(cum, reinterpret_cast<int*>(smem + L::kOffPart), a.batch, [&](int b) {
     return seq_tiles(a, seq_len(a, b, blockIdx.x == 0)) * a.heads * a.row_tiles;
   });
   if (blockIdx.x == 0)
@@ -192,62 +267,104 @@ __global__ void __launch_bounds__(kAtThreads, 2) cache8_attn_kernel(AttnArgs a) 
   const int total = cum[a.batch];
   const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinUnits);
   const int u0 = min(static_cast<int>(blockIdx.x) * per, total), u1 = min(u0 + per, total);
+  uint32_t used = 0;                                 // groups this warp's ring has carried
+  bool dead = false;                                 // a wait gave up
   for (int u = u0; u < u1;) {
     int next;
     const Seg sg = seg_at(a, cum, u, u1, &next);
-    // Queries: lane (g, t) holds row g's coordinates of its chunks.
-    uint32_t qh[NT][KS][QL][2];
-    float cq[NT][2];
-    int lo[NT][2], hi[NT][2];
-    int lo_max = 0, hi_min = 0x7fffffff;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = sg.rt * kRows + nt * 8 + g;
+    const int k0 = sg.t0 + 16 * w;                   // this warp's groups: k0, k0 + 128, ...
+    const int groups = sg.t1 > k0 ? (sg.t1 - k0 + 16 * kAtWarps - 1) / (16 * kAtWarps) : 0;
+    // Pages and scales of 32 groups at a time, one group per lane, the next 32 loaded ahead.
+    const auto load_page = [&](int i) {
+      return i < groups ? static_cast<int>(page_of(a, sg.b, (k0 + i * 16 * kAtWarps) / a.block)) : 0;
+    };
+    const auto ok = [&](int page) { return page >= 0 && page < a.n_blocks; };
+    const auto load_scale = [&](const float* p, int page) {
+      return ok(page) ? p[static_cast<int64_t>(page) * a.heads + sg.kv] : 0.f;
+    };
+    int pg = load_page(lane), pg_next = load_page(32 + lane);
+    const auto issue = [&](int i, int rel) {         // group i = 32 * (batch of pg) + rel
+      const int page = __shfl_sync(0xffffffffu, rel < 32 ? pg : pg_next, rel & 31);
+      if (lane == 0) {
+        const int key = k0 + i * 16 * kAtWarps;
+        // A bad page's group is masked; page 0 is copied in its place.
+        const int64_t ph = static_cast<int64_t>(ok(page) ? page : 0) * a.heads + sg.kv;
+        const int row = static_cast<int>((ph * a.block + key % a.block) * D / 128);
+        const int st = (used + i) % ST;
+        mbar_expect_tx(bar + st, L::kStage);
+        tma_load_2d(ring + st * L::kStage, &kmap, bar + st, 0, row);
+        tma_load_2d(ring + st * L::kStage + L::kHalfStage, &vmap, bar + st, 0, row);
+      }
+    };
+    int issued = 0;
+    if (!dead)
+      for (; issued < ST && issued < groups; ++issued) issue(issued, issued);
+    float sc_k = load_scale(a.ks, pg), sc_v = load_scale(a.vs, pg);
+    float nx_k = 0.f, nx_v = 0.f;
+    __syncthreads();                                 // the last segment's readers of sm_q and sm_row are done
+    // Queries: warp nt prepares the operands of rows 8 nt .. 8 nt + 7; lane (g, t) holds row g's coordinates of its chunks.
+    if (w < NT) {
+      const int r = sg.rt * kRows + w * 8 + g;
       const bool live = r < a.rows;
       const int i = live ? r / a.group : 0, hq = sg.kv * a.group + (live ? r % a.group : 0);
       const int64_t base = (a.first_seq + sg.b) * a.q_bs + hq * a.q_hs + i * a.q_rs;
+      float x[KC][16];
       float amax = 0.f;
-      for (int c = 0; c < KC; ++c)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          amax = fmaxf(amax, live ? fabsf(load_q(a.q, QF, base + 16 * (t + 4 * c) + e)) : 0.f);
+      for (int c = 0; c < KC; ++c) {
+        if (live) load_q16<QF>(a.q, base + 16 * (t + 4 * c), x[c]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (!live) x[c][e] = 0.f;
+          amax = fmaxf(amax, fabsf(x[c][e]));
+        }
+      }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // Times a power of two: the largest coordinate lands in [2^14, 2^15).
       const int E = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
       const float up = __uint_as_float(static_cast<uint32_t>(14 - min(E, 127) + 127) << 23);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        float x[4];
+      for (int c = 0; c < KC; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[e] = live ? load_q(a.q, QF, base + 16 * (t + 4 * (s / 4)) + 4 * (s % 4) + e) * up : 0.f;
-        qh[nt][s][0][0] = pack_half(x[0], x[1]);
-        qh[nt][s][0][1] = pack_half(x[2], x[3]);
-        if (QF) {
+        for (int s = 0; s < 4; ++s) {
+          float* y = x[c] + 4 * s;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] -= __half2float(__float2half_rn(x[e]));
-          qh[nt][s][QL - 1][0] = pack_half(x[0], x[1]);
-          qh[nt][s][QL - 1][1] = pack_half(x[2], x[3]);
+          for (int e = 0; e < 4; ++e) y[e] *= up;
+          sm_q[((w * QL + 0) * KS + 4 * c + s) * 32 + lane] = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+          if (QF) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] -= __half2float(__float2half_rn(y[e]));
+            sm_q[((w * QL + QL - 1) * KS + 4 * c + s) * 32 + lane] = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+          }
         }
+      if (t == 0) {
+        const int end = !live ? 0 : a.causal ? max(0, sg.n - a.nq + i + 1) : sg.n;
+        sm_cq[w * 8 + g] = a.scale2 / up;
+        sm_hi[w * 8 + g] = end;
+        sm_lo[w * 8 + g] = a.window > 0 ? max(0, end - a.window) : 0;
       }
-      const float mine = a.scale2 / up;
-      const int my_hi = !live ? 0 : a.causal ? max(0, sg.n - a.nq + i + 1) : sg.n;
-      const int my_lo = a.window > 0 ? max(0, my_hi - a.window) : 0;
-      int x = live ? my_hi : 0x7fffffff, y = live ? my_lo : 0;
+    }
+    __syncthreads();
+    float cq[NT][2];
+    int lo[NT][2], hi[NT][2];
+    int lo_max = 0, hi_min = 0x7fffffff;             // keys in [lo_max, hi_min) are seen by every row
+    for (int r = 0; r < kRows && sg.rt * kRows + r < a.rows; ++r) {
+      lo_max = max(lo_max, sm_lo[r]);
+      hi_min = min(hi_min, sm_hi[r]);
+    }
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        x = min(x, __shfl_xor_sync(0xffffffffu, x, o));
-        y = max(y, __shfl_xor_sync(0xffffffffu, y, o));
-      }
-      hi_min = min(hi_min, x);
-      lo_max = max(lo_max, y);
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {                  // the score columns of this lane are rows 2t and 2t + 1
-        cq[nt][j] = __shfl_sync(0xffffffffu, mine, (2 * t + j) * 4);
-        hi[nt][j] = __shfl_sync(0xffffffffu, my_hi, (2 * t + j) * 4);
-        lo[nt][j] = __shfl_sync(0xffffffffu, my_lo, (2 * t + j) * 4);
+        cq[nt][j] = sm_cq[nt * 8 + 2 * t + j];
+        lo[nt][j] = sm_lo[nt * 8 + 2 * t + j];
+        hi[nt][j] = sm_hi[nt * 8 + 2 * t + j];
       }
+    uint2 qr[kQRegs ? NT * QL * KS : 1];
+    if (kQRegs) {
+#pragma unroll
+      for (int x = 0; x < NT * QL * KS; ++x) qr[x] = sm_q[x * 32 + lane];
     }
     float acc[NT][MT][4];
     float m[NT][2], l[NT][2];
@@ -259,60 +376,97 @@ __global__ void __launch_bounds__(kAtThreads, 2) cache8_attn_kernel(AttnArgs a) 
 #pragma unroll
       for (int x = 0; x < MT; ++x) acc[nt][x][0] = acc[nt][x][1] = acc[nt][x][2] = acc[nt][x][3] = 0.f;
     }
-    for (int k0 = sg.t0 + 16 * w; k0 < sg.t1; k0 += 16 * kAtWarps) {
-      const int64_t page = page_of(a, sg.b, k0 / a.block);
-      const bool ok = page >= 0 && page < a.n_blocks;
-      if (!ok) {
-        if (lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_BLOCK);
-        continue;
+    for (int i = 0; i < groups; ++i) {
+      const int rel = i & 31;
+      if (rel == 0 && i > 0) {
+        pg = pg_next;
+        sc_k = nx_k;
+        sc_v = nx_v;
+        pg_next = load_page(i + 32 + lane);
       }
-      const int64_t ph = page * a.heads + sg.kv;
-      const float ks = a.ks[ph], vs = a.vs[ph];
-      const uint8_t* kp = a.k + (ph * a.block + k0 % a.block) * D;
-      const uint8_t* vp = a.v + (ph * a.block + k0 % a.block) * D;
-      const int left = sg.n - k0;                    // keys of the group that the sequence has
+      if (rel == 8) {
+        nx_k = load_scale(a.ks, pg_next);
+        nx_v = load_scale(a.vs, pg_next);
+      }
+      const int st = (used + i) % ST;
+      if (!dead && !mbar_wait(bar + st, ((used + i) / ST) & 1, a.wait_ns)) {
+        dead = true;
+        if (a.d_status) atomicOr(a.d_status, TQ_DEV_TIMEOUT);
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) break;
+      const int key0 = k0 + i * 16 * kAtWarps;
+      const float ks = __shfl_sync(0xffffffffu, sc_k, rel), vs = __shfl_sync(0xffffffffu, sc_v, rel);
+      const int page = __shfl_sync(0xffffffffu, pg, rel);
+      const unsigned char* kp = ring + st * L::kStage;
+      const unsigned char* vp = kp + L::kHalfStage;
       uint4 kw[2][KC];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int c = 0; c < KC; ++c)
-          kw[h][c] = *reinterpret_cast<const uint4*>(kp + (g + 8 * h) * D + 16 * (t + 4 * c));
+          kw[h][c] = *reinterpret_cast<const uint4*>(kp + swizzled((g + 8 * h) * D + 16 * (t + 4 * c)));
       uint32_t vw[4][VW];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int row = 2 * t + (j & 1) + 8 * (j >> 1);
-        const bool in = row < left;                  // what lies behind the sequence may be any byte
+        if (VW == 2) {
+          const uint2 x = *reinterpret_cast<const uint2*>(vp + swizzled(row * D + 8 * g));
+          vw[j][0] = x.x;
+          vw[j][1] = x.y;
+        } else {
 #pragma unroll
-        for (int c = 0; c < VW / 2; ++c) {
-          const uint2 x = in ? *reinterpret_cast<const uint2*>(vp + row * D + (VW >= 4 ? 16 * (g + 8 * (c / 2)) + 8 * (c % 2) : 8 * g))
-                             : make_uint2(0u, 0u);
-          vw[j][2 * c] = x.x;
-          vw[j][2 * c + 1] = x.y;
+          for (int c = 0; c < VW / 4; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vp + swizzled(row * D + 16 * (g + 8 * c)));
+            vw[j][4 * c] = x.x;
+            vw[j][4 * c + 1] = x.y;
+            vw[j][4 * c + 2] = x.z;
+            vw[j][4 * c + 3] = x.w;
+          }
         }
+      }
+      __syncwarp();                                  // every lane has its operands: the stage is free
+      if (issued < groups) {
+        issue(issued, issued - (i - rel));
+        ++issued;
+      }
+      if (!ok(page)) {
+        if (lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_BLOCK);
+        continue;
+      }
+      if (key0 + 16 > sg.n) {                        // what lies behind the sequence may be any byte
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (key0 + 2 * t + (j & 1) + 8 * (j >> 1) >= sg.n)
+#pragma unroll
+            for (int x = 0; x < VW; ++x) vw[j][x] = 0u;
       }
       float s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
-      for (int st = 0; st < KS; ++st) {
-        const uint32_t w0 = (&kw[0][st / 4].x)[st % 4], w1 = (&kw[1][st / 4].x)[st % 4];
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t w0 = (&kw[0][k / 4].x)[k % 4], w1 = (&kw[1][k / 4].x)[k % 4];
         const uint32_t a0 = two_halves<INT8, false>(w0), a2 = two_halves<INT8, true>(w0);
         const uint32_t a1 = two_halves<INT8, false>(w1), a3 = two_halves<INT8, true>(w1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          const int at = nt * QL * KS + k;
+          const uint2 b = kQRegs ? qr[at] : sm_q[at * 32 + lane];
           if (QF) {
             // Each step's products are added in fp32: the matrix unit's own sums are cut, not rounded.
+            const uint2 b2 = kQRegs ? qr[at + (QL - 1) * KS] : sm_q[(at + (QL - 1) * KS) * 32 + lane];
             float x[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(x, a0, a1, a2, a3, qh[nt][st][QL - 1][0], qh[nt][st][QL - 1][1]);
-            mma_f16(x, a0, a1, a2, a3, qh[nt][st][0][0], qh[nt][st][0][1]);
+            mma_f16(x, a0, a1, a2, a3, b2.x, b2.y);
+            mma_f16(x, a0, a1, a2, a3, b.x, b.y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[nt][e] += x[e];
           } else {
-            mma_f16(s[nt], a0, a1, a2, a3, qh[nt][st][0][0], qh[nt][st][0][1]);
+            mma_f16(s[nt], a0, a1, a2, a3, b.x, b.y);
           }
         }
       }
-      const bool full = k0 >= lo_max && k0 + 16 <= hi_min;
+      const bool full = key0 >= lo_max && key0 + 16 <= hi_min;
       bool rise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -320,7 +474,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) cache8_attn_kernel(AttnArgs a) 
         for (int e = 0; e < 4; ++e) {
           s[nt][e] *= cq[nt][e & 1] * ks;
           if (!full) {
-            const int key = k0 + g + 8 * (e >> 1);
+            const int key = key0 + g + 8 * (e >> 1);
             if (key < lo[nt][e & 1] || key >= hi[nt][e & 1]) s[nt][e] = -INFINITY;
           }
           rise |= s[nt][e] > m[nt][e & 1] + kSlack;
@@ -398,6 +552,11 @@ __global__ void __launch_bounds__(kAtThreads, 2) cache8_attn_kernel(AttnArgs a) 
         }
       }
     }
+    // Copies that a given-up wait left behind land before the ring is used again or the CTA ends.
+    if (dead)
+      for (int i = issued > ST ? issued - ST : 0; i < issued; ++i)
+        mbar_wait(bar + (used + i) % ST, ((used + i) / ST) & 1);
+    used += groups;
     // Merge the warps: maxima and sums, then the value sums a piece at a time.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -407,66 +566,64 @@ __global__ void __launch_bounds__(kAtThreads, 2) cache8_attn_kernel(AttnArgs a) 
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (g == 0) {
-          sm_m[w][nt * 8 + 2 * t + j] = m[nt][j];
-          sm_l[w][nt * 8 + 2 * t + j] = x;
+          sm_m[w * kRows + nt * 8 + 2 * t + j] = m[nt][j];
+          sm_l[w * kRows + nt * 8 + 2 * t + j] = x;
         }
       }
+    __syncthreads();
+    if (tid < kRows) {
+      float M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kAtWarps; ++k) M = fmaxf(M, sm_m[k * kRows + tid]);
+#pragma unroll
+      for (int k = 0; k < kAtWarps; ++k)
+        if (sm_m[k * kRows + tid] != -INFINITY) sum += sm_l[k * kRows + tid] * fast_exp2(sm_m[k * kRows + tid] - M);
+      sm_top[tid] = M;
+      sm_top[kRows + tid] = sum;
+    }
     __syncthreads();
     float f[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float M = -INFINITY;
-        for (int k = 0; k < kAtWarps; ++k) M = fmaxf(M, sm_m[k][nt * 8 + 2 * t + j]);
-        f[nt][j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - M) * vrun;
-      }
+      for (int j = 0; j < 2; ++j)
+        f[nt][j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - sm_top[nt * 8 + 2 * t + j]) * vrun;
     float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.head && u != u0 ? 1 : 0)) * kRows * (D + 2);
-    constexpr int kPairs = NT * MT;
 #pragma unroll
-    for (int p0 = 0; p0 < kPairs; p0 += 4) {
+    for (int p0 = 0; p0 < NT * MT; p0 += 2) {
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
+      for (int p = 0; p < 2; ++p) {
         const int nt = (p0 + p) / MT, x = (p0 + p) % MT;
-        sm_acc[w][p][lane] = make_float4(acc[nt][x][0] * f[nt][0], acc[nt][x][1] * f[nt][1], acc[nt][x][2] * f[nt][0],
-                                         acc[nt][x][3] * f[nt][1]);
+        sm_acc[(w * 2 + p) * 32 + lane] = make_float4(acc[nt][x][0] * f[nt][0], acc[nt][x][1] * f[nt][1],
+                                                      acc[nt][x][2] * f[nt][0], acc[nt][x][3] * f[nt][1]);
       }
       __syncthreads();
       {
-        const int p = tid >> 6, ln = (tid & 63) >> 1, c = tid & 1;   // two values: coordinate + c, rows 2t' and 2t' + 1
-        float2 sum = make_float2(0.f, 0.f);
+        // One value per thread: coordinate + c / 2, row 2 t' + c % 2.
+        const int p = tid >> 7, ln = (tid & 127) >> 2, c = tid & 3;
+        float val = 0.f;
 #pragma unroll
-        for (int k = 0; k < kAtWarps; ++k) {
-          const float2 y = reinterpret_cast<const float2*>(&sm_acc[k][p][ln])[c];
-          sum.x += y.x;
-          sum.y += y.y;
-        }
+        for (int k = 0; k < kAtWarps; ++k) val += reinterpret_cast<const float*>(sm_acc + (k * 2 + p) * 32 + ln)[c];
         const int nt = (p0 + p) / MT, x = (p0 + p) % MT;
-        const int wd = x >> 1, gg = ln >> 2, tt = ln & 3;
-        const int dim = (VW >= 4 ? 16 * (gg + 8 * (wd / 4)) + 4 * (wd % 4) : 8 * gg + 4 * wd) + 2 * (x & 1) + c;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = nt * 8 + 2 * tt + j, r = sg.rt * kRows + row;
-          if (r >= a.rows) continue;
-          const float val = j ? sum.y : sum.x;
-          float M = -INFINITY, L = 0.f;
-          for (int k = 0; k < kAtWarps; ++k) M = fmaxf(M, sm_m[k][row]);
-          for (int k = 0; k < kAtWarps; ++k)
-            if (sm_m[k][row] != -INFINITY) L += sm_l[k][row] * fast_exp2(sm_m[k][row] - M);
+        const int wd = x >> 1, gg = ln >> 2;
+        const int dim = (VW >= 4 ? 16 * (gg + 8 * (wd / 4)) + 4 * (wd % 4) : 8 * gg + 4 * wd) + 2 * (x & 1) + (c >> 1);
+        const int row = nt * 8 + 2 * (ln & 3) + (c & 1), r = sg.rt * kRows + row;
+        if (r < a.rows) {
+          const float M = sm_top[row], sum = sm_top[kRows + row];
           if (sg.whole) {
             const int i = r / a.group, hq = sg.kv * a.group + r % a.group;
             const int64_t at = (a.first_seq + sg.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + dim;
-            const float o = L == 0.f ? 0.f : val / L;
+            const float o = sum == 0.f ? 0.f : val / sum;
             if (OF) static_cast<float*>(a.out)[at] = o;
             else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
             if (a.lse && dim == 0)
               a.lse[((a.first_seq + sg.b) * a.heads * a.group + hq) * a.nq + i] =
-                  L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
+                  sum == 0.f ? -INFINITY : (M - kLift + log2f(sum)) * kLn2;
           } else {
             rec[row * (D + 2) + 2 + dim] = val;
             if (dim == 0) {
               rec[row * (D + 2)] = M;
-              rec[row * (D + 2) + 1] = L;
+              rec[row * (D + 2) + 1] = sum;
             }
           }
         }
@@ -523,23 +680,54 @@ __global__ void __launch_bounds__(256) cache8_combine_kernel(AttnArgs a, int gri
   }
 }
 
+struct Maps {
+  CUtensorMap k, v;
+};
+
+// The code arrays as rows of 128 bytes, copied in boxes of one group of 16 keys.
+tq_status encode_maps(const tq_cache8* c, Maps* m, const char* what) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return fail(TQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled not found", what);
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(c->n_blocks) * c->heads * c->block * c->d / 128};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(16 * c->d / 128)};
+  const cuuint32_t estr[2] = {1, 1};
+  if (dims[1] > 0x7fffffffu) return fail(TQ_ERR_UNSUPPORTED, "%s: cache beyond 2^38 bytes of keys", what);
+  CUtensorMap* maps[2] = {&m->k, &m->v};
+  uint8_t* base[2] = {c->k, c->v};
+  for (int i = 0; i < 2; ++i) {
+    const CUresult r = fn(maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base[i], dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(TQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", what, static_cast<int>(r));
+  }
+  return TQ_OK;
+}
+
 template <int D, bool INT8, int NT, bool QF, bool OF>
-cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st) {
-  cache8_attn_kernel<D, INT8, NT, QF, OF><<<kAtGrid, kAtThreads, 0, st>>>(a);
-  count_launch();
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch_attn(const Maps& maps, const AttnArgs& a, cudaStream_t st) {
+  constexpr int smem = Smem<D, NT, QF ? 2 : 1>::kBytes;
+  static_assert(smem * Plan<D>::kCtas <= 233472 - 1024 * Plan<D>::kCtas, "shared memory plan exceeds an SM's");
+  auto kernel = cache8_attn_kernel<D, INT8, NT, QF, OF>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cache8_combine_kernel<D, NT, OF><<<dim3(a.heads * a.row_tiles, a.batch), 256, 0, st>>>(a, kAtGrid);
+  constexpr int grid = 148 * Plan<D>::kCtas;         // every CTA resident at once
+  static_assert(grid <= kAtGrid, "the workspace holds kAtGrid CTAs' records");
+  kernel<<<grid, kAtThreads, smem, st>>>(maps.k, maps.v, a);
+  count_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cache8_combine_kernel<D, NT, OF><<<dim3(a.heads * a.row_tiles, a.batch), 256, 0, st>>>(a, grid);
   count_launch();
   return cudaGetLastError();
 }
 
 template <int D, bool INT8, int NT>
-cudaError_t launch_types(bool qf, bool of, const AttnArgs& a, cudaStream_t st) {
-  if (qf && of) return launch_attn<D, INT8, NT, true, true>(a, st);
-  if (qf) return launch_attn<D, INT8, NT, true, false>(a, st);
-  if (of) return launch_attn<D, INT8, NT, false, true>(a, st);
-  return launch_attn<D, INT8, NT, false, false>(a, st);
+cudaError_t launch_types(bool qf, bool of, const Maps& m, const AttnArgs& a, cudaStream_t st) {
+  if (qf && of) return launch_attn<D, INT8, NT, true, true>(m, a, st);
+  if (qf) return launch_attn<D, INT8, NT, true, false>(m, a, st);
+  if (of) return launch_attn<D, INT8, NT, false, true>(m, a, st);
+  return launch_attn<D, INT8, NT, false, false>(m, a, st);
 }
 
 // Query rows a CTA takes together: 8, or 16 where a KV head has more and the
@@ -586,12 +774,11 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
   if (st != TQ_OK) return st;
   if (!block_table && table_stride * batch > cache->n_blocks)
     return fail(TQ_ERR_INVALID_ARG, "%s: without a block table the cache needs batch * table_stride blocks", what);
-  if (!aligned(q, 16) || !aligned(out, 16) || q_batch_stride % 8 || q_head_stride % 8 || q_row_stride % 8 ||
-      out_batch_stride % 8 || out_head_stride % 8 || out_row_stride % 8)
-    return fail(TQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned, strides multiples of 8 elements", what);
-  if (q_batch_stride < 0 || q_head_stride < 0 || q_row_stride < 0 || out_batch_stride < 0 || out_head_stride < 0 ||
-      out_row_stride < 0)
-    return fail(TQ_ERR_INVALID_ARG, "%s: negative stride", what);
+  if (!aligned(q, 16) || !aligned(out, 16) || !stride_ok(batch, q_batch_stride, 8) || !stride_ok(hq, q_head_stride, 8) ||
+      !stride_ok(nq, q_row_stride, 8) || !stride_ok(batch, out_batch_stride, 8) || !stride_ok(hq, out_head_stride, 8) ||
+      !stride_ok(nq, out_row_stride, 8))
+    return fail(TQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned, strides multiples of 8 elements, not negative",
+                what);
   if ((batch > 1 && out_batch_stride < d) || rows_overlap(hq, out_head_stride, nq, out_row_stride, d))
     return fail(TQ_ERR_INVALID_ARG, "%s: the strides of out make rows overlap", what);
   if (d != 64 && d != 128 && d != 256)
@@ -611,7 +798,10 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
   AttnArgs a{cache->heads, cache->block, 0, cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
              q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, row_tiles, nullptr, nullptr, table_stride, 0,
              causal ? 1 : 0, window, scale * kLog2e, out, out_batch_stride, out_head_stride, out_row_stride, lse_out,
-             reinterpret_cast<float*>(static_cast<char*>(workspace) + kCumBytes), static_cast<int*>(workspace), d_status};
+             reinterpret_cast<float*>(static_cast<char*>(workspace) + kCumBytes), static_cast<int*>(workspace), pipeline_wait_ns(), d_status};
+  Maps maps;
+  st = encode_maps(cache, &maps, what);
+  if (st != TQ_OK) return st;
   const bool i8 = cache->code == TQ_INT8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int64_t b0 = 0; b0 < batch; b0 += slice) {
@@ -620,7 +810,7 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
     a.lens = seq_lens + b0;
     a.table = block_table ? block_table + b0 * table_stride : nullptr;
     cudaError_t e;
-#define TQ_C8(D, NT) (i8 ? launch_types<D, true, NT>(qf, of, a, s) : launch_types<D, false, NT>(qf, of, a, s))
+#define TQ_C8(D, NT) (i8 ? launch_types<D, true, NT>(qf, of, maps, a, s) : launch_types<D, false, NT>(qf, of, maps, a, s))
     if (d == 64) e = tile == 16 ? TQ_C8(64, 2) : TQ_C8(64, 1);
     else if (d == 128) e = tile == 16 ? TQ_C8(128, 2) : TQ_C8(128, 1);
     else e = TQ_C8(256, 1);

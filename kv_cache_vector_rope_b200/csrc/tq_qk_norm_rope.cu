@@ -193,9 +193,8 @@ extern "C" tq_status tq_qk_norm_rope(int32_t d, int32_t rot_dim, int64_t n_token
   for (const Side& s : sides) {
     if (s.heads == 0) continue;
     if (!s.p) return fail(TQ_ERR_INVALID_ARG, "%s is NULL", s.name);
-    if (!aligned(s.p, vec) || s.ts % 4 != 0 || s.hs % 4 != 0)
-      return fail(TQ_ERR_INVALID_ARG, "%s must be aligned to four elements, base and strides", s.name);
-    if (s.ts < 0 || s.hs < 0) return fail(TQ_ERR_INVALID_ARG, "%s has a negative stride", s.name);
+    if (!aligned(s.p, vec) || !stride_ok(n_tokens, s.ts, 4) || !stride_ok(s.heads, s.hs, 4))
+      return fail(TQ_ERR_INVALID_ARG, "%s must be aligned to four elements, base and strides (not negative)", s.name);
   }
   for (int i = 2; i < 4; ++i)
     if (sides[i].heads > 0 && rows_overlap(n_tokens, sides[i].ts, sides[i].heads, sides[i].hs, d))

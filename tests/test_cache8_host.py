@@ -64,7 +64,7 @@ def test_attention_host_validation():
     assert _attend(batch=0) == tq.TQ_OK
     for bad in (dict(qd=2), dict(od=5), dict(batch=-1), dict(hq=0), dict(hq=12), dict(nq=0), dict(nq=1 << 26), dict(window=-1),
                 dict(window=5, causal=0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=0), dict(out=0),
-                dict(lens=0), dict(stride=0), dict(table=0, stride=51), dict(q=0x1008), dict(qhs=100), dict(qrs=-4096),
+                dict(lens=0), dict(stride=0), dict(table=0, stride=51), dict(q=0x1008), dict(qhs=100), dict(nq=2, qrs=-4096),
                 dict(obs=64), dict(ohs=64), dict(nq=2, ors=128), dict(ws=0x100010)):
         assert _attend(**bad) == INVALID, bad
     assert _attend(c=_cache(d=96)) == UNSUPPORTED
