@@ -28,6 +28,7 @@ struct RowsArgs {
   int64_t table_stride;
   int64_t first_seq;                                 // of this slice (table == NULL: pages follow the sequence)
   int32_t* d_status;
+  int row_magic;                                     // 2^20 / (pieces per row) + 1
 };
 
 constexpr int kRowThreads = 256;
@@ -61,46 +62,49 @@ __device__ __forceinline__ Span seq_span(const RowsArgs& a, int b, bool tell) {
   return {static_cast<int>(lo), static_cast<int>(hi - lo), st < 0 ? 0 : static_cast<int>(st)};
 }
 
-// One item of the walk: rows [r0, r1) of `page`, whose first is row x0 of x.
+// The sequences' spans, in shared memory: cum[b] is the first block-unit of
+// sequence b, a unit being one block that the call touches.
+struct Spans {
+  int cum[kC8Slice + 1], at[kC8Slice], start[kC8Slice], end[kC8Slice];
+  int part[32];
+};
+template <int T>
+__device__ __forceinline__ void scan_spans(const RowsArgs& a, Spans& s) {
+  scan_counts<T>(s.cum, s.part, a.batch, [&](int b) {
+    const Span x = seq_span(a, b, blockIdx.x == 0);
+    s.at[b] = x.at;
+    s.start[b] = x.start;
+    s.end[b] = x.start + x.n;
+    return x.n > 0 ? (x.start % a.block + x.n + a.block - 1) / a.block : 0;
+  });
+}
+
+// One item of the walk: rows [r0, r1) of head `head` of a page, K or V; row r0 is row x0 of x.
 struct Item {
   int kv, head, r0, r1;
-  int64_t page, x0;
-  bool ok;
+  int page;
+  int64_t x0;
 };
-__device__ __forceinline__ Item item_at(const RowsArgs& a, const int* cum, int64_t item) {
+__device__ __forceinline__ Item item_at(const RowsArgs& a, const Spans& s, int64_t item) {
   Item it;
-  it.head = static_cast<int>(item % a.heads);
-  const int64_t rest = item / a.heads;
-  it.kv = a.code[0] && a.code[1] && a.x[0] && a.x[1] ? static_cast<int>(rest & 1) : (a.x[0] ? 0 : 1);
-  const int u = static_cast<int>(a.x[0] && a.x[1] ? rest >> 1 : rest);
-  const int b = find_seq(cum, a.batch, u);
-  const Span s = seq_span(a, b, false);
-  const int j = s.start / a.block + (u - cum[b]);
-  const int p0 = j * a.block;
-  it.r0 = max(s.start - p0, 0);
-  it.r1 = min(s.start + s.n - p0, a.block);
-  it.x0 = static_cast<int64_t>(s.at) + p0 + it.r0 - s.start;
-  it.page = a.table ? static_cast<int64_t>(a.table[b * a.table_stride + j]) : (a.first_seq + b) * a.table_stride + j;
-  it.ok = it.page >= 0 && it.page < a.n_blocks;
-  if (!it.ok && threadIdx.x == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
+  const bool both = a.x[0] && a.x[1];
+  const unsigned per = static_cast<unsigned>(a.heads) * (both ? 2u : 1u);
+  const int u = static_cast<int>(item / per);
+  const unsigned rest = static_cast<unsigned>(item - static_cast<int64_t>(u) * per);
+  it.kv = both ? rest >= static_cast<unsigned>(a.heads) : (a.x[0] ? 0 : 1);
+  it.head = static_cast<int>(rest) - (both ? it.kv * a.heads : 0);
+  const int b = find_seq(s.cum, a.batch, u);
+  const int start = s.start[b];
+  const int j = start / a.block + (u - s.cum[b]), p0 = j * a.block;
+  it.r0 = max(start - p0, 0);
+  it.r1 = min(s.end[b] - p0, a.block);
+  it.x0 = static_cast<int64_t>(s.at[b]) + p0 + it.r0 - start;
+  const int64_t page = a.table ? static_cast<int64_t>(a.table[b * a.table_stride + j]) : (a.first_seq + b) * a.table_stride + j;
+  it.page = page >= 0 && page < a.n_blocks ? static_cast<int>(page) : -1;
   return it;
 }
 
-// Eight values of a row as floats.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    v[2 * k] = __uint_as_float(w[k] << 16);
-    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-  }
-}
+// Eight values of a row.
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -115,118 +119,216 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int T>
-__device__ __forceinline__ float cta_max(float v, float* red) {
-  v = dev::warp_max(v);
-  __syncthreads();                                   // the last item's readers of red are done
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float m = red[0];
+// Eight values as loaded, kept in registers between the scale and the codes.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int k = 1; k < T / 32; ++k) m = fmaxf(m, red[k]);
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+};
+
+// Largest of `m` over the G threads of a group.
+template <int G>
+__device__ __forceinline__ float group_max(float m, float* red) {
+  m = dev::warp_max(m);
+  if (G == 32) return m;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < G / 32; ++k) m = fmaxf(m, red[k]);
+  __syncthreads();
   return m;
 }
 
-template <typename T, bool INT8>
+// A group of G threads (the CTA, or a warp) takes an item. Each thread keeps up
+// to kKeep pieces of eight values in registers from the pass that finds the
+// block's largest magnitude to the pass that codes them (all of a 64 x 128
+// block for a CTA); what lies beyond is read again, from L2.
+constexpr int kKeep = 4;
+template <typename T, bool INT8, int G>
 __global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(RowsArgs a) {
-  __shared__ int cum[kC8Slice + 1];
-  __shared__ int part[kRowThreads / 32];
+  __shared__ Spans spans;
   __shared__ float red[kRowThreads / 32];
-  const int tid = threadIdx.x;
-  scan_counts<kRowThreads>(cum, part, a.batch, [&](int b) {
-    const Span s = seq_span(a, b, blockIdx.x == 0);
-    return s.n > 0 ? (s.start % a.block + s.n + a.block - 1) / a.block : 0;
-  });
-  const int64_t items = static_cast<int64_t>(cum[a.batch]) * 2 * a.heads;
+  const int gt = threadIdx.x % G;                    // thread of the group
+  scan_spans<kRowThreads>(a, spans);
+  const int64_t items = static_cast<int64_t>(spans.cum[a.batch]) * 2 * a.heads;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kRowThreads / G);
   const int per_row = a.d / 8;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const Item it = item_at(a, cum, item);
-    if (!it.ok) continue;
-    const T* x = static_cast<const T*>(a.x[it.kv]) + it.x0 * a.ts[it.kv] + it.head * a.hs[it.kv];
-    const int64_t ph = it.page * a.heads + it.head;
-    uint8_t* dst = a.code[it.kv] + ph * a.block * a.d;
+  int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
+  Item next = item < items ? item_at(a, spans, item) : Item();
+  for (; item < items; item += step) {
+    const Item it = next;
+    if (item + step < items) next = item_at(a, spans, item + step);      // its page is on the way meanwhile
+    if (it.page < 0) {
+      if (gt == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
+      continue;
+    }
+    const int kv = it.kv;
+    const int64_t ts = a.ts[kv];
+    const T* x = static_cast<const T*>(a.x[kv]) + it.x0 * ts + it.head * a.hs[kv];
+    const int64_t ph = static_cast<int64_t>(it.page) * a.heads + it.head;
+    uint8_t* dst = a.code[kv] + ph * a.block * a.d;
     const int chunks = (it.r1 - it.r0) * per_row;
+    // c / per_row for c < 4096, per_row <= 32: exact, the error is at most c / 2^20 < 1 / 32.
+    const auto where = [&](int c) {
+      const int row = (c * a.row_magic) >> 20;
+      return x + row * ts + (c - row * per_row) * 8;
+    };
+    const float old = it.r0 > 0 ? a.scale[kv][ph] : 0.f;
+    Raw8<T> raw[kKeep];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (gt + k * G < chunks) raw[k].load(where(gt + k * G));
     float m = 0.f;
     bool odd = false;
-    for (int c = tid; c < chunks; c += kRowThreads) {
+    const auto look = [&](const Raw8<T>& r) {
       float v[8];
-      load8(x + (c / per_row) * a.ts[it.kv] + (c % per_row) * 8, v);
+      r.get(v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float u = fabsf(v[k]);
+      for (int e = 0; e < 8; ++e) {
+        const float u = fabsf(v[e]);
         if (u <= kMost) m = fmaxf(m, u); else odd = true;
       }
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (gt + k * G < chunks) look(raw[k]);
+    for (int c = gt + kKeep * G; c < chunks; c += G) {
+      Raw8<T> r;
+      r.load(where(c));
+      look(r);
     }
     if (odd) report(a.d_status, TQ_DEV_NONFINITE);
-    m = cta_max<kRowThreads>(m, red);
+    m = group_max<G>(m, red);
     float scale = block_scale<INT8>(m);
     if (it.r0 > 0) {                                 // the block holds tokens: its scale may only grow
-      const float old = a.scale[it.kv][ph];
       if (old >= scale) {
         scale = old;
       } else {
         const float ratio = old * inv_pow2(scale);
-        for (int c = tid; c < it.r0 * per_row; c += kRowThreads) {
+        for (int c = gt; c < it.r0 * per_row; c += G) {
           uint2* p = reinterpret_cast<uint2*>(dst) + c;
-          uint2 w = *p;
-          uint32_t* ws = &w.x;
+          const uint2 w = *p;
+          const uint32_t ws[2] = {w.x, w.y};
+          uint32_t o[2] = {0u, 0u};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t o = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o |= encode<INT8>(decode<INT8>((ws[h] >> (8 * k)) & 0xffu) * ratio) << (8 * k);
-            ws[h] = o;
-          }
-          *p = w;
+          for (int e = 0; e < 8; ++e)
+            o[e >> 2] |= encode<INT8>(decode<INT8>((ws[e >> 2] >> (8 * (e & 3))) & 0xffu) * ratio) << (8 * (e & 3));
+          *p = make_uint2(o[0], o[1]);
         }
       }
     }
     const float inv = inv_pow2(scale);
-    for (int c = tid; c < chunks; c += kRowThreads) {
+    uint8_t* row0 = dst + static_cast<int64_t>(it.r0) * a.d;
+    const auto put = [&](const Raw8<T>& r, int c) {
       float v[8];
-      load8(x + (c / per_row) * a.ts[it.kv] + (c % per_row) * 8, v);
-      uint32_t o[2] = {0u, 0u};
+      r.get(v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k >> 2] |= encode<INT8>(v[k] * inv) << (8 * (k & 3));
-      *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(it.r0) * a.d + c * 8) = make_uint2(o[0], o[1]);
+      for (int e = 0; e < 8; ++e) v[e] *= inv;
+      *reinterpret_cast<uint2*>(row0 + c * 8) = make_uint2(encode4<INT8>(v), encode4<INT8>(v + 4));
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (gt + k * G < chunks) put(raw[k], gt + k * G);
+    for (int c = gt + kKeep * G; c < chunks; c += G) {
+      Raw8<T> r;
+      r.load(where(c));
+      put(r, c);
     }
-    __syncthreads();                                 // every thread has read the old scale
-    if (tid == 0) a.scale[it.kv][ph] = scale;
+    // Every thread has read the old scale: group_max lies between.
+    if (gt == 0) a.scale[kv][ph] = scale;
   }
 }
 
-template <typename T, bool INT8>
+// Reading back: a thread takes 16 codes at a time, four such pieces in flight.
+template <typename T, bool INT8, int G>
 __global__ void __launch_bounds__(kRowThreads) cache8_read_kernel(RowsArgs a) {
-  __shared__ int cum[kC8Slice + 1];
-  __shared__ int part[kRowThreads / 32];
-  const int tid = threadIdx.x;
-  scan_counts<kRowThreads>(cum, part, a.batch, [&](int b) {
-    const Span s = seq_span(a, b, blockIdx.x == 0);
-    return s.n > 0 ? (s.start % a.block + s.n + a.block - 1) / a.block : 0;
-  });
-  const int64_t items = static_cast<int64_t>(cum[a.batch]) * (a.x[0] && a.x[1] ? 2 : 1) * a.heads;
-  const int per_row = a.d / 8;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const Item it = item_at(a, cum, item);
-    T* x = static_cast<T*>(a.x[it.kv]) + it.x0 * a.ts[it.kv] + it.head * a.hs[it.kv];
-    const int64_t ph = it.page * a.heads + it.head;
-    const float scale = it.ok ? a.scale[it.kv][ph] : 0.f;
-    const uint8_t* src = a.code[it.kv] + (it.ok ? (ph * a.block + it.r0) * a.d : 0);
-    for (int c = tid; c < (it.r1 - it.r0) * per_row; c += kRowThreads) {
-      const uint2 w = it.ok ? *reinterpret_cast<const uint2*>(src + c * 8) : make_uint2(0u, 0u);
-      const uint32_t ws[2] = {w.x, w.y};
-      float v[8];
+  __shared__ Spans spans;
+  const int gt = threadIdx.x % G;
+  scan_spans<kRowThreads>(a, spans);
+  const int64_t items = static_cast<int64_t>(spans.cum[a.batch]) * (a.x[0] && a.x[1] ? 2 : 1) * a.heads;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kRowThreads / G);
+  const int per_row = a.d / 16;
+  int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
+  Item next = item < items ? item_at(a, spans, item) : Item();
+  for (; item < items; item += step) {
+    const Item it = next;
+    if (item + step < items) next = item_at(a, spans, item + step);
+    const bool ok = it.page >= 0;
+    if (!ok && gt == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
+    const int kv = it.kv;
+    const int64_t ts = a.ts[kv];
+    T* x = static_cast<T*>(a.x[kv]) + it.x0 * ts + it.head * a.hs[kv];
+    const int64_t ph = static_cast<int64_t>(ok ? it.page : 0) * a.heads + it.head;
+    const float scale = ok ? a.scale[kv][ph] : 0.f;
+    const uint4* src = reinterpret_cast<const uint4*>(a.code[kv] + (ph * a.block + it.r0) * a.d);
+    const int chunks = (it.r1 - it.r0) * per_row;
+    for (int c0 = gt; c0 < chunks; c0 += kKeep * G) {
+      uint4 raw[kKeep];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = decode<INT8>((ws[k >> 2] >> (8 * (k & 3))) & 0xffu) * scale;
-      store8(x + (c / per_row) * a.ts[it.kv] + (c % per_row) * 8, v);
+      for (int k = 0; k < kKeep; ++k)
+        if (c0 + k * G < chunks) raw[k] = ok ? __ldg(src + c0 + k * G) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < kKeep; ++k) {
+        const int c = c0 + k * G;
+        if (c >= chunks) break;
+        const int row = (c * a.row_magic) >> 20;     // c / per_row, as above
+        T* p = x + row * ts + (c - row * per_row) * 16;
+        const uint32_t ws[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[8];
+          decode4<INT8>(ws[2 * h], v);
+          decode4<INT8>(ws[2 * h + 1], v + 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= scale;
+          store8(p + 8 * h, v);
+        }
+      }
     }
+  }
+}
+
+template <bool WRITE, typename T, bool INT8>
+void launch_group(bool warps, unsigned grid, const RowsArgs& a, cudaStream_t st) {
+  if (WRITE) {
+    if (warps) cache8_write_kernel<T, INT8, 32><<<grid, kRowThreads, 0, st>>>(a);
+    else cache8_write_kernel<T, INT8, kRowThreads><<<grid, kRowThreads, 0, st>>>(a);
+  } else {
+    if (warps) cache8_read_kernel<T, INT8, 32><<<grid, kRowThreads, 0, st>>>(a);
+    else cache8_read_kernel<T, INT8, kRowThreads><<<grid, kRowThreads, 0, st>>>(a);
   }
 }
 
 template <bool WRITE>
 cudaError_t launch_rows(const tq_cache8* c, tq_dtype dtype, RowsArgs a, int64_t batch, cudaStream_t st) {
   const int32_t *cu = a.cu, *start = a.start, *table = a.table;
+  const int per_row = a.d / (WRITE ? 8 : 16);
+  a.row_magic = (1 << 20) / per_row + 1;
+  // A warp per item where the call's sequences bring so few tokens that a warp
+  // holds an item's new rows in registers; else a CTA per item.
+  const bool warps = a.n / batch * (a.d / 8) <= 32 * kKeep;
   for (int64_t b0 = 0; b0 < batch; b0 += kC8Slice) {
     const int64_t nb = batch - b0 < kC8Slice ? batch - b0 : kC8Slice;
     a.batch = static_cast<int>(nb);
@@ -237,25 +339,15 @@ cudaError_t launch_rows(const tq_cache8* c, tq_dtype dtype, RowsArgs a, int64_t 
     // Blocks touched: at most one per token, and two partial ones per sequence beside the full ones.
     const int64_t full = a.n / c->block + 2 * nb;
     const int64_t items = (a.n < full ? a.n : full) * c->heads * (a.x[0] && a.x[1] ? 2 : 1);
+    const int64_t ctas = warps ? (items + kRowThreads / 32 - 1) / (kRowThreads / 32) : items;
     const int64_t most = 148 * 8;
-    const unsigned grid = static_cast<unsigned>(items < most ? items : most);
-    const bool i8 = c->code == TQ_INT8;
+    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
     if (dtype == TQ_F32) {
-      if (WRITE) {
-        if (i8) cache8_write_kernel<float, true><<<grid, kRowThreads, 0, st>>>(a);
-        else cache8_write_kernel<float, false><<<grid, kRowThreads, 0, st>>>(a);
-      } else {
-        if (i8) cache8_read_kernel<float, true><<<grid, kRowThreads, 0, st>>>(a);
-        else cache8_read_kernel<float, false><<<grid, kRowThreads, 0, st>>>(a);
-      }
+      if (c->code == TQ_INT8) launch_group<WRITE, float, true>(warps, grid, a, st);
+      else launch_group<WRITE, float, false>(warps, grid, a, st);
     } else {
-      if (WRITE) {
-        if (i8) cache8_write_kernel<__nv_bfloat16, true><<<grid, kRowThreads, 0, st>>>(a);
-        else cache8_write_kernel<__nv_bfloat16, false><<<grid, kRowThreads, 0, st>>>(a);
-      } else {
-        if (i8) cache8_read_kernel<__nv_bfloat16, true><<<grid, kRowThreads, 0, st>>>(a);
-        else cache8_read_kernel<__nv_bfloat16, false><<<grid, kRowThreads, 0, st>>>(a);
-      }
+      if (c->code == TQ_INT8) launch_group<WRITE, __nv_bfloat16, true>(warps, grid, a, st);
+      else launch_group<WRITE, __nv_bfloat16, false>(warps, grid, a, st);
     }
     count_launch();
     const cudaError_t e = cudaGetLastError();
@@ -296,7 +388,7 @@ tq_status rows_call(const char* what, const tq_cache8* cache, tq_dtype dtype, co
   }
   RowsArgs a{cache->d, cache->heads, cache->block, 0, cache->n_blocks, {cache->k, cache->v},
              {cache->k_scale, cache->v_scale}, {const_cast<void*>(k), const_cast<void*>(v)}, {k_ts, v_ts}, {k_hs, v_hs},
-             n_tokens, cu_tokens, start, block_table, table_stride, 0, d_status};
+             n_tokens, cu_tokens, start, block_table, table_stride, 0, d_status, 0};
   const cudaError_t e = launch_rows<WRITE>(cache, dtype, a, batch, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
   return TQ_OK;

@@ -81,6 +81,45 @@ __device__ __forceinline__ float decode(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
 }
 
+// Four codes at a time.
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode4(const float* y) {
+  if (INT8) return encode<true>(y[0]) | encode<true>(y[1]) << 8 | encode<true>(y[2]) << 16 | encode<true>(y[3]) << 24;
+  float z[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) z[k] = y[k] == y[k] ? y[k] : 0.f;
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(z[0], z[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(z[2], z[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+
+// The low / high two e4m3 codes of a word as two halves.
+template <bool HI>
+__device__ __forceinline__ uint32_t halves_e4m3(uint32_t w) {
+  uint32_t r;
+  if (HI)
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+  else
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+template <bool INT8>
+__device__ __forceinline__ void decode4(uint32_t w, float* v) {
+  if (INT8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = static_cast<float>(static_cast<int8_t>(w >> (8 * k)));
+  } else {
+    const uint32_t lo = halves_e4m3<false>(w), hi = halves_e4m3<true>(w);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
+  }
+}
+
 // Largest b in [0, n) with cum[b] <= u, for cum[0] = 0 <= u < cum[n].
 __device__ __forceinline__ int find_seq(const int* cum, int n, int u) {
   int lo = 0, hi = n - 1;

@@ -125,8 +125,7 @@ __device__ __forceinline__ uint32_t two_halves(uint32_t w) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(1152.f, 1152.f));
     return *reinterpret_cast<const uint32_t*>(&r);
   }
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+  return halves_e4m3<HI>(w);
 }
 
 // Per head dim: 16-byte chunks a lane reads of each of its two keys, 4-byte
@@ -369,6 +368,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     float acc[NT][MT][4];
     float m[NT][2], l[NT][2];
     float vrun = 1.17549435e-38f;                    // the sums are in units of this value scale
+    float vinv = 0.f;                                // 1 / vrun, once a group has set it
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       if (__any_sync(0xffffffffu, rise || vs > vrun)) {
         const float fv = vs > vrun ? vrun / vs : 1.f;
         vrun = fmaxf(vrun, vs);
+        vinv = 1.f / vrun;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float f[2];
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
           }
         }
       }
-      const float vr = vs / vrun;
+      const float vr = vs * vinv;
       uint32_t ph0[NT][2], ph1[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -636,48 +637,94 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 
 // Merges the records of every stream that more than one CTA worked on, and
 // writes the rows of streams with no key at all. One CTA per (sequence, KV
-// head and row tile); a warp per row.
+// head, row tile) and row: the records' maxima and sums are read side by side,
+// then D / 4 lanes walk the coordinates with the other threads dealing the
+// records out among themselves, so that a stream in hundreds of records (one
+// long sequence) costs a few rounds of loads, not one per record.
+constexpr int kCbThreads = 256;
 template <int D, int NT, bool OF>
-__global__ void __launch_bounds__(256) cache8_combine_kernel(AttnArgs a, int grid) {
+__global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, int grid) {
   constexpr int kRows = 8 * NT;
-  const int b = blockIdx.y, stream = blockIdx.x;
+  constexpr int kParts = kCbThreads / (D / 4);       // records in flight side by side
+  __shared__ float wt[kAtGrid];
+  __shared__ float red[2][kCbThreads / 32];
+  __shared__ float4 sums[kParts][D / 4];
+  const int b = blockIdx.z, stream = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+  const int kv = stream / a.row_tiles, rt = stream % a.row_tiles, r = rt * kRows + row;
+  if (r >= a.rows) return;
   const int c0 = a.cum_out[b], tiles = (a.cum_out[b + 1] - c0) / (a.heads * a.row_tiles);
   const int total = a.cum_out[a.batch];
   const int per = max((total + grid - 1) / grid, kMinUnits);
   const int u0 = c0 + stream * tiles, u1 = u0 + tiles;
   const int first = u0 / per, last = tiles > 0 ? (u1 - 1) / per : first;
   if (tiles > 0 && first == last) return;            // one CTA had it all and wrote the rows
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kv = stream / a.row_tiles, rt = stream % a.row_tiles;
-  for (int row = w; row < kRows; row += 8) {
-    const int r = rt * kRows + row;
-    if (r >= a.rows) break;
-    float M = -INFINITY, L = 0.f, sum[D / 32];
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x) sum[x] = 0.f;
-    for (int c = first; tiles > 0 && c <= last; ++c) {
-      const int slot = c == first && u0 != c * per ? 1 : 0;
-      const float* rec = a.rec + ((static_cast<int64_t>(c) * 2 + slot) * kRows + row) * (D + 2);
-      const float m = rec[0], l = rec[1];
-      if (m == -INFINITY) continue;
-      const float mn = fmaxf(M, m), f = M == -INFINITY ? 0.f : fast_exp2(M - mn), h = fast_exp2(m - mn);
-      L = L * f + l * h;
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) sum[x] = sum[x] * f + rec[2 + x * 32 + lane] * h;
-      M = mn;
-    }
-    const int i = r / a.group, hq = kv * a.group + r % a.group;
-    const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x) {
-      if (OF) static_cast<float*>(a.out)[at + x * 32 + lane] = sum[x] * inv;
-      else static_cast<__nv_bfloat16*>(a.out)[at + x * 32 + lane] = __float2bfloat16_rn(sum[x] * inv);
-    }
-    if (a.lse && lane == 0)
-      a.lse[((a.first_seq + b) * a.heads * a.group + hq) * a.nq + i] =
-          L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
+  const int n = tiles > 0 ? last - first + 1 : 0;
+  const auto record = [&](int k) {
+    const int c = first + k, slot = k == 0 && u0 != c * per ? 1 : 0;
+    return a.rec + ((static_cast<int64_t>(c) * 2 + slot) * kRows + row) * (D + 2);
+  };
+  float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;    // n <= kAtGrid <= 2 * kCbThreads
+  if (tid < n) {
+    const float* p = record(tid);
+    m0 = p[0];
+    l0 = p[1];
   }
+  if (tid + kCbThreads < n) {
+    const float* p = record(tid + kCbThreads);
+    m1 = p[0];
+    l1 = p[1];
+  }
+  static_assert(kAtGrid <= 2 * kCbThreads, "two records per thread");
+  const float mw = dev::warp_max(fmaxf(m0, m1));
+  if ((tid & 31) == 0) red[0][tid >> 5] = mw;
+  __syncthreads();
+  float M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kCbThreads / 32; ++k) M = fmaxf(M, red[0][k]);
+  const float w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M), w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
+  if (tid < n) wt[tid] = w0;
+  if (tid + kCbThreads < n) wt[tid + kCbThreads] = w1;
+  const float lw = dev::warp_sum((w0 == 0.f ? 0.f : l0 * w0) + (w1 == 0.f ? 0.f : l1 * w1));
+  if ((tid & 31) == 0) red[1][tid >> 5] = lw;
+  __syncthreads();
+  float L = 0.f;
+#pragma unroll
+  for (int k = 0; k < kCbThreads / 32; ++k) L += red[1][k];
+  const int x = tid % (D / 4), part = tid / (D / 4);
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = part; k < n; k += kParts) {
+    const float w = wt[k];
+    const float2* p = reinterpret_cast<const float2*>(record(k) + 2) + 2 * x;
+    const float2 y0 = p[0], y1 = p[1];
+    sum.x = fmaf(y0.x, w, sum.x);
+    sum.y = fmaf(y0.y, w, sum.y);
+    sum.z = fmaf(y1.x, w, sum.z);
+    sum.w = fmaf(y1.y, w, sum.w);
+  }
+  sums[part][x] = sum;
+  __syncthreads();
+  if (tid >= D / 4) return;
+#pragma unroll
+  for (int k = 1; k < kParts; ++k) {
+    const float4 y = sums[k][x];
+    sum.x += y.x;
+    sum.y += y.y;
+    sum.z += y.z;
+    sum.w += y.w;
+  }
+  const int i = r / a.group, hq = kv * a.group + r % a.group;
+  const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs + 4 * x;
+  const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float y = L == 0.f ? 0.f : o[k] / L;
+    if (OF) static_cast<float*>(a.out)[at + k] = y;
+    else static_cast<__nv_bfloat16*>(a.out)[at + k] = __float2bfloat16_rn(y);
+  }
+  if (a.lse && x == 0)
+    a.lse[((a.first_seq + b) * a.heads * a.group + hq) * a.nq + i] =
+        L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
 }
 
 struct Maps {
@@ -717,7 +764,8 @@ cudaError_t launch_attn(const Maps& maps, const AttnArgs& a, cudaStream_t st) {
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cache8_combine_kernel<D, NT, OF><<<dim3(a.heads * a.row_tiles, a.batch), 256, 0, st>>>(a, grid);
+  const int rows = a.rows < 8 * NT ? a.rows : 8 * NT;
+  cache8_combine_kernel<D, NT, OF><<<dim3(a.heads * a.row_tiles, rows, a.batch), kCbThreads, 0, st>>>(a, grid);
   count_launch();
   return cudaGetLastError();
 }

@@ -9,11 +9,13 @@
 //   (y_i, y_{i+rot/2}) -> (y_i cos a - y_{i+rot/2} sin a, y_i sin a + y_{i+rot/2} cos a),
 //   a = pos * base^(-2i/rot), i < rot/2; elements rot .. d-1 are not turned.
 //
-// A lane holds four values of a row and the four they are paired with, so no
-// value changes lanes; a row takes d / 8 lanes (rounded up to a power of two)
-// and its sum of squares a few shuffles. The angle is formed in fp64 as turns
-// (pos * base^(-2i/rot) / 2 pi; far positions lose whole turns only) and its
-// remainder goes through sincospif; one set per token serves all heads.
+// A lane holds V consecutive values of a row (16 bytes; 8 in bf16 where the
+// alignment is for four only) and the V they are paired with, so no value
+// changes lanes. A warp takes rows of one token, several side by side and two
+// sets of them in flight: the token's angles are formed once by the warp (fp64
+// turns pos * base^(-2i/rot) / 2 pi, whose remainder goes through sincospif:
+// far positions lose whole turns only) and then sit in registers, as the
+// weights do, while the warp walks the token's heads.
 #include "tq_device.cuh"
 #include "tq_cache8.h"
 
@@ -36,122 +38,194 @@ struct NormRopeArgs {
   const int32_t* pos;
   double base;
   int32_t* d_status;
-  int rows_per_cta;                                  // rows (heads) of a token one CTA takes
+  int parts, rows_per_part;                          // a token's rows are dealt to this many warps
 };
 
 constexpr int kNrThreads = 256;
-constexpr int kNrTile = 4;                           // tokens whose angles are formed together
 
-struct F4 {
-  float v[4];
+// V values as loaded.
+template <typename T, int V>
+struct Vec;
+template <>
+struct Vec<float, 4> {
+  float4 x;
+  __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float* v) const { v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w; }
+  static __device__ __forceinline__ void store(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
 };
-__device__ __forceinline__ F4 load4(const float* p) {
-  const float4 x = *reinterpret_cast<const float4*>(p);
-  return {{x.x, x.y, x.z, x.w}};
+__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ F4 load4(const __nv_bfloat16* p) {
-  const uint2 x = *reinterpret_cast<const uint2*>(p);
-  return {{__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-           __uint_as_float(x.y & 0xffff0000u)}};
-}
-__device__ __forceinline__ void store4(float* p, const F4& x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const F4& x) {
-  __nv_bfloat162 a = __floats2bfloat162_rn(x.v[0], x.v[1]), b = __floats2bfloat162_rn(x.v[2], x.v[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-}
+template <>
+struct Vec<__nv_bfloat16, 4> {
+  uint2 x;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16, 8> {
+  uint4 x;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
+    v[4] = __uint_as_float(x.z << 16), v[5] = __uint_as_float(x.z & 0xffff0000u);
+    v[6] = __uint_as_float(x.w << 16), v[7] = __uint_as_float(x.w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]));
+  }
+};
 
-// LPR: lanes per row, the power of two >= d / 8.
-template <typename T, int LPR>
-__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(NormRopeArgs a) {
-  __shared__ float2 turn[kNrTile][128];              // (cos, sin) of pair i of each token of the tile
-  const int tid = threadIdx.x;
-  const int half = a.rot / 2, pass = (a.d - a.rot) / 2;
-  const int rows = a.hq + a.hkv;
-  const int r0 = blockIdx.y * a.rows_per_cta, r1 = min(rows, r0 + a.rows_per_cta);
-  const bool rope = a.pos != nullptr && half > 0;
-  // Thread i forms pair i % 128 of token i / 128 (+2, ...) of a tile.
-  const int pair = tid & 127;
-  const double freq = rope && pair < half ? pow(a.base, -2.0 * pair / a.rot) * 0.15915494309189533577 : 0.0;
-  const int lane = tid & (LPR - 1), slot = tid / LPR;
-  constexpr int kSlots = kNrThreads / LPR;
-  const bool on = lane < a.d / 8;
-  const bool turned = 4 * lane < half;
-  const int e0 = turned ? 4 * lane : a.rot + 4 * lane - half;
-  const int e1 = e0 + (turned ? half : pass);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kNrTile; t0 < a.n;
-       t0 += static_cast<int64_t>(gridDim.x) * kNrTile) {
-    const int nt = static_cast<int>(min(static_cast<int64_t>(kNrTile), a.n - t0));
-    if (rope && pair < half) {
-      for (int t = tid >> 7; t < nt; t += kNrThreads / 128) {
-        const int p = a.pos[t0 + t];
-        if (p < 0 && pair == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_POSITION);
-        const double x = static_cast<double>(p) * freq;
-        float s, c;
-        sincospif(static_cast<float>(2.0 * (x - rint(x))), &s, &c);
-        turn[t][pair] = make_float2(c, s);
+// Rows [r0, r1) of one side (q or k) of a token. LPR: lanes per row, the power
+// of two >= d / 2V; a lane's values start at e0 and e1.
+template <typename T, int V, int LPR>
+__device__ __forceinline__ void side_rows(const T* src, int64_t hs, T* dst, int64_t ohs, int r0, int r1, const float* w,
+                                          float eps, float inv_d, int e0, int e1, bool on, bool turned, const float2* cs) {
+  constexpr int kRows = 32 / LPR;                    // rows of a warp side by side
+  constexpr int kSets = 2;
+  const int sub = (threadIdx.x & 31) / LPR;
+  float w0[V], w1[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    w0[k] = w && on ? __ldg(w + e0 + k) : 1.f;
+    w1[k] = w && on ? __ldg(w + e1 + k) : 1.f;
+  }
+  for (int r = r0 + sub; r - sub < r1; r += kRows * kSets) {
+    Vec<T, V> a[kSets], b[kSets];
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+      const int row = r + s * kRows;
+      if (on && row < r1) {
+        a[s].load(src + row * hs + e0);
+        b[s].load(src + row * hs + e1);
       }
     }
-    __syncthreads();
-    const int count = nt * (r1 - r0);
-    for (int at = slot; at - slot < count; at += kSlots) {      // whole warps stay together for the shuffles
-      const bool live = at < count && on;
-      const int t = at < count ? at / (r1 - r0) : 0;
-      const int r = at < count ? r0 + at % (r1 - r0) : r0;
-      const bool is_q = r < a.hq;
-      const int h = is_q ? r : r - a.hq;
-      const int64_t tok = t0 + t;
-      const T* src = static_cast<const T*>(is_q ? a.q : a.k) +
-                     (is_q ? tok * a.q_ts + h * a.q_hs : tok * a.k_ts + h * a.k_hs);
-      const float* w = is_q ? a.qw : a.kw;
-      F4 x0{{0.f, 0.f, 0.f, 0.f}}, x1 = x0;
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+      const int row = r + s * kRows;
+      const bool live = on && row < r1;
+      float x0[V], x1[V];
       if (live) {
-        x0 = load4(src + e0);
-        x1 = load4(src + e1);
+        a[s].get(x0);
+        b[s].get(x1);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) x0[k] = x1[k] = 0.f;
       }
-      if (w != nullptr || LPR < 32) {
+      if (w) {
         float ss = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ss = fmaf(x0.v[k], x0.v[k], fmaf(x1.v[k], x1.v[k], ss));
+        for (int k = 0; k < V; ++k) ss = fmaf(x0[k], x0[k], fmaf(x1[k], x1[k], ss));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w != nullptr && live) {
-          const float f = rsqrtf(ss / a.d + a.eps);
-          const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + e0));
-          const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + e1));
-          x0 = {{x0.v[0] * f * w0.x, x0.v[1] * f * w0.y, x0.v[2] * f * w0.z, x0.v[3] * f * w0.w}};
-          x1 = {{x1.v[0] * f * w1.x, x1.v[1] * f * w1.y, x1.v[2] * f * w1.z, x1.v[3] * f * w1.w}};
-        }
-      }
-      if (!live) continue;
-      if (rope && turned) {
+        const float f = rsqrtf(ss * inv_d + eps);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 cs = turn[t][e0 + k];
-          const float u = x0.v[k], v = x1.v[k];
-          x0.v[k] = u * cs.x - v * cs.y;
-          x1.v[k] = u * cs.y + v * cs.x;
+        for (int k = 0; k < V; ++k) {
+          x0[k] *= f * w0[k];
+          x1[k] *= f * w1[k];
         }
       }
-      T* dst = static_cast<T*>(is_q ? a.qo : a.ko) +
-               (is_q ? tok * a.qo_ts + h * a.qo_hs : tok * a.ko_ts + h * a.ko_hs);
-      store4(dst + e0, x0);
-      store4(dst + e1, x1);
+      if (turned) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float u = x0[k], v = x1[k];
+          x0[k] = u * cs[k].x - v * cs[k].y;
+          x1[k] = u * cs[k].y + v * cs[k].x;
+        }
+      }
+      if (live) {
+        Vec<T, V>::store(dst + row * ohs + e0, x0);
+        Vec<T, V>::store(dst + row * ohs + e1, x1);
+      }
     }
-    __syncthreads();                                 // the tile's angles are read
   }
 }
 
-template <typename T>
-cudaError_t launch_norm_rope(const NormRopeArgs& a, dim3 grid, cudaStream_t st) {
-  const int lanes = a.d / 8;
-  if (lanes <= 1) qk_norm_rope_kernel<T, 1><<<grid, kNrThreads, 0, st>>>(a);
-  else if (lanes <= 2) qk_norm_rope_kernel<T, 2><<<grid, kNrThreads, 0, st>>>(a);
-  else if (lanes <= 4) qk_norm_rope_kernel<T, 4><<<grid, kNrThreads, 0, st>>>(a);
-  else if (lanes <= 8) qk_norm_rope_kernel<T, 8><<<grid, kNrThreads, 0, st>>>(a);
-  else if (lanes <= 16) qk_norm_rope_kernel<T, 16><<<grid, kNrThreads, 0, st>>>(a);
-  else qk_norm_rope_kernel<T, 32><<<grid, kNrThreads, 0, st>>>(a);
+template <typename T, int V, int LPR>
+__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(NormRopeArgs a) {
+  __shared__ float2 turn[kNrThreads / 32][128];      // (cos, sin) of pair i of each warp's token
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, part_lane = lane & (LPR - 1);
+  const int half = a.rot / 2, pass = (a.d - a.rot) / 2;
+  const bool on = part_lane < a.d / (2 * V);
+  const bool rope = a.pos != nullptr && half > 0;
+  const bool first = V * part_lane < half;           // values that are turned come first
+  const int e0 = first ? V * part_lane : a.rot + V * part_lane - half;
+  const int e1 = e0 + (first ? half : pass);
+  const bool turned = rope && first;
+  double freq[4];                                    // turns per position of pairs lane, lane + 32, ...
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    freq[s] = rope && lane + 32 * s < half ? pow(a.base, -2.0 * (lane + 32 * s) / a.rot) * 0.15915494309189533577 : 0.0;
+  const float inv_d = 1.f / a.d;
+  const int64_t units = a.n * a.parts;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + w; u < units;
+       u += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
+    const int64_t tok = a.parts == 1 ? u : u / a.parts;
+    const int r0 = static_cast<int>(u - tok * a.parts) * a.rows_per_part, r1 = min(a.hq + a.hkv, r0 + a.rows_per_part);
+    float2 cs[V];
+    if (rope) {
+      const int p = a.pos[tok];
+      if (p < 0 && lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_POSITION);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (32 * s >= half) break;
+        const double x = static_cast<double>(p) * freq[s];
+        float sn, c;
+        sincospif(static_cast<float>(2.0 * (x - rint(x))), &sn, &c);
+        turn[w][lane + 32 * s] = make_float2(c, sn);
+      }
+      __syncwarp();
+      if (turned) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) cs[k] = turn[w][e0 + k];
+      }
+      __syncwarp();                                  // read before the next token's are written
+    }
+    if (r0 < a.hq)
+      side_rows<T, V, LPR>(static_cast<const T*>(a.q) + tok * a.q_ts, a.q_hs, static_cast<T*>(a.qo) + tok * a.qo_ts,
+                           a.qo_hs, r0, min(r1, a.hq), a.qw, a.eps, inv_d, e0, e1, on, turned, cs);
+    if (r1 > a.hq)
+      side_rows<T, V, LPR>(static_cast<const T*>(a.k) + tok * a.k_ts, a.k_hs, static_cast<T*>(a.ko) + tok * a.ko_ts,
+                           a.ko_hs, max(r0 - a.hq, 0), r1 - a.hq, a.kw, a.eps, inv_d, e0, e1, on, turned, cs);
+  }
+}
+
+template <typename T, int V>
+cudaError_t launch_norm_rope(NormRopeArgs a, cudaStream_t st) {
+  const int lanes = a.d / (2 * V), rows = a.hq + a.hkv;
+  int lpr = 1;
+  while (lpr < lanes) lpr *= 2;
+  // Warps: one per token, or several where the tokens alone would leave SMs idle
+  // (a part has at least as many rows as a warp holds side by side).
+  const int side = 32 / lpr, most = (rows + side - 1) / side;
+  const int64_t want = (148 * 8 + a.n - 1) / a.n;
+  a.parts = static_cast<int>(want < most ? want : most);
+  a.rows_per_part = ((rows + a.parts - 1) / a.parts + side - 1) / side * side;
+  a.parts = (rows + a.rows_per_part - 1) / a.rows_per_part;
+  const int64_t units = a.n * a.parts;
+  // Small calls take two warps per CTA, so that they reach every SM.
+  const int threads = units <= 148 * 8 ? 64 : kNrThreads;
+  const int64_t ctas = (units + threads / 32 - 1) / (threads / 32);
+  const unsigned grid = static_cast<unsigned>(ctas < 148 * 8 ? ctas : 148 * 8);
+  switch (lpr) {
+    case 1: qk_norm_rope_kernel<T, V, 1><<<grid, threads, 0, st>>>(a); break;
+    case 2: qk_norm_rope_kernel<T, V, 2><<<grid, threads, 0, st>>>(a); break;
+    case 4: qk_norm_rope_kernel<T, V, 4><<<grid, threads, 0, st>>>(a); break;
+    case 8: qk_norm_rope_kernel<T, V, 8><<<grid, threads, 0, st>>>(a); break;
+    case 16: qk_norm_rope_kernel<T, V, 16><<<grid, threads, 0, st>>>(a); break;
+    default: qk_norm_rope_kernel<T, V, 32><<<grid, threads, 0, st>>>(a); break;
+  }
   count_launch();
   return cudaGetLastError();
 }
@@ -203,19 +277,16 @@ extern "C" tq_status tq_qk_norm_rope(int32_t d, int32_t rot_dim, int64_t n_token
     return fail(TQ_ERR_INVALID_ARG, "weights must be 16-byte aligned");
   NormRopeArgs a{d, rot_dim, n_tokens, hq, hkv, q, k, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
                  q_out, k_out, q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride, q_weight,
-                 k_weight, eps, rope ? positions : nullptr, static_cast<double>(rope_base), d_status, 0};
-  const int rows = hq + hkv;
-  const int64_t tiles = (n_tokens + kNrTile - 1) / kNrTile;
-  const int64_t most = 148 * 8;
-  const unsigned gx = static_cast<unsigned>(tiles < most ? tiles : most);
-  // Few tokens: the heads of a token are spread over CTAs too.
-  int parts = 1;
-  while (parts < rows && parts < 64 && static_cast<int64_t>(gx) * parts < 148 && (rows + parts - 1) / parts > 4)
-    parts *= 2;
-  a.rows_per_cta = (rows + parts - 1) / parts;
-  dim3 grid(gx, static_cast<unsigned>((rows + a.rows_per_cta - 1) / a.rows_per_cta));
+                 k_weight, eps, rope ? positions : nullptr, static_cast<double>(rope_base), d_status, 0, 0};
+  // bf16 rows go eight values at a time where bases, strides and halves allow it.
+  bool eight = dtype == TQ_BF16 && d % 16 == 0 && rot_dim % 16 == 0;
+  for (const Side& s : sides)
+    if (s.heads > 0)
+      eight = eight && aligned(s.p, 16) && (n_tokens == 1 || s.ts % 8 == 0) && (s.heads == 1 || s.hs % 8 == 0);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == TQ_F32 ? launch_norm_rope<float>(a, grid, st) : launch_norm_rope<__nv_bfloat16>(a, grid, st);
+  const cudaError_t e = dtype == TQ_F32 ? launch_norm_rope<float, 4>(a, st)
+                        : eight         ? launch_norm_rope<__nv_bfloat16, 8>(a, st)
+                                        : launch_norm_rope<__nv_bfloat16, 4>(a, st);
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "tq_qk_norm_rope launch: %s", cudaGetErrorString(e));
   return TQ_OK;
 }
