@@ -1,11 +1,13 @@
 // tq_cache8_write / tq_cache8_read: an 8-bit paged KV cache with one
 // power-of-two scale for each block of tokens and head.
 //
-// The work item is one (block a sequence touches, head, K or V): its rows are
-// one contiguous piece of the cache, and its scale is theirs alone, so an item
-// needs nothing from another and no atomics. The items follow from the prefix
-// sums of the blocks each sequence touches, which every CTA forms for itself
-// from the lengths in device memory (a call needs no host copy of them).
+// The work item is one (block that a sequence touches, head), K and V of it:
+// its rows are one contiguous piece of each code array and their scales are
+// theirs alone, so an item needs nothing from another and no atomics. The
+// blocks follow from prefix sums over the sequences, which every CTA forms for
+// itself from the lengths in device memory (a call needs no host copy of them).
+#include <type_traits>
+
 #include "tq_cache8.h"
 #include "tq_device.cuh"
 
@@ -31,7 +33,9 @@ struct RowsArgs {
   int row_magic;                                     // 2^20 / (pieces per row) + 1
 };
 
-constexpr int kRowThreads = 256;
+// Threads of a CTA whose warps (G = 32) or all of whose threads take an item.
+__host__ __device__ constexpr int cta_threads(int G) { return G == 32 ? 64 : 256; }
+constexpr int kGroup = 256;                          // G where a CTA takes an item
 
 __device__ __forceinline__ void report(int32_t* d_status, int bit) {
   if (d_status) atomicOr(d_status, bit);
@@ -79,21 +83,15 @@ __device__ __forceinline__ void scan_spans(const RowsArgs& a, Spans& s) {
   });
 }
 
-// One item of the walk: rows [r0, r1) of head `head` of a page, K or V; row r0 is row x0 of x.
-struct Item {
-  int kv, head, r0, r1;
-  int page;
+// One unit of the walk: rows [r0, r1) of a page; row r0 is row x0 of x.
+struct Unit {
+  int r0, r1, page;                                  // page -1: outside the cache
   int64_t x0;
 };
-__device__ __forceinline__ Item item_at(const RowsArgs& a, const Spans& s, int64_t item) {
-  Item it;
-  const bool both = a.x[0] && a.x[1];
-  const unsigned per = static_cast<unsigned>(a.heads) * (both ? 2u : 1u);
-  const int u = static_cast<int>(item / per);
-  const unsigned rest = static_cast<unsigned>(item - static_cast<int64_t>(u) * per);
-  it.kv = both ? rest >= static_cast<unsigned>(a.heads) : (a.x[0] ? 0 : 1);
-  it.head = static_cast<int>(rest) - (both ? it.kv * a.heads : 0);
-  const int b = find_seq(s.cum, a.batch, u);
+// b: the unit's sequence, found by moving on from the last unit's.
+__device__ __forceinline__ Unit unit_at(const RowsArgs& a, const Spans& s, int u, int& b) {
+  while (u >= s.cum[b + 1]) ++b;
+  Unit it;
   const int start = s.start[b];
   const int j = start / a.block + (u - s.cum[b]), p0 = j * a.block;
   it.r0 = max(start - p0, 0);
@@ -104,12 +102,11 @@ __device__ __forceinline__ Item item_at(const RowsArgs& a, const Spans& s, int64
   return it;
 }
 
-// Eight values of a row.
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+// 16 bytes of a row.
+__device__ __forceinline__ void store16(float* p, const float* v) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v) {
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -120,6 +117,8 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 }
 
 // Eight values as loaded, kept in registers between the scale and the codes.
+// top: the largest magnitude, as the bits of a float: whole-number order, in
+// which infinities and NaN come after every finite value.
 template <typename T>
 struct Raw8;
 template <>
@@ -132,6 +131,14 @@ struct Raw8<float> {
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    float v[8];
+    get(v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
+    return m;
   }
 };
 template <>
@@ -146,164 +153,232 @@ struct Raw8<__nv_bfloat16> {
       v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     }
   }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+  }
 };
 
-// Largest of `m` over the G threads of a group.
+// The two largest values (K's, V's) over the G threads of a group.
 template <int G>
-__device__ __forceinline__ float group_max(float m, float* red) {
-  m = dev::warp_max(m);
-  if (G == 32) return m;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+__device__ __forceinline__ void group_max(uint32_t (&m)[2], uint2* red) {
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) m[kv] = __reduce_max_sync(0xffffffffu, m[kv]);
+  if (G == 32) return;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_uint2(m[0], m[1]);
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < G / 32; ++k) m = fmaxf(m, red[k]);
+  for (int k = 0; k < G / 32; ++k) {
+    m[0] = max(m[0], red[k].x);
+    m[1] = max(m[1], red[k].y);
+  }
   __syncthreads();
-  return m;
+}
+
+// Four codes of finite values that are within the code's range once divided by
+// the scale. int8: adding 1.5 * 2^23 rounds to a whole number (ties to even),
+// which is then the low byte of the sum.
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode4_finite(const float* x, float inv) {
+  if (INT8) {
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = __float_as_uint(fmaf(x[k], inv, 12582912.f));
+    return __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+  }
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
 }
 
 // A group of G threads (the CTA, or a warp) takes an item. Each thread keeps up
-// to kKeep pieces of eight values in registers from the pass that finds the
-// block's largest magnitude to the pass that codes them (all of a 64 x 128
-// block for a CTA); what lies beyond is read again, from L2.
+// to kKeep pieces of eight values of K and of V in registers from the pass that
+// finds the blocks' largest magnitudes to the pass that codes them (all of a
+// 64 x 128 block for a CTA); what lies beyond is read again, from L2. The
+// largest magnitude is found on the bits, two bf16 values at a time, and says
+// whether the block has a value that is not finite; only then does the pass that
+// looks at each value run.
 constexpr int kKeep = 4;
 template <typename T, bool INT8, int G>
-__global__ void __launch_bounds__(kRowThreads) cache8_write_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : sizeof(T) == 2 ? 3 : 2) cache8_write_kernel(RowsArgs a) {
   __shared__ Spans spans;
-  __shared__ float red[kRowThreads / 32];
+  __shared__ uint2 red[cta_threads(G) / 32];
   const int gt = threadIdx.x % G;                    // thread of the group
-  scan_spans<kRowThreads>(a, spans);
-  const int64_t items = static_cast<int64_t>(spans.cum[a.batch]) * 2 * a.heads;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kRowThreads / G);
+  scan_spans<cta_threads(G)>(a, spans);
+  const int units = spans.cum[a.batch], step = gridDim.x * (cta_threads(G) / G), head = blockIdx.y;
   const int per_row = a.d / 8;
-  int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
-  Item next = item < items ? item_at(a, spans, item) : Item();
-  for (; item < items; item += step) {
-    const Item it = next;
-    if (item + step < items) next = item_at(a, spans, item + step);      // its page is on the way meanwhile
+  int u = blockIdx.x * (cta_threads(G) / G) + threadIdx.x / G, b = 0;
+  Unit next;
+  if (u < units) next = unit_at(a, spans, u, b);
+  for (; u < units; u += step) {
+    const Unit it = next;
+    if (u + step < units) next = unit_at(a, spans, u + step, b);         // its page is on the way meanwhile
     if (it.page < 0) {
-      if (gt == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
+      if (gt == 0 && head == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
       continue;
     }
-    const int kv = it.kv;
-    const int64_t ts = a.ts[kv];
-    const T* x = static_cast<const T*>(a.x[kv]) + it.x0 * ts + it.head * a.hs[kv];
-    const int64_t ph = static_cast<int64_t>(it.page) * a.heads + it.head;
-    uint8_t* dst = a.code[kv] + ph * a.block * a.d;
+    const int64_t ph = static_cast<int64_t>(it.page) * a.heads + head;
     const int chunks = (it.r1 - it.r0) * per_row;
+    const T* x[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) x[kv] = static_cast<const T*>(a.x[kv]) + it.x0 * a.ts[kv] + head * a.hs[kv];
     // c / per_row for c < 4096, per_row <= 32: exact, the error is at most c / 2^20 < 1 / 32.
-    const auto where = [&](int c) {
+    const auto where = [&](int kv, int c) {
       const int row = (c * a.row_magic) >> 20;
-      return x + row * ts + (c - row * per_row) * 8;
+      return x[kv] + row * a.ts[kv] + (c - row * per_row) * 8;
     };
-    const float old = it.r0 > 0 ? a.scale[kv][ph] : 0.f;
-    Raw8<T> raw[kKeep];
+    Raw8<T> raw[2][kKeep];
 #pragma unroll
-    for (int k = 0; k < kKeep; ++k)
-      if (gt + k * G < chunks) raw[k].load(where(gt + k * G));
-    float m = 0.f;
-    bool odd = false;
-    const auto look = [&](const Raw8<T>& r) {
-      float v[8];
-      r.get(v);
+    for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = fabsf(v[e]);
-        if (u <= kMost) m = fmaxf(m, u); else odd = true;
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k)
-      if (gt + k * G < chunks) look(raw[k]);
-    for (int c = gt + kKeep * G; c < chunks; c += G) {
-      Raw8<T> r;
-      r.load(where(c));
-      look(r);
+      for (int k = 0; k < kKeep; ++k)
+        if (gt + k * G < chunks) raw[kv][k].load(where(kv, gt + k * G));
+    float old[2] = {0.f, 0.f};
+    if (it.r0 > 0) {
+      old[0] = a.scale[0][ph];
+      old[1] = a.scale[1][ph];
     }
-    if (odd) report(a.d_status, TQ_DEV_NONFINITE);
-    m = group_max<G>(m, red);
-    float scale = block_scale<INT8>(m);
-    if (it.r0 > 0) {                                 // the block holds tokens: its scale may only grow
-      if (old >= scale) {
-        scale = old;
-      } else {
-        const float ratio = old * inv_pow2(scale);
-        for (int c = gt; c < it.r0 * per_row; c += G) {
-          uint2* p = reinterpret_cast<uint2*>(dst) + c;
-          const uint2 w = *p;
-          const uint32_t ws[2] = {w.x, w.y};
-          uint32_t o[2] = {0u, 0u};
+    uint32_t m[2] = {0u, 0u};
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            o[e >> 2] |= encode<INT8>(decode<INT8>((ws[e >> 2] >> (8 * (e & 3))) & 0xffu) * ratio) << (8 * (e & 3));
-          *p = make_uint2(o[0], o[1]);
+    for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+      for (int k = 0; k < kKeep; ++k)
+        if (gt + k * G < chunks) m[kv] = max(m[kv], raw[kv][k].top());
+      for (int c = gt + kKeep * G; c < chunks; c += G) {
+        Raw8<T> r;
+        r.load(where(kv, c));
+        m[kv] = max(m[kv], r.top());
+      }
+    }
+    group_max<G>(m, red);
+    const uint32_t most = __float_as_uint(kMost);
+    const bool odd = max(m[0], m[1]) > most;         // a value that is not finite (or beyond 2^127): for all threads alike
+    if (odd) {
+      if (gt == 0) report(a.d_status, TQ_DEV_NONFINITE);
+      m[0] = m[1] = 0u;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll 1
+        for (int c = gt; c < chunks; c += G) {
+          Raw8<T> r;
+          r.load(where(kv, c));
+          float v[8];
+          r.get(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t y = __float_as_uint(v[e]) & 0x7fffffffu;
+            if (y <= most) m[kv] = max(m[kv], y);
+          }
+        }
+      group_max<G>(m, red);
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint8_t* dst = a.code[kv] + ph * a.block * a.d;
+      float scale = block_scale<INT8>(__uint_as_float(m[kv]));
+      if (it.r0 > 0) {                               // the block holds tokens: its scale may only grow
+        if (old[kv] >= scale) {
+          scale = old[kv];
+        } else {
+          const float ratio = old[kv] * inv_pow2(scale);
+#pragma unroll 1
+          for (int c = gt; c < it.r0 * per_row; c += G) {
+            uint2* p = reinterpret_cast<uint2*>(dst) + c;
+            const uint2 w = *p;
+            const uint32_t ws[2] = {w.x, w.y};
+            uint32_t o[2] = {0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              o[e >> 2] |= encode<INT8>(decode<INT8>((ws[e >> 2] >> (8 * (e & 3))) & 0xffu) * ratio) << (8 * (e & 3));
+            *p = make_uint2(o[0], o[1]);
+          }
         }
       }
-    }
-    const float inv = inv_pow2(scale);
-    uint8_t* row0 = dst + static_cast<int64_t>(it.r0) * a.d;
-    const auto put = [&](const Raw8<T>& r, int c) {
-      float v[8];
-      r.get(v);
+      const float inv = inv_pow2(scale);
+      uint2* row0 = reinterpret_cast<uint2*>(dst + static_cast<int64_t>(it.r0) * a.d);
+      const auto put = [&](const Raw8<T>& r, int c) {
+        float v[8];
+        r.get(v);
+        row0[c] = make_uint2(encode4_finite<INT8>(v, inv), encode4_finite<INT8>(v + 4, inv));
+      };
+      if (odd) {
+#pragma unroll 1
+        for (int c = gt; c < chunks; c += G) {
+          Raw8<T> r;
+          r.load(where(kv, c));
+          float v[8];
+          r.get(v);
+          uint32_t o[2] = {0u, 0u};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= inv;
-      *reinterpret_cast<uint2*>(row0 + c * 8) = make_uint2(encode4<INT8>(v), encode4<INT8>(v + 4));
-    };
+          for (int e = 0; e < 8; ++e) o[e >> 2] |= encode<INT8>(v[e] * inv) << (8 * (e & 3));
+          row0[c] = make_uint2(o[0], o[1]);
+        }
+      } else {
 #pragma unroll
-    for (int k = 0; k < kKeep; ++k)
-      if (gt + k * G < chunks) put(raw[k], gt + k * G);
-    for (int c = gt + kKeep * G; c < chunks; c += G) {
-      Raw8<T> r;
-      r.load(where(c));
-      put(r, c);
+        for (int k = 0; k < kKeep; ++k)
+          if (gt + k * G < chunks) put(raw[kv][k], gt + k * G);
+        for (int c = gt + kKeep * G; c < chunks; c += G) {
+          Raw8<T> r;
+          r.load(where(kv, c));
+          put(r, c);
+        }
+      }
+      if (gt == 0) a.scale[kv][ph] = scale;          // every thread has read the old one: group_max lies between
     }
-    // Every thread has read the old scale: group_max lies between.
-    if (gt == 0) a.scale[kv][ph] = scale;
   }
 }
 
-// Reading back: a thread takes 16 codes at a time, four such pieces in flight.
+// Reading back: a piece is what makes 16 bytes of output (8 codes for bf16, 4
+// for fp32), so that a warp's loads and stores are both contiguous; 4 KB of
+// codes of K and of V are in flight per CTA and pass.
 template <typename T, bool INT8, int G>
-__global__ void __launch_bounds__(kRowThreads) cache8_read_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : 4) cache8_read_kernel(RowsArgs a) {
+  constexpr int P = 16 / sizeof(T);
+  constexpr int kPieces = 32 / P;                    // 32 codes a thread
+  using Raw = typename std::conditional<P == 8, uint2, uint32_t>::type;
   __shared__ Spans spans;
   const int gt = threadIdx.x % G;
-  scan_spans<kRowThreads>(a, spans);
-  const int64_t items = static_cast<int64_t>(spans.cum[a.batch]) * (a.x[0] && a.x[1] ? 2 : 1) * a.heads;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kRowThreads / G);
-  const int per_row = a.d / 16;
-  int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / G) + threadIdx.x / G;
-  Item next = item < items ? item_at(a, spans, item) : Item();
-  for (; item < items; item += step) {
-    const Item it = next;
-    if (item + step < items) next = item_at(a, spans, item + step);
+  scan_spans<cta_threads(G)>(a, spans);
+  const int units = spans.cum[a.batch], step = gridDim.x * (cta_threads(G) / G), head = blockIdx.y;
+  const int per_row = a.d / P;
+  int u = blockIdx.x * (cta_threads(G) / G) + threadIdx.x / G, b = 0;
+  Unit next;
+  if (u < units) next = unit_at(a, spans, u, b);
+  for (; u < units; u += step) {
+    const Unit it = next;
+    if (u + step < units) next = unit_at(a, spans, u + step, b);
     const bool ok = it.page >= 0;
-    if (!ok && gt == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
-    const int kv = it.kv;
-    const int64_t ts = a.ts[kv];
-    T* x = static_cast<T*>(a.x[kv]) + it.x0 * ts + it.head * a.hs[kv];
-    const int64_t ph = static_cast<int64_t>(ok ? it.page : 0) * a.heads + it.head;
-    const float scale = ok ? a.scale[kv][ph] : 0.f;
-    const uint4* src = reinterpret_cast<const uint4*>(a.code[kv] + (ph * a.block + it.r0) * a.d);
+    if (!ok && gt == 0 && head == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
+    const int64_t ph = static_cast<int64_t>(ok ? it.page : 0) * a.heads + head;
     const int chunks = (it.r1 - it.r0) * per_row;
-    for (int c0 = gt; c0 < chunks; c0 += kKeep * G) {
-      uint4 raw[kKeep];
+    for (int c0 = gt; c0 < chunks; c0 += kPieces * G) {
+      Raw raw[2][kPieces];
+      float scale[2];
 #pragma unroll
-      for (int k = 0; k < kKeep; ++k)
-        if (c0 + k * G < chunks) raw[k] = ok ? __ldg(src + c0 + k * G) : make_uint4(0u, 0u, 0u, 0u);
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!a.x[kv]) continue;
+        const Raw* src = reinterpret_cast<const Raw*>(a.code[kv] + (ph * a.block + it.r0) * a.d);
+        scale[kv] = ok ? a.scale[kv][ph] : 0.f;
 #pragma unroll
-      for (int k = 0; k < kKeep; ++k) {
-        const int c = c0 + k * G;
-        if (c >= chunks) break;
-        const int row = (c * a.row_magic) >> 20;     // c / per_row, as above
-        T* p = x + row * ts + (c - row * per_row) * 16;
-        const uint32_t ws[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+        for (int k = 0; k < kPieces; ++k)
+          if (c0 + k * G < chunks) raw[kv][k] = ok ? src[c0 + k * G] : Raw();
+      }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[8];
-          decode4<INT8>(ws[2 * h], v);
-          decode4<INT8>(ws[2 * h + 1], v + 4);
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!a.x[kv]) continue;
+        T* x = static_cast<T*>(a.x[kv]) + it.x0 * a.ts[kv] + head * a.hs[kv];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= scale;
-          store8(p + 8 * h, v);
+        for (int k = 0; k < kPieces; ++k) {
+          const int c = c0 + k * G;
+          if (c >= chunks) break;
+          const int row = (c * a.row_magic) >> 20;   // c / per_row, as above (c < 8192, per_row <= 64)
+          const uint32_t* ws = reinterpret_cast<const uint32_t*>(&raw[kv][k]);
+          float v[P];
+#pragma unroll
+          for (int h = 0; h < P / 4; ++h) decode4<INT8>(ws[h], v + 4 * h);
+#pragma unroll
+          for (int e = 0; e < P; ++e) v[e] *= scale[kv];
+          store16(x + row * a.ts[kv] + (c - row * per_row) * P, v);
         }
       }
     }
@@ -311,20 +386,20 @@ __global__ void __launch_bounds__(kRowThreads) cache8_read_kernel(RowsArgs a) {
 }
 
 template <bool WRITE, typename T, bool INT8>
-void launch_group(bool warps, unsigned grid, const RowsArgs& a, cudaStream_t st) {
+void launch_group(bool warps, dim3 grid, const RowsArgs& a, cudaStream_t st) {
   if (WRITE) {
-    if (warps) cache8_write_kernel<T, INT8, 32><<<grid, kRowThreads, 0, st>>>(a);
-    else cache8_write_kernel<T, INT8, kRowThreads><<<grid, kRowThreads, 0, st>>>(a);
+    if (warps) cache8_write_kernel<T, INT8, 32><<<grid, cta_threads(32), 0, st>>>(a);
+    else cache8_write_kernel<T, INT8, kGroup><<<grid, cta_threads(kGroup), 0, st>>>(a);
   } else {
-    if (warps) cache8_read_kernel<T, INT8, 32><<<grid, kRowThreads, 0, st>>>(a);
-    else cache8_read_kernel<T, INT8, kRowThreads><<<grid, kRowThreads, 0, st>>>(a);
+    if (warps) cache8_read_kernel<T, INT8, 32><<<grid, cta_threads(32), 0, st>>>(a);
+    else cache8_read_kernel<T, INT8, kGroup><<<grid, cta_threads(kGroup), 0, st>>>(a);
   }
 }
 
 template <bool WRITE>
 cudaError_t launch_rows(const tq_cache8* c, tq_dtype dtype, RowsArgs a, int64_t batch, cudaStream_t st) {
   const int32_t *cu = a.cu, *start = a.start, *table = a.table;
-  const int per_row = a.d / (WRITE ? 8 : 16);
+  const int per_row = a.d / (WRITE || dtype == TQ_BF16 ? 8 : 4);
   a.row_magic = (1 << 20) / per_row + 1;
   // A warp per item where the call's sequences bring so few tokens that a warp
   // holds an item's new rows in registers; else a CTA per item.
@@ -337,11 +412,10 @@ cudaError_t launch_rows(const tq_cache8* c, tq_dtype dtype, RowsArgs a, int64_t 
     a.start = start + b0;
     a.table = table ? table + b0 * a.table_stride : nullptr;
     // Blocks touched: at most one per token, and two partial ones per sequence beside the full ones.
-    const int64_t full = a.n / c->block + 2 * nb;
-    const int64_t items = (a.n < full ? a.n : full) * c->heads * (a.x[0] && a.x[1] ? 2 : 1);
-    const int64_t ctas = warps ? (items + kRowThreads / 32 - 1) / (kRowThreads / 32) : items;
-    const int64_t most = 148 * 8;
-    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
+    const int64_t full = a.n / c->block + 2 * nb, units = a.n < full ? a.n : full;
+    const int64_t ctas = warps ? (units + cta_threads(32) / 32 - 1) / (cta_threads(32) / 32) : units;
+    const int64_t most = (148 * 8 + c->heads - 1) / c->heads;
+    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(c->heads));
     if (dtype == TQ_F32) {
       if (c->code == TQ_INT8) launch_group<WRITE, float, true>(warps, grid, a, st);
       else launch_group<WRITE, float, false>(warps, grid, a, st);
@@ -415,7 +489,7 @@ tq_status check_cache8(const tq_cache8* c, const char* what) {
     return fail(TQ_ERR_INVALID_ARG, "%s: block must be 16, 32, 64 or 128 tokens (got %d)", what, c->block);
   if (c->code != TQ_E4M3 && c->code != TQ_INT8)
     return fail(TQ_ERR_INVALID_ARG, "%s: code must be TQ_E4M3 or TQ_INT8", what);
-  if (c->heads < 1 || c->heads > 65536) return fail(TQ_ERR_INVALID_ARG, "%s: heads must be in [1, 65536]", what);
+  if (c->heads < 1 || c->heads > 65535) return fail(TQ_ERR_INVALID_ARG, "%s: heads must be in [1, 65535]", what);
   if (c->n_blocks < 1 || c->n_blocks > 0x7fffffff)
     return fail(TQ_ERR_INVALID_ARG, "%s: n_blocks must be in [1, 2^31)", what);
   if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(TQ_ERR_INVALID_ARG, "%s: NULL cache pointer", what);

@@ -81,18 +81,6 @@ __device__ __forceinline__ float decode(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
 }
 
-// Four codes at a time.
-template <bool INT8>
-__device__ __forceinline__ uint32_t encode4(const float* y) {
-  if (INT8) return encode<true>(y[0]) | encode<true>(y[1]) << 8 | encode<true>(y[2]) << 16 | encode<true>(y[3]) << 24;
-  float z[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) z[k] = y[k] == y[k] ? y[k] : 0.f;
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(z[0], z[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(z[2], z[3]), __NV_SATFINITE, __NV_E4M3);
-  return lo | hi << 16;
-}
-
 // The low / high two e4m3 codes of a word as two halves.
 template <bool HI>
 __device__ __forceinline__ uint32_t halves_e4m3(uint32_t w) {

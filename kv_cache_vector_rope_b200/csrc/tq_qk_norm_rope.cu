@@ -9,13 +9,12 @@
 //   (y_i, y_{i+rot/2}) -> (y_i cos a - y_{i+rot/2} sin a, y_i sin a + y_{i+rot/2} cos a),
 //   a = pos * base^(-2i/rot), i < rot/2; elements rot .. d-1 are not turned.
 //
-// A lane holds V consecutive values of a row (16 bytes; 8 in bf16 where the
-// alignment is for four only) and the V they are paired with, so no value
-// changes lanes. A warp takes rows of one token, several side by side and two
-// sets of them in flight: the token's angles are formed once by the warp (fp64
-// turns pos * base^(-2i/rot) / 2 pi, whose remainder goes through sincospif:
-// far positions lose whole turns only) and then sit in registers, as the
-// weights do, while the warp walks the token's heads.
+// A lane holds four consecutive values of a row and the four they are paired
+// with, so no value changes lanes. A warp takes the rows of one token, several
+// side by side and four sets of them in flight: the token's angles are formed
+// once by the warp (fp64 turns pos * base^(-2i/rot) / 2 pi, whose remainder goes
+// through sincospif: far positions lose whole turns only) and stay in registers
+// as products with the weights while the warp walks the token's heads.
 #include "tq_device.cuh"
 #include "tq_cache8.h"
 
@@ -28,10 +27,12 @@ struct NormRopeArgs {
   int hq, hkv;
   const void* q;
   const void* k;
-  int64_t q_ts, q_hs, k_ts, k_hs;
+  int64_t q_ts, k_ts;
+  int q_hs, k_hs;                                    // a token's heads lie within 2^31 elements
   void* qo;
   void* ko;
-  int64_t qo_ts, qo_hs, ko_ts, ko_hs;
+  int64_t qo_ts, ko_ts;
+  int qo_hs, ko_hs;
   const float* qw;
   const float* kw;
   float eps;
@@ -43,167 +44,178 @@ struct NormRopeArgs {
 
 constexpr int kNrThreads = 256;
 
-// V values as loaded.
-template <typename T, int V>
+// Four values as loaded.
+template <typename T>
 struct Vec;
 template <>
-struct Vec<float, 4> {
+struct Vec<float> {
   float4 x;
   __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
-  __device__ __forceinline__ void get(float* v) const { v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w; }
-  static __device__ __forceinline__ void store(float* p, const float* v) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  __device__ __forceinline__ void get(float2 (&v)[2]) const { v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w); }
+  static __device__ __forceinline__ void store(float* p, const float2 (&v)[2]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
   }
 };
-__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 template <>
-struct Vec<__nv_bfloat16, 4> {
+struct Vec<__nv_bfloat16> {
   uint2 x;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xffff0000u);
-    v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
+  __device__ __forceinline__ void get(float2 (&v)[2]) const {
+    v[0] = make_float2(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
+    v[1] = make_float2(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]));
-  }
-};
-template <>
-struct Vec<__nv_bfloat16, 8> {
-  uint4 x;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xffff0000u);
-    v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
-    v[4] = __uint_as_float(x.z << 16), v[5] = __uint_as_float(x.z & 0xffff0000u);
-    v[6] = __uint_as_float(x.w << 16), v[7] = __uint_as_float(x.w & 0xffff0000u);
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]));
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float2 (&v)[2]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0].x, v[0].y), b = __floats2bfloat162_rn(v[1].x, v[1].y);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
 };
 
+// Two fp32 products (sums) per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+
 // Rows [r0, r1) of one side (q or k) of a token. LPR: lanes per row, the power
-// of two >= d / 2V; a lane's values start at e0 and e1.
-template <typename T, int V, int LPR>
-__device__ __forceinline__ void side_rows(const T* src, int64_t hs, T* dst, int64_t ohs, int r0, int r1, const float* w,
-                                          float eps, float inv_d, int e0, int e1, bool on, bool turned, const float2* cs) {
+// of two >= d / 8; a lane's values start at e0 and e1. With w0, w1 the weights
+// and (c, s) the angle of a pair (u, v) and f the row's norm factor:
+//   f (u w0 c - v w1 s),  f (u w0 s + v w1 c).
+template <typename T, int LPR>
+__device__ __forceinline__ void side_rows(const T* src, int hs, T* dst, int ohs, int r0, int r1, const float* w,
+                                          float eps, float inv_d, int e0, int e1, bool on, const float2 (&c)[2],
+                                          const float2 (&sn)[2]) {
   constexpr int kRows = 32 / LPR;                    // rows of a warp side by side
-  constexpr int kSets = 2;
+  constexpr int kSets = 4;
   const int sub = (threadIdx.x & 31) / LPR;
-  float w0[V], w1[V];
+  float2 uc[2], vs[2], us[2], vc[2];
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    w0[k] = w && on ? __ldg(w + e0 + k) : 1.f;
-    w1[k] = w && on ? __ldg(w + e1 + k) : 1.f;
+  for (int k = 0; k < 2; ++k) {
+    float2 w0 = make_float2(1.f, 1.f), w1 = w0;
+    if (w && on) {
+      w0 = __ldg(reinterpret_cast<const float2*>(w + e0) + k);
+      w1 = __ldg(reinterpret_cast<const float2*>(w + e1) + k);
+    }
+    uc[k] = mul2(w0, c[k]);
+    us[k] = mul2(w0, sn[k]);
+    vc[k] = mul2(w1, c[k]);
+    vs[k] = mul2(w1, make_float2(-sn[k].x, -sn[k].y));
   }
+  src += e0;
+  dst += e0;
+  const int gap = e1 - e0;
+#pragma unroll 1
   for (int r = r0 + sub; r - sub < r1; r += kRows * kSets) {
-    Vec<T, V> a[kSets], b[kSets];
+    Vec<T> a[kSets], b[kSets];
 #pragma unroll
     for (int s = 0; s < kSets; ++s) {
       const int row = r + s * kRows;
       if (on && row < r1) {
-        a[s].load(src + row * hs + e0);
-        b[s].load(src + row * hs + e1);
+        const T* p = src + row * hs;
+        a[s].load(p);
+        b[s].load(p + gap);
       }
     }
 #pragma unroll
     for (int s = 0; s < kSets; ++s) {
       const int row = r + s * kRows;
       const bool live = on && row < r1;
-      float x0[V], x1[V];
+      float2 u[2], v[2];
       if (live) {
-        a[s].get(x0);
-        b[s].get(x1);
+        a[s].get(u);
+        b[s].get(v);
       } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) x0[k] = x1[k] = 0.f;
+        u[0] = u[1] = v[0] = v[1] = make_float2(0.f, 0.f);
       }
+      float f = 1.f;
       if (w) {
-        float ss = 0.f;
-#pragma unroll
-        for (int k = 0; k < V; ++k) ss = fmaf(x0[k], x0[k], fmaf(x1[k], x1[k], ss));
+        const float2 s2 = fma2(u[0], u[0], fma2(u[1], u[1], fma2(v[0], v[0], mul2(v[1], v[1]))));
+        float ss = s2.x + s2.y;
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float f = rsqrtf(ss * inv_d + eps);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          x0[k] *= f * w0[k];
-          x1[k] *= f * w1[k];
-        }
-      }
-      if (turned) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float u = x0[k], v = x1[k];
-          x0[k] = u * cs[k].x - v * cs[k].y;
-          x1[k] = u * cs[k].y + v * cs[k].x;
-        }
+        f = rsqrtf(ss * inv_d + eps);
       }
       if (live) {
-        Vec<T, V>::store(dst + row * ohs + e0, x0);
-        Vec<T, V>::store(dst + row * ohs + e1, x1);
+        const float2 ff = make_float2(f, f);
+        float2 y0[2], y1[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          y0[k] = mul2(ff, fma2(u[k], uc[k], mul2(v[k], vs[k])));
+          y1[k] = mul2(ff, fma2(u[k], us[k], mul2(v[k], vc[k])));
+        }
+        T* p = dst + row * ohs;
+        Vec<T>::store(p, y0);
+        Vec<T>::store(p + gap, y1);
       }
     }
   }
 }
 
-template <typename T, int V, int LPR>
-__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(NormRopeArgs a) {
+template <typename T, int LPR>
+__global__ void __launch_bounds__(kNrThreads, 3) qk_norm_rope_kernel(NormRopeArgs a) {
   __shared__ float2 turn[kNrThreads / 32][128];      // (cos, sin) of pair i of each warp's token
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, part_lane = lane & (LPR - 1);
   const int half = a.rot / 2, pass = (a.d - a.rot) / 2;
-  const bool on = part_lane < a.d / (2 * V);
+  const bool on = part_lane < a.d / 8;
   const bool rope = a.pos != nullptr && half > 0;
-  const bool first = V * part_lane < half;           // values that are turned come first
-  const int e0 = first ? V * part_lane : a.rot + V * part_lane - half;
+  const bool first = 4 * part_lane < half;           // values that are turned come first
+  const int e0 = first ? 4 * part_lane : a.rot + 4 * part_lane - half;
   const int e1 = e0 + (first ? half : pass);
   const bool turned = rope && first;
-  double freq[4];                                    // turns per position of pairs lane, lane + 32, ...
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-    freq[s] = rope && lane + 32 * s < half ? pow(a.base, -2.0 * (lane + 32 * s) / a.rot) * 0.15915494309189533577 : 0.0;
+  __shared__ double freq[128];                       // turns per position of each pair
+  for (int i = threadIdx.x; rope && i < half; i += blockDim.x)
+    freq[i] = pow(a.base, -2.0 * i / a.rot) * 0.15915494309189533577;
+  __syncthreads();
   const float inv_d = 1.f / a.d;
   const int64_t units = a.n * a.parts;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + w; u < units;
        u += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
     const int64_t tok = a.parts == 1 ? u : u / a.parts;
     const int r0 = static_cast<int>(u - tok * a.parts) * a.rows_per_part, r1 = min(a.hq + a.hkv, r0 + a.rows_per_part);
-    float2 cs[V];
+    // Elements that are not turned go by the angle 0.
+    float2 c[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     if (rope) {
       const int p = a.pos[tok];
       if (p < 0 && lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_POSITION);
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (32 * s >= half) break;
-        const double x = static_cast<double>(p) * freq[s];
-        float sn, c;
-        sincospif(static_cast<float>(2.0 * (x - rint(x))), &sn, &c);
-        turn[w][lane + 32 * s] = make_float2(c, sn);
+#pragma unroll 1
+      for (int i = lane; i < half; i += 32) {
+        const double x = static_cast<double>(p) * freq[i];
+        float2 y;
+        sincospif(static_cast<float>(2.0 * (x - rint(x))), &y.y, &y.x);
+        turn[w][i] = y;
       }
       __syncwarp();
       if (turned) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) cs[k] = turn[w][e0 + k];
+        for (int k = 0; k < 2; ++k) {
+          const float2 x = turn[w][e0 + 2 * k], y = turn[w][e0 + 2 * k + 1];
+          c[k] = make_float2(x.x, y.x);
+          sn[k] = make_float2(x.y, y.y);
+        }
       }
       __syncwarp();                                  // read before the next token's are written
     }
     if (r0 < a.hq)
-      side_rows<T, V, LPR>(static_cast<const T*>(a.q) + tok * a.q_ts, a.q_hs, static_cast<T*>(a.qo) + tok * a.qo_ts,
-                           a.qo_hs, r0, min(r1, a.hq), a.qw, a.eps, inv_d, e0, e1, on, turned, cs);
+      side_rows<T, LPR>(static_cast<const T*>(a.q) + tok * a.q_ts, a.q_hs, static_cast<T*>(a.qo) + tok * a.qo_ts,
+                           a.qo_hs, r0, min(r1, a.hq), a.qw, a.eps, inv_d, e0, e1, on, c, sn);
     if (r1 > a.hq)
-      side_rows<T, V, LPR>(static_cast<const T*>(a.k) + tok * a.k_ts, a.k_hs, static_cast<T*>(a.ko) + tok * a.ko_ts,
-                           a.ko_hs, max(r0 - a.hq, 0), r1 - a.hq, a.kw, a.eps, inv_d, e0, e1, on, turned, cs);
+      side_rows<T, LPR>(static_cast<const T*>(a.k) + tok * a.k_ts, a.k_hs, static_cast<T*>(a.ko) + tok * a.ko_ts,
+                           a.ko_hs, max(r0 - a.hq, 0), r1 - a.hq, a.kw, a.eps, inv_d, e0, e1, on, c, sn);
   }
 }
 
-template <typename T, int V>
+template <typename T>
 cudaError_t launch_norm_rope(NormRopeArgs a, cudaStream_t st) {
-  const int lanes = a.d / (2 * V), rows = a.hq + a.hkv;
+  const int lanes = a.d / 8, rows = a.hq + a.hkv;
   int lpr = 1;
   while (lpr < lanes) lpr *= 2;
   // Warps: one per token, or several where the tokens alone would leave SMs idle
@@ -219,12 +231,12 @@ cudaError_t launch_norm_rope(NormRopeArgs a, cudaStream_t st) {
   const int64_t ctas = (units + threads / 32 - 1) / (threads / 32);
   const unsigned grid = static_cast<unsigned>(ctas < 148 * 8 ? ctas : 148 * 8);
   switch (lpr) {
-    case 1: qk_norm_rope_kernel<T, V, 1><<<grid, threads, 0, st>>>(a); break;
-    case 2: qk_norm_rope_kernel<T, V, 2><<<grid, threads, 0, st>>>(a); break;
-    case 4: qk_norm_rope_kernel<T, V, 4><<<grid, threads, 0, st>>>(a); break;
-    case 8: qk_norm_rope_kernel<T, V, 8><<<grid, threads, 0, st>>>(a); break;
-    case 16: qk_norm_rope_kernel<T, V, 16><<<grid, threads, 0, st>>>(a); break;
-    default: qk_norm_rope_kernel<T, V, 32><<<grid, threads, 0, st>>>(a); break;
+    case 1: qk_norm_rope_kernel<T, 1><<<grid, threads, 0, st>>>(a); break;
+    case 2: qk_norm_rope_kernel<T, 2><<<grid, threads, 0, st>>>(a); break;
+    case 4: qk_norm_rope_kernel<T, 4><<<grid, threads, 0, st>>>(a); break;
+    case 8: qk_norm_rope_kernel<T, 8><<<grid, threads, 0, st>>>(a); break;
+    case 16: qk_norm_rope_kernel<T, 16><<<grid, threads, 0, st>>>(a); break;
+    default: qk_norm_rope_kernel<T, 32><<<grid, threads, 0, st>>>(a); break;
   }
   count_launch();
   return cudaGetLastError();
@@ -270,23 +282,22 @@ extern "C" tq_status tq_qk_norm_rope(int32_t d, int32_t rot_dim, int64_t n_token
     if (!aligned(s.p, vec) || !stride_ok(n_tokens, s.ts, 4) || !stride_ok(s.heads, s.hs, 4))
       return fail(TQ_ERR_INVALID_ARG, "%s must be aligned to four elements, base and strides (not negative)", s.name);
   }
+  for (Side& s : sides) {
+    if (s.heads <= 1) s.hs = 0;                      // never used
+    if (s.heads > 1 && s.hs > 0x7fffffff / s.heads)
+      return fail(TQ_ERR_UNSUPPORTED, "%s: the heads of a token span 2^31 elements or more", s.name);
+  }
   for (int i = 2; i < 4; ++i)
     if (sides[i].heads > 0 && rows_overlap(n_tokens, sides[i].ts, sides[i].heads, sides[i].hs, d))
       return fail(TQ_ERR_INVALID_ARG, "%s: its strides make rows overlap", sides[i].name);
   if ((q_weight && !aligned(q_weight, 16)) || (k_weight && !aligned(k_weight, 16)))
     return fail(TQ_ERR_INVALID_ARG, "weights must be 16-byte aligned");
-  NormRopeArgs a{d, rot_dim, n_tokens, hq, hkv, q, k, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
-                 q_out, k_out, q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride, q_weight,
+  const auto head_stride = [&](int i) { return static_cast<int>(sides[i].hs); };
+  NormRopeArgs a{d, rot_dim, n_tokens, hq, hkv, q, k, q_token_stride, k_token_stride, head_stride(0), head_stride(1),
+                 q_out, k_out, q_out_token_stride, k_out_token_stride, head_stride(2), head_stride(3), q_weight,
                  k_weight, eps, rope ? positions : nullptr, static_cast<double>(rope_base), d_status, 0, 0};
-  // bf16 rows go eight values at a time where bases, strides and halves allow it.
-  bool eight = dtype == TQ_BF16 && d % 16 == 0 && rot_dim % 16 == 0;
-  for (const Side& s : sides)
-    if (s.heads > 0)
-      eight = eight && aligned(s.p, 16) && (n_tokens == 1 || s.ts % 8 == 0) && (s.heads == 1 || s.hs % 8 == 0);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == TQ_F32 ? launch_norm_rope<float, 4>(a, st)
-                        : eight         ? launch_norm_rope<__nv_bfloat16, 8>(a, st)
-                                        : launch_norm_rope<__nv_bfloat16, 4>(a, st);
+  const cudaError_t e = dtype == TQ_F32 ? launch_norm_rope<float>(a, st) : launch_norm_rope<__nv_bfloat16>(a, st);
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "tq_qk_norm_rope launch: %s", cudaGetErrorString(e));
   return TQ_OK;
 }
