@@ -29,9 +29,7 @@
 // permuted so that a lane's operands are 16 contiguous bytes of the cache.
 #include <cuda.h>
 
-#include "tq_cache8.h"
-#include "tq_device.cuh"
-#include "tq_sm100.cuh"
+#include "tq_cache8_attn.cuh"
 
 namespace tq {
 namespace {
@@ -41,59 +39,9 @@ using namespace sm100;
 
 constexpr int kAtThreads = 256;
 constexpr int kAtWarps = kAtThreads / 32;
-constexpr int kAtGrid = 148 * 2;                     // at most two CTAs per SM
+constexpr int kAtGrid = kMaxRecs;                    // at most two CTAs per SM
 constexpr int kUnit = 64;                            // keys per unit of the split
 constexpr int kMinUnits = 2;                         // a CTA takes at least this many units
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-// Weights are kept as 2^(s - m + kLift): halves hold them to 2^-24, and the
-// running maximum m is moved only when a score exceeds it by kSlack octaves.
-constexpr float kLift = 6.f;
-constexpr float kSlack = 8.f;
-
-struct AttnArgs {
-  int heads, block, batch;
-  int64_t n_blocks;
-  const uint8_t* k;
-  const uint8_t* v;
-  const float* ks;
-  const float* vs;
-  const void* q;
-  int64_t q_bs, q_hs, q_rs;
-  int group, nq, rows;                               // rows = group * nq per KV head
-  int row_tiles;
-  const int32_t* lens;                               // of this slice
-  const int32_t* table;
-  int64_t table_stride;
-  int64_t first_seq;
-  int causal;
-  int window;
-  float scale2;                                      // softmax scale * log2 e
-  void* out;
-  int64_t o_bs, o_hs, o_rs;
-  float* lse;                                        // [batch][hq][nq] or NULL
-  float* rec;                                        // [grid][2][rows of a tile][2 + d]
-  int* cum_out;                                      // [batch + 1], for the combine kernel
-  uint64_t wait_ns;
-  int32_t* d_status;
-};
-
-__device__ __forceinline__ int seq_len(const AttnArgs& a, int b, bool tell) {
-  const int64_t n = a.lens[b], cap = a.table_stride * a.block;
-  if (n < 0 || n > cap) {
-    if (tell && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_LENGTH);
-    return n < 0 ? 0 : static_cast<int>(cap);
-  }
-  return static_cast<int>(n);
-}
-// First key any row of the sequence sees.
-__device__ __forceinline__ int seq_first(const AttnArgs& a, int n) {
-  return a.window > 0 ? max(0, n - a.nq + 1 - a.window) : 0;
-}
-__device__ __forceinline__ int seq_tiles(const AttnArgs& a, int n) {
-  return n == 0 ? 0 : (n + kUnit - 1) / kUnit - seq_first(a, n) / kUnit;
-}
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -106,28 +54,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The low / high two codes of a word as two halves.
-template <bool INT8, bool HI>
-__device__ __forceinline__ uint32_t two_halves(uint32_t w) {
-  if (INT8) {
-    // 0x64uu is 1024 + u; u = code + 128.
-    const uint32_t x = __byte_perm(w ^ 0x80808080u, 0x64646464u, HI ? 0x4342 : 0x4140);
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(1152.f, 1152.f));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  return halves_e4m3<HI>(w);
-}
-
 // Per head dim: 16-byte chunks a lane reads of each of its two keys, 4-byte
 // words it reads of each of its four values, ring stages per warp and CTAs per
 // SM (three stages of 4 KB for each of 16 warps are 192 KB at d = 128).
@@ -169,62 +95,6 @@ struct Smem {
   static constexpr int kBytes = kOffCum + 4 * (kC8Slice + 1) + 1024;   // and room to align the base
 };
 
-// One (sequence, KV head, row tile, key range) of a CTA's range.
-struct Seg {
-  int b, kv, rt, n, t0, t1;                          // keys [t0, t1)
-  bool whole;                                        // all keys of the stream
-  bool head;                                         // the stream's first keys
-};
-
-__device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, int uend, int* next) {
-  Seg s;
-  s.b = find_seq(cum, a.batch, u);
-  s.n = seq_len(a, s.b, false);
-  const int tiles = seq_tiles(a, s.n), rel = u - cum[s.b];
-  const int stream = rel / tiles, tile0 = rel % tiles;
-  s.kv = stream / a.row_tiles;
-  s.rt = stream % a.row_tiles;
-  const int nt = min(tiles - tile0, uend - u);
-  const int first = seq_first(a, s.n);
-  s.t0 = (first / kUnit + tile0) * kUnit;
-  s.t1 = min(s.t0 + nt * kUnit, s.n);
-  if (tile0 == 0) s.t0 = first / 16 * 16;
-  s.head = tile0 == 0;
-  s.whole = nt == tiles;
-  *next = u + nt;
-  return s;
-}
-
-__device__ __forceinline__ int64_t page_of(const AttnArgs& a, int b, int blk) {
-  return a.table ? static_cast<int64_t>(a.table[b * a.table_stride + blk]) : (a.first_seq + b) * a.table_stride + blk;
-}
-
-// Sixteen consecutive values of a query row.
-template <bool F32>
-__device__ __forceinline__ void load_q16(const void* p, int64_t i, float* x) {
-  if (F32) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 y = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i)[k];
-      x[4 * k] = y.x;
-      x[4 * k + 1] = y.y;
-      x[4 * k + 2] = y.z;
-      x[4 * k + 3] = y.w;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint4 y = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i)[k];
-      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        x[8 * k + 2 * h] = __uint_as_float(w[h] << 16);
-        x[8 * k + 2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
-      }
-    }
-  }
-}
-
 // Where byte `at` of a half stage lies: 16-byte chunk c of 128-byte row r sits at chunk c ^ (r % 8).
 __device__ __forceinline__ int swizzled(int at) { return at ^ ((at >> 3) & 0x70); }
 
@@ -259,12 +129,12 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     mbar_fence_init();
   }
   scan_counts<kAtThreads>(cum, reinterpret_cast<int*>(smem + L::kOffPart), a.batch, [&](int b) {
-    return seq_tiles(a, seq_len(a, b, blockIdx.x == 0)) * a.heads * a.row_tiles;
+    return head_units(a, seq_len(a, b, blockIdx.x == 0)) * a.heads;
   });
   if (blockIdx.x == 0)
     for (int b = tid; b <= a.batch; b += kAtThreads) a.cum_out[b] = cum[b];
   const int total = cum[a.batch];
-  const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinUnits);
+  const int per = units_per_cta(a, total, gridDim.x);
   const int u0 = min(static_cast<int>(blockIdx.x) * per, total), u1 = min(u0 + per, total);
   uint32_t used = 0;                                 // groups this warp's ring has carried
   bool dead = false;                                 // a wait gave up
@@ -338,10 +208,10 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
           }
         }
       if (t == 0) {
-        const int end = !live ? 0 : a.causal ? max(0, sg.n - a.nq + i + 1) : sg.n;
+        const int end = live ? row_hi(a, sg.n, i) : 0;
         sm_cq[w * 8 + g] = a.scale2 / up;
         sm_hi[w * 8 + g] = end;
-        sm_lo[w * 8 + g] = a.window > 0 ? max(0, end - a.window) : 0;
+        sm_lo[w * 8 + g] = row_lo(a, end);
       }
     }
     __syncthreads();
@@ -589,7 +459,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         f[nt][j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - sm_top[nt * 8 + 2 * t + j]) * vrun;
-    float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.head && u != u0 ? 1 : 0)) * kRows * (D + 2);
+    float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.head && u != u0 ? 1 : 0)) * kRows * (kRecHead + D);
 #pragma unroll
     for (int p0 = 0; p0 < NT * MT; p0 += 2) {
 #pragma unroll
@@ -621,10 +491,10 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
               a.lse[((a.first_seq + sg.b) * a.heads * a.group + hq) * a.nq + i] =
                   sum == 0.f ? -INFINITY : (M - kLift + log2f(sum)) * kLn2;
           } else {
-            rec[row * (D + 2) + 2 + dim] = val;
+            rec[row * (kRecHead + D) + kRecHead + dim] = val;
             if (dim == 0) {
-              rec[row * (D + 2)] = M;
-              rec[row * (D + 2) + 1] = sum;
+              rec[row * (kRecHead + D)] = M;
+              rec[row * (kRecHead + D) + 1] = sum;
             }
           }
         }
@@ -633,98 +503,6 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     }
     u = next;
   }
-}
-
-// Merges the records of every stream that more than one CTA worked on, and
-// writes the rows of streams with no key at all. One CTA per (sequence, KV
-// head, row tile) and row: the records' maxima and sums are read side by side,
-// then D / 4 lanes walk the coordinates with the other threads dealing the
-// records out among themselves, so that a stream in hundreds of records (one
-// long sequence) costs a few rounds of loads, not one per record.
-constexpr int kCbThreads = 256;
-template <int D, int NT, bool OF>
-__global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, int grid) {
-  constexpr int kRows = 8 * NT;
-  constexpr int kParts = kCbThreads / (D / 4);       // records in flight side by side
-  __shared__ float wt[kAtGrid];
-  __shared__ float red[2][kCbThreads / 32];
-  __shared__ float4 sums[kParts][D / 4];
-  const int b = blockIdx.z, stream = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-  const int kv = stream / a.row_tiles, rt = stream % a.row_tiles, r = rt * kRows + row;
-  if (r >= a.rows) return;
-  const int c0 = a.cum_out[b], tiles = (a.cum_out[b + 1] - c0) / (a.heads * a.row_tiles);
-  const int total = a.cum_out[a.batch];
-  const int per = max((total + grid - 1) / grid, kMinUnits);
-  const int u0 = c0 + stream * tiles, u1 = u0 + tiles;
-  const int first = u0 / per, last = tiles > 0 ? (u1 - 1) / per : first;
-  if (tiles > 0 && first == last) return;            // one CTA had it all and wrote the rows
-  const int n = tiles > 0 ? last - first + 1 : 0;
-  const auto record = [&](int k) {
-    const int c = first + k, slot = k == 0 && u0 != c * per ? 1 : 0;
-    return a.rec + ((static_cast<int64_t>(c) * 2 + slot) * kRows + row) * (D + 2);
-  };
-  float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;    // n <= kAtGrid <= 2 * kCbThreads
-  if (tid < n) {
-    const float* p = record(tid);
-    m0 = p[0];
-    l0 = p[1];
-  }
-  if (tid + kCbThreads < n) {
-    const float* p = record(tid + kCbThreads);
-    m1 = p[0];
-    l1 = p[1];
-  }
-  static_assert(kAtGrid <= 2 * kCbThreads, "two records per thread");
-  const float mw = dev::warp_max(fmaxf(m0, m1));
-  if ((tid & 31) == 0) red[0][tid >> 5] = mw;
-  __syncthreads();
-  float M = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < kCbThreads / 32; ++k) M = fmaxf(M, red[0][k]);
-  const float w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M), w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
-  if (tid < n) wt[tid] = w0;
-  if (tid + kCbThreads < n) wt[tid + kCbThreads] = w1;
-  const float lw = dev::warp_sum((w0 == 0.f ? 0.f : l0 * w0) + (w1 == 0.f ? 0.f : l1 * w1));
-  if ((tid & 31) == 0) red[1][tid >> 5] = lw;
-  __syncthreads();
-  float L = 0.f;
-#pragma unroll
-  for (int k = 0; k < kCbThreads / 32; ++k) L += red[1][k];
-  const int x = tid % (D / 4), part = tid / (D / 4);
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = part; k < n; k += kParts) {
-    const float w = wt[k];
-    const float2* p = reinterpret_cast<const float2*>(record(k) + 2) + 2 * x;
-    const float2 y0 = p[0], y1 = p[1];
-    sum.x = fmaf(y0.x, w, sum.x);
-    sum.y = fmaf(y0.y, w, sum.y);
-    sum.z = fmaf(y1.x, w, sum.z);
-    sum.w = fmaf(y1.y, w, sum.w);
-  }
-  sums[part][x] = sum;
-  __syncthreads();
-  if (tid >= D / 4) return;
-#pragma unroll
-  for (int k = 1; k < kParts; ++k) {
-    const float4 y = sums[k][x];
-    sum.x += y.x;
-    sum.y += y.y;
-    sum.z += y.z;
-    sum.w += y.w;
-  }
-  const int i = r / a.group, hq = kv * a.group + r % a.group;
-  const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs + 4 * x;
-  const float o[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float y = L == 0.f ? 0.f : o[k] / L;
-    if (OF) static_cast<float*>(a.out)[at + k] = y;
-    else static_cast<__nv_bfloat16*>(a.out)[at + k] = __float2bfloat16_rn(y);
-  }
-  if (a.lse && x == 0)
-    a.lse[((a.first_seq + b) * a.heads * a.group + hq) * a.nq + i] =
-        L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
 }
 
 struct Maps {
@@ -758,16 +536,12 @@ cudaError_t launch_attn(const Maps& maps, const AttnArgs& a, cudaStream_t st) {
   auto kernel = cache8_attn_kernel<D, INT8, NT, QF, OF>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  constexpr int grid = 148 * Plan<D>::kCtas;         // every CTA resident at once
+  constexpr int grid = kSms * Plan<D>::kCtas;         // every CTA resident at once
   static_assert(grid <= kAtGrid, "the workspace holds kAtGrid CTAs' records");
   kernel<<<grid, kAtThreads, smem, st>>>(maps.k, maps.v, a);
   count_launch();
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int rows = a.rows < 8 * NT ? a.rows : 8 * NT;
-  cache8_combine_kernel<D, NT, OF><<<dim3(a.heads * a.row_tiles, rows, a.batch), kCbThreads, 0, st>>>(a, grid);
-  count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : launch_combine<D, OF>(a, grid, st);
 }
 
 template <int D, bool INT8, int NT>
@@ -784,14 +558,20 @@ int rows_of(int d, int rows, bool f32) { return rows > 8 && d <= 128 && !f32 ? 1
 
 constexpr size_t kCumBytes = (sizeof(int) * (kC8Slice + 1) + 255) / 256 * 256;
 
-size_t attn_workspace(int d) { return kCumBytes + sizeof(float) * kAtGrid * 2 * 16 * static_cast<size_t>(d + 2); }
+size_t attn_workspace(int d, int64_t rows) {
+  const size_t few = sizeof(float) * kAtGrid * 2 * 16 * static_cast<size_t>(kRecHead + d);
+  const size_t many = chunk_supported(d, false, static_cast<int>(rows)) ? chunk_record_bytes(d) : 0;
+  return kCumBytes + (few > many ? few : many);
+}
 
 }  // namespace
 }  // namespace tq
 
 extern "C" size_t tq_cache8_attention_workspace_bytes(const tq_cache8* cache, int32_t batch, int32_t hq, int32_t nq) {
-  if (tq::check_cache8(cache, "tq_cache8_attention_workspace_bytes") != TQ_OK || batch < 0 || hq < 1 || nq < 1) return 0;
-  return tq::attn_workspace(cache->d);
+  if (tq::check_cache8(cache, "tq_cache8_attention_workspace_bytes") != TQ_OK || batch < 0 || hq < 1 || nq < 1 ||
+      hq % cache->heads != 0 || static_cast<int64_t>(hq) * nq > 0x3fffffff)
+    return 0;
+  return tq::attn_workspace(cache->d, static_cast<int64_t>(hq / cache->heads) * nq);
 }
 
 extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, tq_dtype q_dtype, int64_t q_batch_stride,
@@ -831,25 +611,30 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
     return fail(TQ_ERR_INVALID_ARG, "%s: the strides of out make rows overlap", what);
   if (d != 64 && d != 128 && d != 256)
     return fail(TQ_ERR_UNSUPPORTED, "%s: d=%d not built (64, 128, 256)", what, d);
-  if (!workspace || workspace_bytes < attn_workspace(d))
-    return fail(TQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, workspace_bytes, attn_workspace(d));
+  const int group = hq / cache->heads, rows = group * nq;
+  if (!workspace || workspace_bytes < attn_workspace(d, rows))
+    return fail(TQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, workspace_bytes, attn_workspace(d, rows));
   if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
   const bool qf = q_dtype == TQ_F32, of = out_dtype == TQ_F32;
-  const int group = hq / cache->heads, rows = group * nq;
-  const int tile = rows_of(d, rows, qf || of), row_tiles = (rows + tile - 1) / tile;
+  const bool many = chunk_supported(d, qf || of, rows);
+  const int tile = many ? kChunkRows : rows_of(d, rows, qf || of), row_tiles = (rows + tile - 1) / tile;
+  const int unit = many ? kChunkUnit : kUnit;
   // Units of one launch stay below 2^30: batches are cut into slices.
-  const int64_t per_seq = ((table_stride * cache->block + kUnit - 1) / kUnit) * cache->heads * row_tiles;
+  const int64_t per_seq = ((table_stride * cache->block + unit - 1) / unit + 1) * cache->heads * row_tiles;
   if (per_seq > (1 << 25))
     return fail(TQ_ERR_UNSUPPORTED, "%s: heads x query rows x capacity of one sequence too large", what);
   int64_t slice = (1 << 30) / per_seq;
   if (slice > kC8Slice) slice = kC8Slice;
   AttnArgs a{cache->heads, cache->block, 0, cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
-             q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, row_tiles, nullptr, nullptr, table_stride, 0,
+             q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, tile, row_tiles, unit, many ? kChunkMinUnits : kMinUnits,
+             nullptr, nullptr, table_stride, 0,
              causal ? 1 : 0, window, scale * kLog2e, out, out_batch_stride, out_head_stride, out_row_stride, lse_out,
              reinterpret_cast<float*>(static_cast<char*>(workspace) + kCumBytes), static_cast<int*>(workspace), pipeline_wait_ns(), d_status};
   Maps maps;
-  st = encode_maps(cache, &maps, what);
-  if (st != TQ_OK) return st;
+  if (!many) {
+    st = encode_maps(cache, &maps, what);
+    if (st != TQ_OK) return st;
+  }
   const bool i8 = cache->code == TQ_INT8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int64_t b0 = 0; b0 < batch; b0 += slice) {
@@ -859,7 +644,8 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
     a.table = block_table ? block_table + b0 * table_stride : nullptr;
     cudaError_t e;
 #define TQ_C8(D, NT) (i8 ? launch_types<D, true, NT>(qf, of, maps, a, s) : launch_types<D, false, NT>(qf, of, maps, a, s))
-    if (d == 64) e = tile == 16 ? TQ_C8(64, 2) : TQ_C8(64, 1);
+    if (many) e = launch_chunk(d, i8, a, s);
+    else if (d == 64) e = tile == 16 ? TQ_C8(64, 2) : TQ_C8(64, 1);
     else if (d == 128) e = tile == 16 ? TQ_C8(128, 2) : TQ_C8(128, 1);
     else e = TQ_C8(256, 1);
 #undef TQ_C8

@@ -1,0 +1,286 @@
+// What the kernels of tq_cache8_attention share: their arguments, how the work
+// is dealt to the CTAs, operand loads, and the merge of partial results.
+#pragma once
+
+#include "tq_cache8.h"
+#include "tq_device.cuh"
+#include "tq_sm100.cuh"
+
+namespace tq {
+namespace c8 {
+
+constexpr int kSms = 148;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Weights are kept as 2^(s - m + kLift): halves hold them to 2^-24, and the
+// running maximum m is moved only when a score exceeds it by kSlack octaves.
+constexpr float kLift = 6.f;
+constexpr float kSlack = 8.f;
+// A partial record: per row its maximum, its sum, two unused floats, d value sums.
+constexpr int kRecHead = 4;
+constexpr int kMaxRecs = 2 * kSms;                   // CTAs that may leave records of one stream
+
+struct AttnArgs {
+  int heads, block, batch;
+  int64_t n_blocks;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* ks;
+  const float* vs;
+  const void* q;
+  int64_t q_bs, q_hs, q_rs;
+  int group, nq, rows;                               // rows = group * nq per KV head, row r: position r / group
+  int tile_rows, row_tiles;                          // rows a CTA takes together
+  int unit, min_units;                               // keys per unit of the split, units a CTA takes at least
+  const int32_t* lens;                               // of this slice
+  const int32_t* table;
+  int64_t table_stride;
+  int64_t first_seq;
+  int causal;
+  int window;
+  float scale2;                                      // softmax scale * log2 e
+  void* out;
+  int64_t o_bs, o_hs, o_rs;
+  float* lse;                                        // [batch][hq][nq] or NULL
+  float* rec;                                        // [grid][2][tile_rows][kRecHead + d]
+  int* cum_out;                                      // [batch + 1], for the combine kernel
+  uint64_t wait_ns;
+  int32_t* d_status;
+};
+
+__device__ __forceinline__ int seq_len(const AttnArgs& a, int b, bool tell) {
+  const int64_t n = a.lens[b], cap = a.table_stride * a.block;
+  if (n < 0 || n > cap) {
+    if (tell && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_LENGTH);
+    return n < 0 ? 0 : static_cast<int>(cap);
+  }
+  return static_cast<int>(n);
+}
+
+// Keys [lo, hi) that row position i sees of a sequence of n keys.
+__device__ __forceinline__ int row_hi(const AttnArgs& a, int n, int i) { return a.causal ? max(0, n - a.nq + i + 1) : n; }
+__device__ __forceinline__ int row_lo(const AttnArgs& a, int hi) { return a.window > 0 ? max(0, hi - a.window) : 0; }
+
+// First key and end of what the rows of row tile rt see together, and how many
+// units of the split that is (units start at multiples of a.unit).
+struct KeyRange {
+  int lo, hi, units;
+};
+__device__ __forceinline__ KeyRange tile_range(const AttnArgs& a, int n, int rt) {
+  KeyRange r;
+  const int r0 = rt * a.tile_rows, r1 = min(a.rows, r0 + a.tile_rows) - 1;
+  r.hi = row_hi(a, n, r1 / a.group);
+  r.lo = row_lo(a, row_hi(a, n, r0 / a.group));
+  r.units = r.hi > r.lo ? (r.hi + a.unit - 1) / a.unit - r.lo / a.unit : 0;
+  return r;
+}
+// Units of one KV head of a sequence.
+__device__ __forceinline__ int head_units(const AttnArgs& a, int n) {
+  int u = 0;
+  if (n > 0)
+    for (int rt = 0; rt < a.row_tiles; ++rt) u += tile_range(a, n, rt).units;
+  return u;
+}
+
+// The units of all (sequence, KV head, row tile) streams, in that order, are
+// dealt to the CTAs in equal contiguous ranges.
+__device__ __forceinline__ int units_per_cta(const AttnArgs& a, int total, int grid) {
+  return max((total + grid - 1) / grid, a.min_units);
+}
+
+// One stream's part of a CTA's range.
+struct Seg {
+  int b, kv, rt, n, t0, t1;                          // keys [t0, t1); t0 is a multiple of 16
+  bool whole;                                        // all keys of the stream
+  bool head;                                         // the stream's first keys
+};
+__device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, int uend, int* next) {
+  Seg s;
+  s.b = find_seq(cum, a.batch, u);
+  s.n = seq_len(a, s.b, false);
+  const int per_head = (cum[s.b + 1] - cum[s.b]) / a.heads;
+  int rel = u - cum[s.b];
+  s.kv = rel / per_head;
+  rel -= s.kv * per_head;
+  s.rt = 0;
+  KeyRange r = tile_range(a, s.n, 0);
+  while (rel >= r.units) {
+    rel -= r.units;
+    r = tile_range(a, s.n, ++s.rt);
+  }
+  const int nu = min(r.units - rel, uend - u);
+  s.head = rel == 0;
+  s.whole = nu == r.units;
+  s.t0 = s.head ? r.lo / 16 * 16 : (r.lo / a.unit + rel) * a.unit;
+  s.t1 = min((r.lo / a.unit + rel + nu) * a.unit, r.hi);
+  *next = u + nu;
+  return s;
+}
+
+__device__ __forceinline__ int64_t page_of(const AttnArgs& a, int b, int blk) {
+  return a.table ? static_cast<int64_t>(a.table[b * a.table_stride + blk]) : (a.first_seq + b) * a.table_stride + blk;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The low / high two codes of a word as two halves.
+template <bool INT8, bool HI>
+__device__ __forceinline__ uint32_t two_halves(uint32_t w) {
+  if (INT8) {
+    // 0x64uu is 1024 + u; u = code + 128.
+    const uint32_t x = __byte_perm(w ^ 0x80808080u, 0x64646464u, HI ? 0x4342 : 0x4140);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(1152.f, 1152.f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return halves_e4m3<HI>(w);
+}
+
+// Sixteen consecutive values of a query row.
+template <bool F32>
+__device__ __forceinline__ void load_q16(const void* p, int64_t i, float* x) {
+  if (F32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 y = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i)[k];
+      x[4 * k] = y.x;
+      x[4 * k + 1] = y.y;
+      x[4 * k + 2] = y.z;
+      x[4 * k + 3] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 y = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i)[k];
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        x[8 * k + 2 * h] = __uint_as_float(w[h] << 16);
+        x[8 * k + 2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
+      }
+    }
+  }
+}
+
+// Merges the records of every stream that more than one CTA worked on, and
+// writes the rows of streams with no key at all. One CTA per (sequence, KV
+// head, row tile) and row: the records' maxima and sums are read side by side,
+// then D / 4 lanes walk the coordinates with the other threads dealing the
+// records out among themselves, so that a stream in hundreds of records (one
+// long sequence) costs a few rounds of loads, not one per record.
+constexpr int kCbThreads = 256;
+template <int D, bool OF>
+__global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, int grid) {
+  constexpr int kParts = kCbThreads / (D / 4);       // records in flight side by side
+  __shared__ float wt[kMaxRecs];
+  __shared__ float red[2][kCbThreads / 32];
+  __shared__ float4 sums[kParts][D / 4];
+  const int b = blockIdx.z, stream = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+  const int kv = stream / a.row_tiles, rt = stream % a.row_tiles, r = rt * a.tile_rows + row;
+  if (r >= a.rows) return;
+  const int c0 = a.cum_out[b], per_head = (a.cum_out[b + 1] - c0) / a.heads;
+  const int per = units_per_cta(a, a.cum_out[a.batch], grid);
+  int u0 = c0 + kv * per_head, units = 0;
+  if (per_head > 0) {
+    const int n = seq_len(a, b, false);
+    for (int x = 0; x < rt; ++x) u0 += tile_range(a, n, x).units;
+    units = tile_range(a, n, rt).units;
+  }
+  const int first = u0 / per, last = units > 0 ? (u0 + units - 1) / per : first;
+  if (units > 0 && first == last) return;            // one CTA had it all and wrote the rows
+  const int n = units > 0 ? last - first + 1 : 0;
+  const auto record = [&](int k) {
+    const int c = first + k, slot = k == 0 && u0 != c * per ? 1 : 0;
+    return a.rec + ((static_cast<int64_t>(c) * 2 + slot) * a.tile_rows + row) * (kRecHead + D);
+  };
+  float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;    // n <= kMaxRecs <= 2 * kCbThreads
+  if (tid < n) {
+    const float* p = record(tid);
+    m0 = p[0];
+    l0 = p[1];
+  }
+  if (tid + kCbThreads < n) {
+    const float* p = record(tid + kCbThreads);
+    m1 = p[0];
+    l1 = p[1];
+  }
+  static_assert(kMaxRecs <= 2 * kCbThreads, "two records per thread");
+  const float mw = dev::warp_max(fmaxf(m0, m1));
+  if ((tid & 31) == 0) red[0][tid >> 5] = mw;
+  __syncthreads();
+  float M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kCbThreads / 32; ++k) M = fmaxf(M, red[0][k]);
+  const float w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M), w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
+  if (tid < n) wt[tid] = w0;
+  if (tid + kCbThreads < n) wt[tid + kCbThreads] = w1;
+  const float lw = dev::warp_sum((w0 == 0.f ? 0.f : l0 * w0) + (w1 == 0.f ? 0.f : l1 * w1));
+  if ((tid & 31) == 0) red[1][tid >> 5] = lw;
+  __syncthreads();
+  float L = 0.f;
+#pragma unroll
+  for (int k = 0; k < kCbThreads / 32; ++k) L += red[1][k];
+  const int x = tid % (D / 4), part = tid / (D / 4);
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = part; k < n; k += kParts) {
+    const float w = wt[k];
+    const float4 y = reinterpret_cast<const float4*>(record(k) + kRecHead)[x];
+    sum.x = fmaf(y.x, w, sum.x);
+    sum.y = fmaf(y.y, w, sum.y);
+    sum.z = fmaf(y.z, w, sum.z);
+    sum.w = fmaf(y.w, w, sum.w);
+  }
+  sums[part][x] = sum;
+  __syncthreads();
+  if (tid >= D / 4) return;
+#pragma unroll
+  for (int k = 1; k < kParts; ++k) {
+    const float4 y = sums[k][x];
+    sum.x += y.x;
+    sum.y += y.y;
+    sum.z += y.z;
+    sum.w += y.w;
+  }
+  const int i = r / a.group, hq = kv * a.group + r % a.group;
+  const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs + 4 * x;
+  const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float y = L == 0.f ? 0.f : o[k] / L;
+    if (OF) static_cast<float*>(a.out)[at + k] = y;
+    else static_cast<__nv_bfloat16*>(a.out)[at + k] = __float2bfloat16_rn(y);
+  }
+  if (a.lse && x == 0)
+    a.lse[((a.first_seq + b) * a.heads * a.group + hq) * a.nq + i] =
+        L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
+}
+
+// Rows that one tile of tile_rows can have, for the combine kernel's grid.
+template <int D, bool OF>
+cudaError_t launch_combine(const AttnArgs& a, int grid, cudaStream_t st) {
+  const int rows = a.rows < a.tile_rows ? a.rows : a.tile_rows;
+  cache8_combine_kernel<D, OF><<<dim3(a.heads * a.row_tiles, rows, a.batch), kCbThreads, 0, st>>>(a, grid);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace c8
+
+// The tensor-memory kernel for many query rows (tq_cache8_chunk.cu): bf16
+// queries and outputs, d 64 or 128.
+constexpr int kChunkRows = 256;                      // rows a CTA takes together
+constexpr int kChunkUnit = 128;                      // keys per unit
+constexpr int kChunkMinUnits = 4;
+bool chunk_supported(int d, bool f32, int rows);
+size_t chunk_record_bytes(int d);
+cudaError_t launch_chunk(int d, bool int8, const c8::AttnArgs& a, cudaStream_t st);
+
+}  // namespace tq
