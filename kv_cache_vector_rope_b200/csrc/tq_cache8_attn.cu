@@ -624,7 +624,7 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
   if (per_seq > (1 << 25))
     return fail(TQ_ERR_UNSUPPORTED, "%s: heads x query rows x capacity of one sequence too large", what);
   int64_t slice = (1 << 30) / per_seq;
-  if (slice > kC8Slice) slice = kC8Slice;
+  if (slice > (many ? kChunkSlice : kC8Slice)) slice = many ? kChunkSlice : kC8Slice;
   AttnArgs a{cache->heads, cache->block, 0, cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
              q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, tile, row_tiles, unit, many ? kChunkMinUnits : kMinUnits,
              nullptr, nullptr, table_stride, 0,

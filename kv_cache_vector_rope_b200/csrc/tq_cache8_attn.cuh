@@ -279,6 +279,7 @@ cudaError_t launch_combine(const AttnArgs& a, int grid, cudaStream_t st) {
 constexpr int kChunkRows = 256;                      // rows a CTA takes together
 constexpr int kChunkUnit = 128;                      // keys per unit
 constexpr int kChunkMinUnits = 4;
+constexpr int kChunkSlice = 256;                     // sequences per launch
 bool chunk_supported(int d, bool f32, int rows);
 size_t chunk_record_bytes(int d);
 cudaError_t launch_chunk(int d, bool int8, const c8::AttnArgs& a, cudaStream_t st);

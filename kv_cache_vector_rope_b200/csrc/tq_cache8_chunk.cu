@@ -8,7 +8,8 @@
 //   O += P V    P (halves) in tensor memory over S, O (128 x d fp32) in tensor memory.
 // Two query tiles alternate: while one's weights are formed, the other's two
 // products run. Warps 0-3 and 4-7 form weights (one row per thread), warps 8-11
-// turn codes into halves, warp 12 issues the products.
+// turn codes into halves, warp 12 issues the products, warp 13 copies codes in
+// (a bulk copy per 16 keys, which lie in one page) and looks pages and scales up.
 //
 // Codes become halves once per CTA for all 256 rows. An 8-bit code is exactly a
 // half; a block's scale is a power of two, and so is its ratio to the largest
@@ -28,25 +29,40 @@ using namespace sm100;
 constexpr int kThreads = 512;                        // four warpgroups: weights, weights, codes, products
 constexpr int kTile = kChunkUnit;                    // keys per step
 static_assert(kTile == 128 && kChunkRows == 256, "tiles of 128 x 128");
-constexpr int kRegsWeights = 176, kRegsCodes = 112, kRegsProducts = 40;
+constexpr int kRegsWeights = 152, kRegsCodes = 104, kRegsProducts = 104;
 static_assert((2 * kRegsWeights + kRegsCodes + kRegsProducts) * 128 <= 128 * kThreads, "within the launch's registers");
+
+// What the copying warp says of a tile: the reference scales, which groups of
+// 16 keys are in the tile (loaded), which of them lie outside the cache (bad),
+// and each group's scales over the references.
+struct TileInfo {
+  float kref, vref;
+  uint32_t loaded, bad;
+  float rk[8], rv[8];
+};
 
 template <int D>
 struct Smem {
   static constexpr int kTileBytes = 128 * D * 2;     // 128 rows of halves: D / 64 atoms of [128][128 B], 128-byte swizzle
+  static constexpr int kRawBytes = 128 * D;          // 128 rows of codes
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = 2 * kTileBytes;       // two stages
   static constexpr int kOffV = kOffK + 2 * kTileBytes;
-  static constexpr int kOffInfo = kOffV + 2 * kTileBytes;        // float4 [4]: K scale, V scale, bad groups
-  static constexpr int kOffBar = kOffInfo + 64;
-  static constexpr int kBars = 17;
+  static constexpr int kOffRawK = kOffV + 2 * kTileBytes;
+  static constexpr int kOffRawV = kOffRawK + kRawBytes;
+  static constexpr int kOffInfo = kOffRawV + kRawBytes;          // TileInfo [4]
+  static constexpr int kOffBar = kOffInfo + 4 * static_cast<int>(sizeof(TileInfo));
+  static constexpr int kBars = 21;
   static constexpr int kOffTmem = kOffBar + 8 * (kBars + 1);
   static constexpr int kOffPart = kOffTmem + 16;
   static constexpr int kOffCum = kOffPart + 4 * (kThreads / 32);
-  static constexpr int kBytes = kOffCum + 4 * (kC8Slice + 1) + 1024;
+  static constexpr int kBytes = kOffCum + 4 * (kChunkSlice + 1) + 1024;
 };
 
-enum Bar { kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12, kPvDone = 14, kDrain = 16 };
+enum Bar {
+  kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12, kPvDone = 14,
+  kRawFull = 16, kRawEmpty = 18, kDrain = 20         // raw: K, V
+};
 
 // Tensor memory columns: S of tile q at 128 q (its first 64 become P), O at 256 + D q.
 constexpr uint32_t kTmemCols = 512;
@@ -68,6 +84,16 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t next)
   return d;
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 template <int R>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -81,30 +107,50 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16 codes of row `row`, coordinates 16 c .., as halves times `ratio` into a tile.
-template <int D, bool INT8>
-__device__ __forceinline__ void put_codes(uint32_t tile, int row, int c, const uint4& w, bool scaled, __half2 ratio) {
-  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+// 16 codes as halves times `ratio`, to two 16-byte chunks of a tile. Lanes of
+// odd 64-coordinate atoms store their second chunk first (the caller gives the
+// two addresses and words in that order), so that eight lanes meet eight
+// different bank groups.
+template <bool INT8>
+__device__ __forceinline__ void put_codes(uint32_t at0, uint32_t at1, const uint32_t (&w)[4], bool scaled, float ratio) {
   uint32_t h[8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    h[2 * k] = two_halves<INT8, false>(ws[k]);
-    h[2 * k + 1] = two_halves<INT8, true>(ws[k]);
+    h[2 * k] = two_halves<INT8, false>(w[k]);
+    h[2 * k + 1] = two_halves<INT8, true>(w[k]);
   }
   if (scaled) {
+    const __half2 r = __float2half2_rn(ratio);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), ratio);
+      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), r);
       h[k] = *reinterpret_cast<const uint32_t*>(&x);
     }
   }
-  const int atom = c >> 2, at = (c & 3) * 2;
-  const uint32_t base = tile + atom * (128 * 128) + row * 128;
-  // Lanes of odd atoms store their second half first, so that eight lanes meet eight different bank groups.
-  const bool odd = atom & 1;
-  const int first = at + (odd ? 1 : 0), second = at + (odd ? 0 : 1);
-  sts128(base + ((first ^ (row & 7)) << 4), odd ? h[4] : h[0], odd ? h[5] : h[1], odd ? h[6] : h[2], odd ? h[7] : h[3]);
-  sts128(base + ((second ^ (row & 7)) << 4), odd ? h[0] : h[4], odd ? h[1] : h[5], odd ? h[2] : h[6], odd ? h[3] : h[7]);
+  sts128(at0, h[0], h[1], h[2], h[3]);
+  sts128(at1, h[4], h[5], h[6], h[7]);
+}
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 template <int D, bool INT8>
@@ -114,10 +160,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
   unsigned char* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   const uint32_t base = smem_u32(smem);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-  float4* info = reinterpret_cast<float4*>(smem + L::kOffInfo);
+  TileInfo* info = reinterpret_cast<TileInfo*>(smem + L::kOffInfo);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + L::kOffTmem);
   int* cum = reinterpret_cast<int*>(smem + L::kOffCum);
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be the same for the warp
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar + kKFull + s, 128);
@@ -128,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
       mbar_init(bar + kSFull + s, 1);
       mbar_init(bar + kPFull + s, 128);
       mbar_init(bar + kPvDone + s, 1);
+      mbar_init(bar + kRawFull + s, 1);
+      mbar_init(bar + kRawEmpty + s, 128);
     }
     mbar_init(bar + kDrain, 1);
     mbar_fence_init();
@@ -144,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_at;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
   const int total = cum[a.batch];
   const int per = units_per_cta(a, total, gridDim.x);
   const int u0 = min(static_cast<int>(blockIdx.x) * per, total), u1 = min(u0 + per, total);
@@ -218,68 +267,96 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         alive = __all_sync(0xffffffffu, wait(kSFull + q, tiles_seen + j));
         if (!alive) break;
         tc_fence_after();
-        uint32_t sr[4][32];
+        const TileInfo& inf = info[(walked + j) & 3];
+        const float f = fmaxf(cq * inf.kref, 1.17549435e-38f);   // not 0: masked scores stay -inf
+        const float vref = inf.vref;
+        const uint32_t bad = inf.bad;
+        const bool masked = k0 < lo_max || k0 + kTile > hi_min || bad;
+        // 32 scores at a time, the next 32 on the way: a loop whose code stays in the instruction cache (unrolled over
+        // the tile it ran at an instruction per 12 cycles). The weights of scores 32 c .. go to columns 16 c ..,
+        // over scores that have been read.
+        const auto weights = [&](uint32_t (&x)[32], int c) {
+          if (masked) {
+            const int from = lo - (k0 + 32 * c), end = hi - (k0 + 32 * c);
+            uint32_t see = end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u;
+            see &= from >= 32 ? 0u : from <= 0 ? 0xffffffffu : ~((1u << from) - 1u);
+            see &= ((bad >> (2 * c)) & 1 ? 0u : 0xffffu) | ((bad >> (2 * c + 1)) & 1 ? 0u : 0xffff0000u);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, sr[c]);
-        tmem_ld_wait();
-        const float4 inf = info[(walked + j) & 3];
-        const float f = fmaxf(cq * inf.x, 1.17549435e-38f);   // not 0: masked scores stay -inf
-        const uint32_t bad = __float_as_uint(inf.z);
-        if (k0 < lo_max || k0 + kTile > hi_min || bad) {
+            for (int e = 0; e < 32; ++e)
+              if (!(see & (1u << e))) x[e] = 0xff800000u;
+          }
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int key = k0 + 32 * c + e;
-              if (key < lo || key >= hi || (bad >> (2 * c + e / 16)) & 1) sr[c][e] = 0xff800000u;
-            }
-        }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            top[c] = fmaxf(top[c], fmaxf(__uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1])));
-        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
-        if (__any_sync(0xffffffffu, mt > m + kSlack || inf.y != vrun)) {
-          const float mn = fmaxf(m, mt);
-          const float fm = mn == m ? 1.f : fast_exp2(m - mn);
-          m = mn;
-          l *= fm;
-          if (j > 0) {
-            // O of the tiles before is complete before it is scaled.
-            alive = __all_sync(0xffffffffu, wait(kPvDone + q, tiles_seen + j - 1));
-            if (!alive) break;
-            tc_fence_after();
-            const float fo = fm * (vrun / inf.y);
+          for (int e = 0; e < 32; e += 4) {
+            top[0] = fmaxf(top[0], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+            top[1] = fmaxf(top[1], fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+          }
+          const float mt = fmaxf(top[0], top[1]) * f;
+          if (__any_sync(0xffffffffu, mt > m + kSlack || vref != vrun)) {
+            // The maximum is too low by more than kSlack octaves, or the values' reference has grown: what has been
+            // summed up, in l, in O and in this tile's weights so far, is scaled to the new ones.
+            const float mn = fmaxf(m, mt);
+            const float fm = mn == m ? 1.f : fast_exp2(m - mn);
+            m = mn;
+            l *= fm;
+            if (j > 0) {
+              alive = __all_sync(0xffffffffu, wait(kPvDone + q, tiles_seen + j - 1));   // O is complete up to the last tile
+              tc_fence_after();
+              const float fo = fm * (vrun / vref);
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o_at + 32 * c, o);
+              for (int k = 0; alive && k < D / 16; ++k) {
+                uint32_t o[16];
+                tmem_ld16(o_at + 16 * k, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+                tmem_st16(o_at + 16 * k, o);
+              }
+            }
+            const __half2 fh = __float2half2_rn(fm);
+#pragma unroll 1
+            for (int k = 0; k < c; ++k) {
+              uint32_t o[16];
+              tmem_ld16(s_at + 16 * k, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
-              tmem_st32(o_at + 32 * c, o);
+              for (int e = 0; e < 16; ++e) {
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), fh);
+                o[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              tmem_st16(s_at + 16 * k, o);
             }
+            vrun = vref;
           }
-          vrun = inf.y;
-        }
-        // p = 2^(s f - m + kLift); a row that has seen no key yet has m = -inf, and every s is -inf too.
-        const float off = m == -INFINITY ? 0.f : kLift - m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+          // p = 2^(s f - m + kLift); a row that has seen no key yet has m = -inf, and every s is -inf too.
+          const float off = m == -INFINITY ? 0.f : kLift - m;
+          float2 sum = make_float2(0.f, 0.f);
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float p0 = fast_exp2(fmaf(__uint_as_float(sr[c][2 * e]), f, off));
-            const float p1 = fast_exp2(fmaf(__uint_as_float(sr[c][2 * e + 1]), f, off));
-            sum[e & 3] += p0 + p1;
-            pk[e] = pack_half(p0, p1);
+            float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
+                            make_float2(off, off));
+            y.x = fast_exp2(y.x);
+            y.y = fast_exp2(y.y);
+            sum = add2(sum, y);
+            pk[e] = pack_half(y.x, y.y);
           }
+          l += sum.x + sum.y;
           tmem_st16(s_at + 16 * c, pk);
+        };
+        uint32_t x0[32], x1[32];
+        tmem_ld32(s_at, x0);
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tmem_ld32(s_at + 32 * (c + 1), x1);
+          weights(x0, c);
+          tmem_ld_wait();
+          if (c < 2) tmem_ld32(s_at + 64, x0);
+          weights(x1, c + 1);
+          tmem_ld_wait();
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (!alive) break;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar + kPFull + q);
@@ -336,153 +413,268 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
     // ------------------------------------------------------------ codes to halves
     regs_down<kRegsCodes>();
     constexpr int kPer = D / 16;                     // 16-byte pieces of a row, and of a thread per tile
-    const int ct = tid - 256;
+    constexpr int kStepRows = 128 / kPer;            // rows that the 128 threads take at a time
+    const int ct = tid - 256, row = ct / kPer, c = ct % kPer;
+    // A thread's pieces: rows row, row + kStepRows, ... (a multiple of 8 rows on: the same swizzle).
+    const bool odd = (c >> 2) & 1;
+    const uint32_t to = (c >> 2) * (128 * 128) + row * 128;
+    const uint32_t at0 = to + ((((c & 3) * 2 + (odd ? 1 : 0)) ^ (row & 7)) << 4);
+    const uint32_t at1 = to + ((((c & 3) * 2 + (odd ? 0 : 1)) ^ (row & 7)) << 4);
     uint32_t it = 0;
-    float vref = 0.f;
     for (int u = u0; alive && u < u1;) {
       int next;
       const Seg sg = seg_at(a, cum, u, u1, &next);
       const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
-      vref = 0.f;
-      // Lane g of each warp keeps page and scales of keys 16 g .. of the tile (lanes 8.. idle); keys the segment does
-      // not reach have page -1, pages outside the cache -2.
-      const auto load_page = [&](int j) {
-        const int key = key0 + j * kTile + 16 * lane;
-        if (lane >= 8 || key < sg.t0 || key >= sg.t1) return -1;
-        const int64_t p = page_of(a, sg.b, key / a.block);
-        return p >= 0 && p < a.n_blocks ? static_cast<int>(p) : -2;
-      };
-      const auto load_scale = [&](const float* p, int page) {
-        return page >= 0 ? p[static_cast<int64_t>(page) * a.heads + sg.kv] : 0.f;
-      };
-      const auto load_raw = [&](const uint8_t* codes, int page, int j, uint4 (&raw)[kPer]) {
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-          const int row = (x * 128 + ct) / kPer, c = (x * 128 + ct) % kPer;
-          const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
-          const int key = key0 + j * kTile + row;
-          const bool in = pg >= 0 && key < sg.n;     // what lies behind the sequence may be any byte
-          raw[x] = in ? *reinterpret_cast<const uint4*>(
-                            codes + ((static_cast<int64_t>(pg) * a.heads + sg.kv) * a.block + key % a.block) * D + 16 * c)
-                      : make_uint4(0u, 0u, 0u, 0u);
-        }
-      };
-      int pg = load_page(0);
-      uint4 kraw[kPer], vraw[kPer];
-      load_raw(a.k, pg, 0, kraw);
-      load_raw(a.v, pg, 0, vraw);
-      float ks = load_scale(a.ks, pg), vs = load_scale(a.vs, pg);
-      for (int j = 0; j < tiles; ++j, ++it) {
-        const int pg_next = j + 1 < tiles ? load_page(j + 1) : -1;
-        const uint32_t bad = __ballot_sync(0xffffffffu, pg == -2);
-        if (bad && ct == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_BLOCK);
-        float kref = dev::warp_max(ks);
-        if (!(kref > 0.f)) kref = 1.f;               // no page at all
-        vref = fmaxf(vref, dev::warp_max(vs));
-        if (!(vref > 0.f)) vref = 1.17549435e-38f;
-        const float rk = pg >= 0 ? ks / kref : 0.f, rv = pg >= 0 ? vs / vref : 0.f;
-        const bool k_scaled = __any_sync(0xffffffffu, lane < 8 && rk != 1.f);
-        const bool v_scaled = __any_sync(0xffffffffu, lane < 8 && rv != 1.f);
-        if (ct == 0) info[it & 3] = make_float4(kref, vref, __uint_as_float(bad), 0.f);
+      for (int j = 0; alive && j < tiles; ++j, ++it) {
         const uint32_t st = it & 1, parity = (it >> 1) & 1;
-        alive = __all_sync(0xffffffffu, wait(kKEmpty + st, parity ^ 1));
-        if (!alive) break;
-        const uint32_t kt = base + L::kOffK + st * L::kTileBytes, vt = base + L::kOffV + st * L::kTileBytes;
+        const int left = sg.n - (key0 + j * kTile);  // what lies behind the sequence may be any byte
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          alive = __all_sync(0xffffffffu, wait(kRawFull + kv, it) && wait((kv ? kVEmpty : kKEmpty) + st, parity ^ 1));
+          if (!alive) break;
+          const TileInfo& inf = info[it & 3];
+          const float* ratios = kv ? inf.rv : inf.rk;
+          const uint32_t loaded = inf.loaded;
+          bool scaled = false;
 #pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-          const int row = (x * 128 + ct) / kPer, c = (x * 128 + ct) % kPer;
-          const __half2 ratio = __float2half2_rn(__shfl_sync(0xffffffffu, rk, row >> 4));
-          put_codes<D, INT8>(kt, row, c, kraw[x], k_scaled, ratio);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar + kKFull + st);
-        float ks_next = 0.f, vs_next = 0.f;
-        if (j + 1 < tiles) {
-          load_raw(a.k, pg_next, j + 1, kraw);
-          ks_next = load_scale(a.ks, pg_next);
-          vs_next = load_scale(a.vs, pg_next);
-        }
-        alive = __all_sync(0xffffffffu, wait(kVEmpty + st, parity ^ 1));
-        if (!alive) break;
+          for (int x = 0; x < 8; ++x) scaled |= ((loaded >> x) & 1) && ratios[x] != 1.f;
+          const uint4* raw = reinterpret_cast<const uint4*>(smem + (kv ? L::kOffRawV : L::kOffRawK)) + ct;
+          const uint32_t tile = base + (kv ? L::kOffV : L::kOffK) + st * L::kTileBytes;
+          const bool clean = left >= kTile && loaded == 0xffu;
+          uint4 codes[kPer];
 #pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-          const int row = (x * 128 + ct) / kPer, c = (x * 128 + ct) % kPer;
-          const __half2 ratio = __float2half2_rn(__shfl_sync(0xffffffffu, rv, row >> 4));
-          put_codes<D, INT8>(vt, row, c, vraw[x], v_scaled, ratio);
+          for (int x = 0; x < kPer; ++x) codes[x] = raw[x * 128];
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) {
+            const int group = (x * kStepRows + row) >> 4;
+            uint4 y = codes[x];
+            if (!clean && (!((loaded >> group) & 1) || x * kStepRows + row >= left)) y = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t words[4] = {odd ? y.z : y.x, odd ? y.w : y.y, odd ? y.x : y.z, odd ? y.y : y.w};
+            put_codes<INT8>(tile + at0 + x * kStepRows * 128, tile + at1 + x * kStepRows * 128, words, scaled,
+                            scaled ? ratios[group] : 1.f);
+          }
+          mbar_arrive(bar + kRawEmpty + kv);
+          fence_proxy_async_smem();
+          mbar_arrive(bar + (kv ? kVFull : kKFull) + st);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(bar + kVFull + st);
-        if (j + 1 < tiles) load_raw(a.v, pg_next, j + 1, vraw);
-        pg = pg_next;
-        ks = ks_next;
-        vs = vs_next;
       }
       u = next;
     }
   } else {
     // ------------------------------------------------------------ products
     regs_down<kRegsProducts>();
-    if (w == 12 && lane == 0) {
+    if (w == 12) {
+      // The whole warp walks the loop, so that descriptors stay warp-uniform,
+      // and one elected lane issues: from a single-lane branch each product
+      // took 390 cycles to issue (a chunk of 2 x 1024 tokens 1417 us).
+      const bool leader = elect_one();
       constexpr uint32_t kIdS = idesc_f16(128, 128, false), kIdO = idesc_f16(128, D, true);
+      const uint64_t q_desc = desc_k_sw128(base + L::kOffQ), k_desc = desc_k_sw128(base + L::kOffK);
+      const uint64_t v_desc = desc_mn_sw128(base + L::kOffV, 128 * 128);
       uint32_t it = 0, segs[2] = {0, 0}, done[2] = {0, 0};
-      const auto scores = [&](int q, uint32_t st) {
+      const auto ready = [&](int which, uint32_t parity) { return __all_sync(0xffffffffu, wait(which, parity)); };
+      const auto scores = [&](int q, uint32_t st, bool last) {
+        const uint64_t qd = q_desc + ((q * L::kTileBytes) >> 4), kd = k_desc + ((st * L::kTileBytes) >> 4);
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-          umma_ss(tmem + 128 * q, desc_k_sw128(base + L::kOffQ + q * L::kTileBytes + off),
-                  desc_k_sw128(base + L::kOffK + st * L::kTileBytes + off), kIdS, k != 0);
+          for (int k = 0; k < D / 16; ++k) {
+            constexpr int kAtom = 128 * 128;
+            const uint64_t off = static_cast<uint64_t>(((k >> 2) * kAtom + (k & 3) * 32) >> 4);
+            umma_ss(tmem + 128 * q, qd + off, kd + off, kIdS, k != 0);
+          }
+          umma_commit(bar + kSFull + q);
+          if (last) umma_commit(bar + kKEmpty + st);
         }
-        umma_commit(bar + kSFull + q);
       };
-      const auto values = [&](int q, uint32_t st, bool first) {
+      const auto values = [&](int q, uint32_t st, bool first, bool last) {
+        const uint64_t vd = v_desc + ((st * L::kTileBytes) >> 4);
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_ts(tmem + 256 + D * q, tmem + 128 * q + 8 * k,
-                  desc_mn_sw128(base + L::kOffV + st * L::kTileBytes + k * 16 * 128, 128 * 128), kIdO, !(first && k == 0));
-        umma_commit(bar + kPvDone + q);
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_ts(tmem + 256 + D * q, tmem + 128 * q + 8 * k, vd + static_cast<uint64_t>((k * 16 * 128) >> 4), kIdO,
+                    !(first && k == 0));
+          umma_commit(bar + kPvDone + q);
+          if (last) umma_commit(bar + kVEmpty + st);
+        }
       };
       for (int u = u0; alive && u < u1;) {
         int next;
         const Seg sg = seg_at(a, cum, u, u1, &next);
         const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
-        const int nq = a.rows - sg.rt * kChunkRows > 128 ? 2 : 1;
-        for (int j = 0; alive && j <= tiles; ++j) {
+        const int nq = __shfl_sync(0xffffffffu, a.rows - sg.rt * kChunkRows > 128 ? 2 : 1, 0);
+        const int steps = __shfl_sync(0xffffffffu, tiles, 0);
+        for (int j = 0; alive && j <= steps; ++j) {
           // Step j: the values of tile j - 1, then the scores of tile j, query tile by query tile.
           const uint32_t st = (it + j) & 1, was = st ^ 1;
-          if (j < tiles && !wait(kKFull + st, (it + j) >> 1)) alive = false;
-          for (int q = 0; alive && q < nq; ++q) {
+          if (j < steps) alive = ready(kKFull + st, (it + j) >> 1);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (!alive || q >= nq) break;
             if (j > 0) {
-              if (q == 0 && !wait(kVFull + was, (it + j - 1) >> 1)) alive = false;
-              if (alive && !wait(kPFull + q, done[q])) alive = false;
+              alive = (q > 0 || ready(kVFull + was, (it + j - 1) >> 1)) && ready(kPFull + q, done[q]);
               if (!alive) break;
               tc_fence_after();
-              values(q, was, j == 1);
+              values(q, was, j == 1, q == nq - 1);
               ++done[q];
-              if (q == nq - 1) umma_commit(bar + kVEmpty + was);
             } else {
-              if (!wait(kQFull + q, segs[q])) alive = false;
+              alive = ready(kQFull + q, segs[q]);
               if (!alive) break;
               ++segs[q];
             }
-            if (j < tiles) {
+            if (j < steps) {
               tc_fence_after();
-              scores(q, st);
-              if (q == nq - 1) umma_commit(bar + kKEmpty + st);
+              scores(q, st, q == nq - 1);
             }
           }
+          __syncwarp();
         }
-        it += tiles;
+        it += steps;
         u = next;
       }
       // What was issued ends, and its last arrivals land, before tensor memory is freed and the CTA ends.
-      umma_commit(bar + kDrain);
+      if (leader) umma_commit(bar + kDrain);
+      __syncwarp();
       mbar_wait(bar + kDrain, 0);
+    } else if (w == 13) {
+      // ---------------------------------------------------------- codes in: lane g < 8 takes keys 16 g .. of each tile
+      uint32_t it = 0;
+      const uint32_t bytes = 16 * D;
+      for (int u = u0; alive && u < u1;) {
+        int next;
+        const Seg sg = seg_at(a, cum, u, u1, &next);
+        const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
+        float vref = 0.f;
+        // -1: keys the segment does not reach, -2: a page outside the cache.
+        const auto load_page = [&](int j) {
+          const int key = key0 + j * kTile + 16 * lane;
+          if (j >= tiles || lane >= 8 || key < sg.t0 || key >= sg.t1) return -1;
+          const int64_t p = page_of(a, sg.b, key / a.block);
+          return p >= 0 && p < a.n_blocks ? static_cast<int>(p) : -2;
+        };
+        const auto load_scale = [&](const float* p, int page) {
+          return page >= 0 ? p[static_cast<int64_t>(page) * a.heads + sg.kv] : 0.f;
+        };
+        int page = load_page(0), page1 = load_page(1);
+        float ks = load_scale(a.ks, page), vs = load_scale(a.vs, page);
+        for (int j = 0; j < tiles; ++j, ++it) {
+          const int page2 = load_page(j + 2);
+          const float ks1 = load_scale(a.ks, page1), vs1 = load_scale(a.vs, page1);
+          const uint32_t loaded = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -2);
+          if (bad && lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_BLOCK);
+          float kref = dev::warp_max(ks);
+          if (!(kref > 0.f)) kref = 1.f;             // no page at all
+          vref = fmaxf(vref, dev::warp_max(vs));
+          const float vr = vref > 0.f ? vref : 1.17549435e-38f;
+          const int64_t at = ((static_cast<int64_t>(page) * a.heads + sg.kv) * a.block + (key0 + j * kTile + 16 * lane) % a.block) * D;
+          const uint32_t sum = __popc(loaded) * bytes;
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            alive = __all_sync(0xffffffffu, wait(kRawEmpty + kv, it + 1));
+            if (!alive) break;
+            if (kv == 0) {
+              TileInfo& inf = info[it & 3];
+              if (lane == 0) {
+                inf.kref = kref;
+                inf.vref = vr;
+                inf.loaded = loaded;
+                inf.bad = bad;
+              }
+              if (lane < 8) {
+                inf.rk[lane] = ks / kref;
+                inf.rv[lane] = vs / vr;
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(bar + kRawFull + kv, sum);
+            __syncwarp();
+            if (page >= 0)
+              bulk_load(base + (kv ? L::kOffRawV : L::kOffRawK) + lane * bytes, (kv ? a.v : a.k) + at, bytes, bar + kRawFull + kv);
+          }
+          if (!alive) break;
+          page = page1;
+          page1 = page2;
+          ks = ks1;
+          vs = vs1;
+        }
+        u = next;
+      }
+      // Copies in flight land before the CTA ends (bar kRawFull's phase `it - 1` is the last one armed, if any).
+      if (it > 0 || !alive)
+        for (int kv = 0; kv < 2; ++kv) {
+          mbar_wait(bar + kRawFull + kv, (it - 1) & 1);
+          if (!alive) mbar_wait(bar + kRawFull + kv, it & 1, 1000000ull);
+        }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (w == 12) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Merges the records of the streams that the CTAs' ranges cut, a warp per row.
+// Block x < grid - 1 looks at the cut between CTAs x and x + 1 and takes the
+// stream it runs through, if it is that stream's first cut; the blocks behind
+// write the rows of streams with no key at all.
+constexpr int kMergeEmpty = 8;
+template <int D>
+__global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 8 + w;
+  const auto put = [&](int b, int kv, int r, const float* y, float inv, float lse) {
+    const int i = r / a.group, hq = kv * a.group + r % a.group;
+    const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs;
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(to + e) = __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[((a.first_seq + b) * a.heads * a.group + hq) * a.nq + i] = lse;
+  };
+  float y[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
+  const int total = a.cum_out[a.batch], per = units_per_cta(a, total, grid);
+  if (static_cast<int>(blockIdx.x) >= grid - 1) {
+    for (int b = blockIdx.x - (grid - 1); b < a.batch; b += kMergeEmpty) {
+      const int n = seq_len(a, b, false);
+      for (int rt = 0; rt < a.row_tiles; ++rt) {
+        if (n > 0 && tile_range(a, n, rt).units > 0) continue;
+        const int r = rt * a.tile_rows + row;
+        if (r < a.rows)
+          for (int kv = 0; kv < a.heads; ++kv) put(b, kv, r, y, 0.f, -INFINITY);
+      }
+    }
+    return;
+  }
+  const int cut = (blockIdx.x + 1) * per;
+  if (cut >= total) return;
+  int next;
+  const Seg sg = seg_at(a, a.cum_out, cut, total, &next);
+  const int units = tile_range(a, sg.n, sg.rt).units, u0 = next - units;
+  if (u0 == cut || u0 < static_cast<int>(blockIdx.x) * per) return;   // cut at its start, or cut before as well
+  const int r = sg.rt * a.tile_rows + row;
+  if (r >= a.rows) return;
+  const int first = blockIdx.x, n = (u0 + units - 1) / per - first + 1;
+  const auto record = [&](int k) {
+    const int c = first + k, slot = k == 0 && u0 != c * per ? 1 : 0;
+    return a.rec + ((static_cast<int64_t>(c) * 2 + slot) * a.tile_rows + row) * (kRecHead + D);
+  };
+  float M = -INFINITY;
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, record(k)[0]);
+  M = dev::warp_max(M);
+  float l = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float* p = record(k);
+    const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M);
+    l += f == 0.f ? 0.f : p[1] * f;
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(p + kRecHead + lane * (D / 32) + e);
+      y[e] = fmaf(x.x, f, y[e]);
+      y[e + 1] = fmaf(x.y, f, y[e + 1]);
+    }
+  }
+  put(sg.b, sg.kv, r, y, l == 0.f ? 0.f : 1.f / l, l == 0.f ? -INFINITY : (M - kLift + log2f(l)) * kLn2);
 }
 
 template <int D, bool INT8>
@@ -494,7 +686,10 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
   cache8_chunk_kernel<D, INT8><<<kSms, kThreads, smem, st>>>(a);
   count_launch();
   e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_combine<D, false>(a, kSms, st);
+  if (e != cudaSuccess) return e;
+  cache8_merge_kernel<D><<<dim3(kSms - 1 + kMergeEmpty, kChunkRows / 8), 256, 0, st>>>(a, kSms);
+  count_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace
