@@ -612,14 +612,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
   if (w == 12) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Merges the records of the streams that the CTAs' ranges cut, a warp per row.
+// Merges the records of the streams that the CTAs' ranges cut, a warp per row
+// and four rows per warp, one after another.
 // Block x < grid - 1 looks at the cut between CTAs x and x + 1 and takes the
 // stream it runs through, if it is that stream's first cut; the blocks behind
 // write the rows of streams with no key at all.
-constexpr int kMergeEmpty = 8;
+constexpr int kMergeEmpty = 8, kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 8 + w;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = (blockIdx.y * 8 + w) * kMergeRows;
   const auto put = [&](int b, int kv, int r, const float* y, float inv, float lse) {
     const int i = r / a.group, hq = kv * a.group + r % a.group;
     const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs;
@@ -629,18 +630,16 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid)
       *reinterpret_cast<__nv_bfloat162*>(to + e) = __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
     if (a.lse && lane == 0) a.lse[((a.first_seq + b) * a.heads * a.group + hq) * a.nq + i] = lse;
   };
-  float y[D / 32];
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
   const int total = a.cum_out[a.batch], per = units_per_cta(a, total, grid);
   if (static_cast<int>(blockIdx.x) >= grid - 1) {
     for (int b = blockIdx.x - (grid - 1); b < a.batch; b += kMergeEmpty) {
       const int n = seq_len(a, b, false);
       for (int rt = 0; rt < a.row_tiles; ++rt) {
         if (n > 0 && tile_range(a, n, rt).units > 0) continue;
-        const int r = rt * a.tile_rows + row;
-        if (r < a.rows)
-          for (int kv = 0; kv < a.heads; ++kv) put(b, kv, r, y, 0.f, -INFINITY);
+        const float y[D / 32] = {};
+        for (int row = row0; row < row0 + kMergeRows; ++row)
+          if (rt * a.tile_rows + row < a.rows)
+            for (int kv = 0; kv < a.heads; ++kv) put(b, kv, rt * a.tile_rows + row, y, 0.f, -INFINITY);
       }
     }
     return;
@@ -651,30 +650,35 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid)
   const Seg sg = seg_at(a, a.cum_out, cut, total, &next);
   const int units = tile_range(a, sg.n, sg.rt).units, u0 = next - units;
   if (u0 == cut || u0 < static_cast<int>(blockIdx.x) * per) return;   // cut at its start, or cut before as well
-  const int r = sg.rt * a.tile_rows + row;
-  if (r >= a.rows) return;
   const int first = blockIdx.x, n = (u0 + units - 1) / per - first + 1;
-  const auto record = [&](int k) {
-    const int c = first + k, slot = k == 0 && u0 != c * per ? 1 : 0;
-    return a.rec + ((static_cast<int64_t>(c) * 2 + slot) * a.tile_rows + row) * (kRecHead + D);
-  };
-  float M = -INFINITY;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, record(k)[0]);
-  M = dev::warp_max(M);
-  float l = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float* p = record(k);
-    const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M);
-    l += f == 0.f ? 0.f : p[1] * f;
+  const int slot0 = u0 != first * per ? 1 : 0;
+  for (int row = row0; row < row0 + kMergeRows; ++row) {
+    const int r = sg.rt * a.tile_rows + row;
+    if (r >= a.rows) return;
+    const auto record = [&](int k) {
+      return a.rec + ((static_cast<int64_t>(first + k) * 2 + (k == 0 ? slot0 : 0)) * kChunkRows + row) * (kRecHead + D);
+    };
+    float y[D / 32];
 #pragma unroll
-    for (int e = 0; e < D / 32; e += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(p + kRecHead + lane * (D / 32) + e);
-      y[e] = fmaf(x.x, f, y[e]);
-      y[e + 1] = fmaf(x.y, f, y[e + 1]);
+    for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, record(k)[0]);
+    M = dev::warp_max(M);
+    float l = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float* p = record(k);
+      const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M);
+      l += f == 0.f ? 0.f : p[1] * f;
+#pragma unroll
+      for (int e = 0; e < D / 32; e += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p + kRecHead + lane * (D / 32) + e);
+        y[e] = fmaf(x.x, f, y[e]);
+        y[e + 1] = fmaf(x.y, f, y[e + 1]);
+      }
     }
+    put(sg.b, sg.kv, r, y, l == 0.f ? 0.f : 1.f / l, l == 0.f ? -INFINITY : (M - kLift + log2f(l)) * kLn2);
   }
-  put(sg.b, sg.kv, r, y, l == 0.f ? 0.f : 1.f / l, l == 0.f ? -INFINITY : (M - kLift + log2f(l)) * kLn2);
 }
 
 template <int D, bool INT8>
@@ -687,7 +691,7 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cache8_merge_kernel<D><<<dim3(kSms - 1 + kMergeEmpty, kChunkRows / 8), 256, 0, st>>>(a, kSms);
+  cache8_merge_kernel<D><<<dim3(kSms - 1 + kMergeEmpty, kChunkRows / 8 / kMergeRows), 256, 0, st>>>(a, kSms);
   count_launch();
   return cudaGetLastError();
 }
