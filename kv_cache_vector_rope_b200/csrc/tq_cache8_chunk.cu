@@ -6,8 +6,9 @@
 // CTA takes 256 rows (two query tiles of 128) and walks 128 keys at a time,
 //   S = Q K^T   both operands in shared memory, S (128 x 128 fp32) in tensor memory,
 //   O += P V    P (halves) in tensor memory over S, O (128 x d fp32) in tensor memory.
-// Two query tiles alternate: while one's weights are formed, the other's two
-// products run. Warps 0-3 and 4-7 form weights (one row per thread), warps 8-11
+// Two query tiles alternate, and each takes the 128 keys in two halves: while the
+// weights of one half are formed, the values of the half before and the scores
+// of the half after run, so that neither side waits for the other. Warps 0-3 and 4-7 form weights (one row per thread), warps 8-11
 // turn codes into halves, warp 12 issues the products, warp 13 copies codes in
 // (a bulk copy per 16 keys, which lie in one page) and looks pages and scales up.
 //
@@ -52,7 +53,7 @@ struct Smem {
   static constexpr int kOffRawV = kOffRawK + kRawBytes;
   static constexpr int kOffInfo = kOffRawV + kRawBytes;          // TileInfo [4]
   static constexpr int kOffBar = kOffInfo + 4 * static_cast<int>(sizeof(TileInfo));
-  static constexpr int kBars = 21;
+  static constexpr int kBars = 27;
   static constexpr int kOffTmem = kOffBar + 8 * (kBars + 1);
   static constexpr int kOffPart = kOffTmem + 16;
   static constexpr int kOffCum = kOffPart + 4 * (kThreads / 32);
@@ -60,11 +61,13 @@ struct Smem {
 };
 
 enum Bar {
-  kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12, kPvDone = 14,
-  kRawFull = 16, kRawEmpty = 18, kDrain = 20         // raw: K, V
+  kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kQFull = 8, kRawFull = 10, kRawEmpty = 12,   // raw: K, V
+  // Query tile q, half h at 2 q + h. One barrier per half and a phase per tile: a wait tells a phase from the one
+  // before it only, and up to two halves of one query tile are under way.
+  kSFull = 14, kPFull = 18, kPvDone = 22, kDrain = 26
 };
 
-// Tensor memory columns: S of tile q at 128 q (its first 64 become P), O at 256 + D q.
+// Tensor memory columns: S of tile q, half h at 128 q + 64 h (its first 32 become P), O at 256 + D q.
 constexpr uint32_t kTmemCols = 512;
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
@@ -147,6 +150,31 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
+// Scores of keys that a row does not see become -inf: those outside [from, end)
+// of the 32, and those of bad groups of 16.
+__device__ __forceinline__ void hide(uint32_t (&x)[32], int from, int end, uint32_t bad) {
+  uint32_t see = end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u;
+  see &= from >= 32 ? 0u : from <= 0 ? 0xffffffffu : ~((1u << from) - 1u);
+  see &= (bad & 1 ? 0u : 0xffffu) | (bad & 2 ? 0u : 0xffff0000u);
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(see & (1u << e))) x[e] = 0xff800000u;
+}
+// Weights 2^(x f + off) of 32 scores: their sum, and as halves to 16 columns.
+__device__ __forceinline__ void weights(const uint32_t (&x)[32], float f, float off, float2& sum, uint32_t at) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
+                    make_float2(off, off));
+    y.x = fast_exp2(y.x);
+    y.y = fast_exp2(y.y);
+    sum = add2(sum, y);
+    pk[e] = pack_half(y.x, y.y);
+  }
+  tmem_st16(at, pk);
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(smem_u32(bar))
@@ -167,16 +195,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
   const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be the same for the warp
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar + kKFull + s, 128);
-      mbar_init(bar + kVFull + s, 128);
+      mbar_init(bar + kKFull + s, 4);
+      mbar_init(bar + kVFull + s, 4);
       mbar_init(bar + kKEmpty + s, 1);
       mbar_init(bar + kVEmpty + s, 1);
-      mbar_init(bar + kQFull + s, 128);
-      mbar_init(bar + kSFull + s, 1);
-      mbar_init(bar + kPFull + s, 128);
-      mbar_init(bar + kPvDone + s, 1);
+      mbar_init(bar + kQFull + s, 4);
+      mbar_init(bar + kSFull + 2 * s, 1);
+      mbar_init(bar + kSFull + 2 * s + 1, 1);
+      mbar_init(bar + kPFull + 2 * s, 4);
+      mbar_init(bar + kPFull + 2 * s + 1, 4);
+      mbar_init(bar + kPvDone + 2 * s, 1);
+      mbar_init(bar + kPvDone + 2 * s + 1, 1);
       mbar_init(bar + kRawFull + s, 1);
-      mbar_init(bar + kRawEmpty + s, 128);
+      mbar_init(bar + kRawEmpty + s, 4);
     }
     mbar_init(bar + kDrain, 1);
     mbar_fence_init();
@@ -202,6 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
     if (mbar_wait(bar + which, parity & 1, a.wait_ns)) return true;
     if (a.d_status) atomicOr(a.d_status, TQ_DEV_TIMEOUT);
     return false;
+  };
+  // One arrival per warp: 32 lanes' arrivals at one barrier queue up for hundreds of cycles.
+  const auto arrive = [&](int which) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + which);
   };
   bool alive = true;
 
@@ -255,113 +291,78 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           sts128(to + (((c0 + 1) ^ (wr & 7)) << 4), h[4], h[5], h[6], h[7]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar + kQFull + q);
+        arrive(kQFull + q);
       }
       const int hi = live ? row_hi(a, sg.n, i) : 0, lo = row_lo(a, hi);
       // Keys in [lo_max, hi_min) are seen by every row of the tile.
       const int hi_min = row_hi(a, sg.n, r0 / a.group);
       const int lo_max = row_lo(a, row_hi(a, sg.n, min(r0 + 127, a.rows - 1) / a.group));
       float m = -INFINITY, l = 0.f, vrun = 0.f;
-      for (int j = 0; j < tiles; ++j) {
-        const int k0 = key0 + j * kTile;
-        alive = __all_sync(0xffffffffu, wait(kSFull + q, tiles_seen + j));
+      for (int j = 0; j < 2 * tiles; ++j) {          // halves of 64 keys
+        const int half = j & 1, k0 = key0 + j * 64;
+        const uint32_t at = s_at + 64 * half;
+        alive = __all_sync(0xffffffffu, wait(kSFull + 2 * q + half, tiles_seen + (j >> 1)));
         if (!alive) break;
         tc_fence_after();
-        const TileInfo& inf = info[(walked + j) & 3];
+        uint32_t x0[32], x1[32];
+        tmem_ld32(at, x0);
+        tmem_ld32(at + 32, x1);
+        const TileInfo& inf = info[(walked + (j >> 1)) & 3];
         const float f = fmaxf(cq * inf.kref, 1.17549435e-38f);   // not 0: masked scores stay -inf
         const float vref = inf.vref;
-        const uint32_t bad = inf.bad;
-        const bool masked = k0 < lo_max || k0 + kTile > hi_min || bad;
-        // 32 scores at a time, the next 32 on the way: a loop whose code stays in the instruction cache (unrolled over
-        // the tile it ran at an instruction per 12 cycles). The weights of scores 32 c .. go to columns 16 c ..,
-        // over scores that have been read.
-        const auto weights = [&](uint32_t (&x)[32], int c) {
-          if (masked) {
-            const int from = lo - (k0 + 32 * c), end = hi - (k0 + 32 * c);
-            uint32_t see = end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u;
-            see &= from >= 32 ? 0u : from <= 0 ? 0xffffffffu : ~((1u << from) - 1u);
-            see &= ((bad >> (2 * c)) & 1 ? 0u : 0xffffu) | ((bad >> (2 * c + 1)) & 1 ? 0u : 0xffff0000u);
+        const uint32_t bad = inf.bad >> (4 * half);
+        const bool masked = k0 < lo_max || k0 + 64 > hi_min || (bad & 15);
+        tmem_ld_wait();
+        if (masked) {
+          hide(x0, lo - k0, hi - k0, bad);
+          hide(x1, lo - k0 - 32, hi - k0 - 32, bad >> 2);
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see & (1u << e))) x[e] = 0xff800000u;
-          }
-          float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            top[0] = fmaxf(top[0], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-            top[1] = fmaxf(top[1], fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
-          }
-          const float mt = fmaxf(top[0], top[1]) * f;
-          if (__any_sync(0xffffffffu, mt > m + kSlack || vref != vrun)) {
-            // The maximum is too low by more than kSlack octaves, or the values' reference has grown: what has been
-            // summed up, in l, in O and in this tile's weights so far, is scaled to the new ones.
-            const float mn = fmaxf(m, mt);
-            const float fm = mn == m ? 1.f : fast_exp2(m - mn);
-            m = mn;
-            l *= fm;
-            if (j > 0) {
-              alive = __all_sync(0xffffffffu, wait(kPvDone + q, tiles_seen + j - 1));   // O is complete up to the last tile
-              tc_fence_after();
-              const float fo = fm * (vrun / vref);
+        for (int e = 0; e < 32; e += 4) {
+          top[0] = fmaxf(top[0], fmaxf(__uint_as_float(x0[e]), __uint_as_float(x0[e + 1])));
+          top[1] = fmaxf(top[1], fmaxf(__uint_as_float(x0[e + 2]), __uint_as_float(x0[e + 3])));
+          top[2] = fmaxf(top[2], fmaxf(__uint_as_float(x1[e]), __uint_as_float(x1[e + 1])));
+          top[3] = fmaxf(top[3], fmaxf(__uint_as_float(x1[e + 2]), __uint_as_float(x1[e + 3])));
+        }
+        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
+        if (__any_sync(0xffffffffu, mt > m + kSlack || vref != vrun)) {
+          // The maximum is too low by more than kSlack octaves, or the values' reference has grown: what has been
+          // summed up, in l and in O, is scaled to the new ones.
+          const float mn = fmaxf(m, mt);
+          const float fm = mn == m ? 1.f : fast_exp2(m - mn);
+          m = mn;
+          l *= fm;
+          if (j > 0) {
+            // O holds the half before, and with it all others: the products end in order.
+            alive = __all_sync(0xffffffffu, wait(kPvDone + 2 * q + (half ^ 1), tiles_seen + ((j - 1) >> 1)));
+            if (!alive) break;
+            tc_fence_after();
+            const float fo = fm * (vrun / vref);
 #pragma unroll 1
-              for (int k = 0; alive && k < D / 16; ++k) {
-                uint32_t o[16];
-                tmem_ld16(o_at + 16 * k, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
-                tmem_st16(o_at + 16 * k, o);
-              }
-            }
-            const __half2 fh = __float2half2_rn(fm);
-#pragma unroll 1
-            for (int k = 0; k < c; ++k) {
+            for (int k = 0; k < D / 16; ++k) {
               uint32_t o[16];
-              tmem_ld16(s_at + 16 * k, o);
+              tmem_ld16(o_at + 16 * k, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), fh);
-                o[e] = *reinterpret_cast<const uint32_t*>(&y);
-              }
-              tmem_st16(s_at + 16 * k, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+              tmem_st16(o_at + 16 * k, o);
             }
-            vrun = vref;
           }
-          // p = 2^(s f - m + kLift); a row that has seen no key yet has m = -inf, and every s is -inf too.
-          const float off = m == -INFINITY ? 0.f : kLift - m;
-          float2 sum = make_float2(0.f, 0.f);
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
-                            make_float2(off, off));
-            y.x = fast_exp2(y.x);
-            y.y = fast_exp2(y.y);
-            sum = add2(sum, y);
-            pk[e] = pack_half(y.x, y.y);
-          }
-          l += sum.x + sum.y;
-          tmem_st16(s_at + 16 * c, pk);
-        };
-        uint32_t x0[32], x1[32];
-        tmem_ld32(s_at, x0);
-        tmem_ld_wait();
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          tmem_ld32(s_at + 32 * (c + 1), x1);
-          weights(x0, c);
-          tmem_ld_wait();
-          if (c < 2) tmem_ld32(s_at + 64, x0);
-          weights(x1, c + 1);
-          tmem_ld_wait();
+          vrun = vref;
         }
-        if (!alive) break;
+        // p = 2^(s f - m + kLift); a row that has seen no key yet has m = -inf, and every s is -inf too.
+        const float off = m == -INFINITY ? 0.f : kLift - m;
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+        weights(x0, f, off, sum0, at);
+        weights(x1, f, off, sum1, at + 16);
+        sum0 = add2(sum0, sum1);
+        l += sum0.x + sum0.y;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar + kPFull + q);
+        arrive(kPFull + 2 * q + half);
       }
-      if (alive) alive = __all_sync(0xffffffffu, wait(kPvDone + q, tiles_seen + tiles - 1));
+      if (alive) alive = __all_sync(0xffffffffu, wait(kPvDone + 2 * q + 1, tiles_seen + tiles - 1));
       if (!alive) break;
       tiles_seen += tiles;
       walked += tiles;
@@ -453,9 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
             put_codes<INT8>(tile + at0 + x * kStepRows * 128, tile + at1 + x * kStepRows * 128, words, scaled,
                             scaled ? ratios[group] : 1.f);
           }
-          mbar_arrive(bar + kRawEmpty + kv);
           fence_proxy_async_smem();
-          mbar_arrive(bar + (kv ? kVFull : kKFull) + st);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar + kRawEmpty + kv);
+            mbar_arrive(bar + (kv ? kVFull : kKFull) + st);
+          }
         }
       }
       u = next;
@@ -468,32 +472,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
       // and one elected lane issues: from a single-lane branch each product
       // took 390 cycles to issue (a chunk of 2 x 1024 tokens 1417 us).
       const bool leader = elect_one();
-      constexpr uint32_t kIdS = idesc_f16(128, 128, false), kIdO = idesc_f16(128, D, true);
+      constexpr uint32_t kIdS = idesc_f16(128, 64, false), kIdO = idesc_f16(128, D, true);
       const uint64_t q_desc = desc_k_sw128(base + L::kOffQ), k_desc = desc_k_sw128(base + L::kOffK);
       const uint64_t v_desc = desc_mn_sw128(base + L::kOffV, 128 * 128);
       uint32_t it = 0, segs[2] = {0, 0}, done[2] = {0, 0};
       const auto ready = [&](int which, uint32_t parity) { return __all_sync(0xffffffffu, wait(which, parity)); };
-      const auto scores = [&](int q, uint32_t st, bool last) {
-        const uint64_t qd = q_desc + ((q * L::kTileBytes) >> 4), kd = k_desc + ((st * L::kTileBytes) >> 4);
+      const auto scores = [&](int q, int half, uint32_t st, bool last) {
+        const uint64_t qd = q_desc + ((q * L::kTileBytes) >> 4), kd = k_desc + ((st * L::kTileBytes + half * 64 * 128) >> 4);
         if (leader) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             constexpr int kAtom = 128 * 128;
             const uint64_t off = static_cast<uint64_t>(((k >> 2) * kAtom + (k & 3) * 32) >> 4);
-            umma_ss(tmem + 128 * q, qd + off, kd + off, kIdS, k != 0);
+            umma_ss(tmem + 128 * q + 64 * half, qd + off, kd + off, kIdS, k != 0);
           }
-          umma_commit(bar + kSFull + q);
+          umma_commit(bar + kSFull + 2 * q + half);
           if (last) umma_commit(bar + kKEmpty + st);
         }
       };
-      const auto values = [&](int q, uint32_t st, bool first, bool last) {
-        const uint64_t vd = v_desc + ((st * L::kTileBytes) >> 4);
+      const auto values = [&](int q, int half, uint32_t st, bool first, bool last) {
+        const uint64_t vd = v_desc + ((st * L::kTileBytes + half * 64 * 128) >> 4);
         if (leader) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_ts(tmem + 256 + D * q, tmem + 128 * q + 8 * k, vd + static_cast<uint64_t>((k * 16 * 128) >> 4), kIdO,
-                    !(first && k == 0));
-          umma_commit(bar + kPvDone + q);
+          for (int k = 0; k < 4; ++k)
+            umma_ts(tmem + 256 + D * q, tmem + 128 * q + 64 * half + 8 * k, vd + static_cast<uint64_t>((k * 16 * 128) >> 4),
+                    kIdO, !(first && k == 0));
+          umma_commit(bar + kPvDone + 2 * q + half);
           if (last) umma_commit(bar + kVEmpty + st);
         }
       };
@@ -504,31 +508,35 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         const int nq = __shfl_sync(0xffffffffu, a.rows - sg.rt * kChunkRows > 128 ? 2 : 1, 0);
         const int steps = __shfl_sync(0xffffffffu, tiles, 0);
         for (int j = 0; alive && j <= steps; ++j) {
-          // Step j: the values of tile j - 1, then the scores of tile j, query tile by query tile.
+          // Step j: half by half and query tile by query tile, the values of tile j - 1, then the scores of tile j.
           const uint32_t st = (it + j) & 1, was = st ^ 1;
           if (j < steps) alive = ready(kKFull + st, (it + j) >> 1);
+          if (alive && j > 0) alive = ready(kVFull + was, (it + j - 1) >> 1);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            if (!alive || q >= nq) break;
+          for (int x = 0; x < 4; ++x) {
+            const int half = x >> 1, q = x & 1;
+            if (!alive || q >= nq) continue;
+            const bool last = half == 1 && q == nq - 1;
             if (j > 0) {
-              alive = (q > 0 || ready(kVFull + was, (it + j - 1) >> 1)) && ready(kPFull + q, done[q]);
-              if (!alive) break;
+              alive = ready(kPFull + 2 * q + half, done[q] + j - 1);
+              if (!alive) continue;
               tc_fence_after();
-              values(q, was, j == 1, q == nq - 1);
-              ++done[q];
-            } else {
+              values(q, half, was, j == 1 && half == 0, last);
+            } else if (half == 0) {
               alive = ready(kQFull + q, segs[q]);
-              if (!alive) break;
+              if (!alive) continue;
               ++segs[q];
             }
             if (j < steps) {
               tc_fence_after();
-              scores(q, st, q == nq - 1);
+              scores(q, half, st, last);
             }
           }
           __syncwarp();
         }
         it += steps;
+        done[0] += steps;
+        if (nq > 1) done[1] += steps;
         u = next;
       }
       // What was issued ends, and its last arrivals land, before tensor memory is freed and the CTA ends.
