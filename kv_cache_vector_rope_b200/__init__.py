@@ -4,7 +4,8 @@ and attention computed directly over the packed cache.
 This package is a thin ctypes binding over ``libtq.so`` (C ABI declared in
 ``include/tq.h``). Every function here only marshals arguments — tensor
 pointers, sizes, the current CUDA stream — and calls the library of the same
-name; all arithmetic runs in the library's CUDA kernels (or, for
+name (the calls of a serving step through ``_tq_torch``, a C++ extension, the
+others through ctypes); all arithmetic runs in the library's CUDA kernels (or, for
 ``tq_make_codebook``, its host C++ code). There is no Python or CPU fallback:
 if the library is missing, importing the binding raises.
 
@@ -114,6 +115,10 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+try:
+    from . import _tq_torch as _bind            # checks and marshalling of the short calls (binding/tq_torch.cpp)
+except ImportError as e:
+    raise ImportError("_tq_torch.so is not built or does not load; run `python kv_cache_vector_rope_b200/build.py`") from e
 
 
 def exported_symbols() -> list[str]:
@@ -150,7 +155,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:                                       # the raw handle: a Stream object costs 3 us a call
+    if stream is None:                          # the raw handle: a Stream object costs 3 us a call
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -319,51 +324,6 @@ def tq_dequantize_sign_mean(lay: Layout, is_key: bool, planes: Planes, n_vectors
                                         _stream(stream)))
 
 
-# The checks below are written out flat: a call of a decode step takes the GPU 3 to 10 us, and these lines are most of
-# what it takes the host.
-def _on_device(*tensors) -> None:
-    """Every given tensor is a CUDA tensor on the current device (the library launches there)."""
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:          # -1 for a CPU tensor
-            raise ValueError(f"a {list(t.shape)} tensor is on {t.device}: all must be CUDA tensors on the current "
-                             f"device (cuda:{dev})")
-
-
-def _int32(t, name: str, shape: tuple) -> None:
-    """An int32 tensor, contiguous, of the given shape."""
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
-
-
-def _status_word(t) -> int | None:
-    if t is None:
-        return None
-    if t.dtype is not torch.int32 or t.numel() < 1:
-        raise ValueError("d_status must be an int32 tensor with an element")
-    return t.data_ptr()
-
-
-def _weight(w, name: str, d: int) -> int | None:
-    if w is None:
-        return None
-    if w.dtype is not torch.float32 or w.shape != (d,) or not w.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape [{d}]")
-    return w.data_ptr()
-
-
-def _heads(x: torch.Tensor, o: torch.Tensor, one: torch.Tensor, name: str) -> tuple:
-    """Pointers and strides of [tokens, heads, d] rows and of the rows they become."""
-    xs, os_ = x.stride(), o.stride()
-    if x.dim() != 3 or x.shape[0] != one.shape[0] or x.shape[2] != one.shape[2] or o.shape != x.shape:
-        raise ValueError(f"{name} and {name}_out must be [tokens, heads, d] tensors of the same shape")
-    if x.numel() and (xs[2] != 1 or os_[2] != 1):
-        raise ValueError(f"{name} and {name}_out must have unit stride along d")
-    if x.dtype is not one.dtype or o.dtype is not one.dtype:
-        raise ValueError("q, k and their outputs must have one dtype")
-    return x.shape[1], x.data_ptr(), xs[0], xs[1], o.data_ptr(), os_[0], os_[1]
-
-
 def tq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None,
                     k_out: torch.Tensor | None, q_weight: torch.Tensor | None = None,
                     k_weight: torch.Tensor | None = None, eps: float = 1e-6, positions: torch.Tensor | None = None,
@@ -373,23 +333,8 @@ def tq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch
 
     The tensors may be strided views (unit stride along d), an output its own input; a side that is None is left out,
     as is the norm of a side without a weight ([d] float32) and the rotation without positions ([tokens] int32)."""
-    one = q if q is not None else k
-    if one is None or one.dim() != 3:
-        raise ValueError("q and k must be [tokens, heads, d] tensors, one of them at least")
-    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
-        raise ValueError("q and q_out, and k and k_out, go together")
-    n, d = one.shape[0], one.shape[2]
-    hq, qp, qt, qh, qop, qot, qoh = _heads(q, q_out, one, "q") if q is not None else (0, None, 0, 0, None, 0, 0)
-    hk, kp, kt, kh, kop, kot, koh = _heads(k, k_out, one, "k") if k is not None else (0, None, 0, 0, None, 0, 0)
-    pos = None
-    if positions is not None:
-        _int32(positions, "positions", (n,))
-        pos = positions.data_ptr()
-    _on_device(q, k, q_out, k_out, q_weight, k_weight, positions, d_status)
-    st = _lib.tq_qk_norm_rope(d, d if rot_dim is None else rot_dim, n, hq, hk, _dtype_code(one), qp, qt, qh, kp, kt, kh,
-                              qop, qot, qoh, kop, kot, koh, _weight(q_weight, "q_weight", d),
-                              _weight(k_weight, "k_weight", d), eps, pos, rope_base, _status_word(d_status),
-                              _stream(stream))
+    st = _bind.qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, eps, positions, rope_base, rot_dim, d_status,
+                            None if stream is None else _stream(stream))
     if st:
         _check(st)
 
@@ -437,51 +382,24 @@ def alloc_cache8(n_blocks: int, heads: int, block: int, d: int, code: str = "e4m
     return Cache8(*codes, *scales, code)
 
 
-def _table8(c: _Cache8, table, batch: int) -> tuple:
-    """Pointer and stride of a block table (without one, every sequence has an equal share of the pages)."""
-    if table is None:
-        return None, c.n_blocks // max(batch, 1)
-    if table.dim() != 2 or table.shape[0] != batch or table.dtype is not torch.int32 or not table.is_contiguous():
-        raise ValueError("block_table must be a contiguous int32 [batch, blocks] tensor")
-    return table.data_ptr(), table.shape[1]
-
-
-def _rows8(fn, cache: Cache8, k, v, cu_tokens, start, block_table, d_status, stream) -> None:
-    c = cache.c()
-    one = k if k is not None else v
-    if one is None:
-        raise ValueError("k and v are both None")
-    shape = (one.shape[0], c.heads, c.d)
-    for x in (k, v):
-        if x is not None and (x.shape != shape or x.dtype is not one.dtype or (x.stride(2) != 1 and x.numel())):
-            raise ValueError(f"k and v must be [tokens, {c.heads}, {c.d}] tensors of one dtype with unit stride along d")
-    kp, kt, kh = (k.data_ptr(), k.stride(0), k.stride(1)) if k is not None else (None, 0, 0)
-    vp, vt, vh = (v.data_ptr(), v.stride(0), v.stride(1)) if v is not None else (None, 0, 0)
-    batch = start.shape[0]
-    _int32(cu_tokens, "cu_tokens", (batch + 1,))
-    _int32(start, "start", (batch,))
-    table, stride = _table8(c, block_table, batch)
-    _on_device(cache.k, cache.v, cache.k_scale, cache.v_scale, k, v, cu_tokens, start, block_table, d_status)
-    st = fn(c, _dtype_code(one), kp, kt, kh, vp, vt, vh, shape[0], batch, cu_tokens.data_ptr(), start.data_ptr(), table,
-            stride, _status_word(d_status), _stream(stream))
-    if st:
-        _check(st)
-
-
 def tq_cache8_write(cache: Cache8, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, start: torch.Tensor,
                     block_table: torch.Tensor | None = None, d_status: torch.Tensor | None = None, stream=None) -> None:
     """Quantises rows cu_tokens[b] .. cu_tokens[b+1]-1 of k and v ([tokens, heads, d]) into positions start[b], ...
     of sequence b (cu_tokens int32 [batch+1], start int32 [batch], block_table int32 [batch, blocks])."""
-    if k is None or v is None:
-        raise ValueError("tq_cache8_write needs k and v")
-    _rows8(_lib.tq_cache8_write, cache, k, v, cu_tokens, start, block_table, d_status, stream)
+    st = _bind.cache8_rows(True, cache.k, cache.v, cache.k_scale, cache.v_scale, cache.code, k, v, cu_tokens, start,
+                           block_table, d_status, None if stream is None else _stream(stream))
+    if st:
+        _check(st)
 
 
 def tq_cache8_read(cache: Cache8, k_out: torch.Tensor | None, v_out: torch.Tensor | None, cu_tokens: torch.Tensor,
                    start: torch.Tensor, block_table: torch.Tensor | None = None, d_status: torch.Tensor | None = None,
                    stream=None) -> None:
     """Reads positions start[b], ... of sequence b back into rows cu_tokens[b] .. cu_tokens[b+1]-1 of k_out and v_out."""
-    _rows8(_lib.tq_cache8_read, cache, k_out, v_out, cu_tokens, start, block_table, d_status, stream)
+    st = _bind.cache8_rows(False, cache.k, cache.v, cache.k_scale, cache.v_scale, cache.code, k_out, v_out, cu_tokens, start,
+                           block_table, d_status, None if stream is None else _stream(stream))
+    if st:
+        _check(st)
 
 
 def tq_cache8_attention_workspace_bytes(cache: Cache8, batch: int, hq: int, nq: int) -> int:
@@ -499,28 +417,9 @@ def tq_cache8_attention(cache: Cache8, q: torch.Tensor, seq_lens: torch.Tensor, 
                         d_status: torch.Tensor | None = None, stream=None) -> None:
     """Attention of q ([batch, hq, nq, d], any strides with unit stride along d) over the first seq_lens[b] tokens of
     each sequence; row i stands at position seq_lens[b] - nq + i. out is as q, lse_out float32 [batch, hq, nq]."""
-    c = cache.c()
-    if q.dim() != 4 or out.shape != q.shape:
-        raise ValueError("q and out must be [batch, hq, nq, d] tensors of the same shape")
-    batch, hq, nq, d = q.shape
-    qb, qh, qr, qd = q.stride()
-    ob, oh, orow, od = out.stride()
-    if (qd != 1 or od != 1) and q.numel():
-        raise ValueError("q and out must have unit stride along d")
-    if d != c.d:
-        raise ValueError(f"q has d = {d}, the cache {c.d}")
-    _int32(seq_lens, "seq_lens", (batch,))
-    table, stride = _table8(c, block_table, batch)
-    lse = None
-    if lse_out is not None:
-        if lse_out.dtype is not torch.float32 or lse_out.shape != (batch, hq, nq) or not lse_out.is_contiguous():
-            raise ValueError("lse_out must be a contiguous float32 [batch, hq, nq] tensor")
-        lse = lse_out.data_ptr()
-    _on_device(cache.k, cache.v, cache.k_scale, cache.v_scale, q, out, seq_lens, workspace, block_table, lse_out, d_status)
-    st = _lib.tq_cache8_attention(c, q.data_ptr(), _dtype_code(q), qb, qh, qr, batch, hq, nq, seq_lens.data_ptr(), table,
-                                  stride, causal, window, 1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
-                                  _dtype_code(out), ob, oh, orow, lse, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _status_word(d_status), _stream(stream))
+    st = _bind.cache8_attention(cache.k, cache.v, cache.k_scale, cache.v_scale, cache.code, q, seq_lens, out, workspace,
+                                block_table, causal, window, scale, lse_out, d_status,
+                                None if stream is None else _stream(stream))
     if st:
         _check(st)
 

@@ -1,4 +1,5 @@
-"""Builds libtq.so (the CUDA library behind the C ABI in include/tq.h) in-tree.
+"""Builds libtq.so (the CUDA library behind the C ABI in include/tq.h) and
+_tq_torch.so (checks and marshalling of the short calls) in-tree.
 
     python kv_cache_vector_rope_b200/build.py          # compile if stale
     python kv_cache_vector_rope_b200/build.py --force  # always compile
@@ -20,6 +21,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtq.so")
+BINDING_SRC = os.path.join(PKG, "binding", "tq_torch.cpp")
+BINDING = os.path.join(PKG, "_tq_torch.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -62,7 +65,31 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return LIB
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The Python extension, by the host compiler against torch's headers; links libtq.so next to it."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "tq.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include") if os.path.isabs(nvcc()) else None
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], INCLUDE, *([cuda] if cuda else [])]
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f for i in includes for f in ("-isystem", i)), "-o", tmp, BINDING_SRC, f"-L{PKG}", "-l:libtq.so",
+           "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     force = "--force" in sys.argv
     extra = ["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else None
     print(build(force=force or bool(extra), verbose=True, extra=extra))
+    print(build_binding(force=force, verbose=True))

@@ -79,12 +79,40 @@ def test_sizes():
     assert f(ctypes.byref(_cache()), 2, 32, 1) > 0 and f(ctypes.byref(_cache(block=5)), 2, 32, 1) == 0
 
 
-def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+def _refuses(what, f, *a, **k):
+    with pytest.raises(ValueError, match=what):
+        f(*a, **k)
+
+
+def test_binding_refuses_before_anything_is_launched():
     c = tq.alloc_cache8(4, 2, 16, 64, device="cpu")
     assert c.nbytes() == tq.tq_cache8_bytes(64, 2, 16, 4)
-    x = torch.zeros(3, 2, 64)
-    cu, start = torch.tensor([0, 3], dtype=torch.int32), torch.tensor([0], dtype=torch.int32)
-    if not torch.cuda.is_available():
-        return                                               # the current device is asked for first
-    with pytest.raises(ValueError, match="CUDA"):
-        tq.tq_cache8_write(c, x, x, cu, start)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    x, cu, start, table = torch.zeros(3, 2, 64), i32(0, 3), i32(0), torch.zeros(1, 4, dtype=torch.int32)
+    for f in (tq.tq_cache8_write, tq.tq_cache8_read):
+        _refuses("CUDA", f, c, x, x, cu, start)
+        _refuses("tensor", f, c, "x", x, cu, start)
+        _refuses("heads and d", f, c, x[:, :1], x, cu, start)
+        _refuses("heads and d", f, c, x, x.bfloat16(), cu, start)
+        _refuses("unit stride", f, c, x.transpose(1, 2).contiguous().transpose(1, 2), x, cu, start)
+        _refuses("cu_tokens is None", f, c, x, x, None, start)
+        _refuses("start", f, c, x, x, cu, start[0])
+    _refuses("k and v are needed", tq.tq_cache8_write, c, x, None, cu, start)
+    _refuses("both None", tq.tq_cache8_read, c, None, None, cu, start)
+    bad = tq.Cache8(c.k, c.v, c.k_scale, c.v_scale[:2], "e4m3")
+    _refuses("scales", tq.tq_cache8_read, bad, x, x, cu, start)
+    _refuses("code", tq.tq_cache8_read, tq.Cache8(c.k, c.v, c.k_scale, c.v_scale, "e5m2"), x, x, cu, start)
+    q, ws = torch.zeros(1, 4, 1, 64), torch.zeros(1 << 20, dtype=torch.uint8)
+    _refuses("CUDA", tq.tq_cache8_attention, c, q, start, q, ws, table)
+    _refuses("same shape", tq.tq_cache8_attention, c, q, start, q[0], ws, table)
+    _refuses("q's d", tq.tq_cache8_attention, c, q[..., :32], start, q[..., :32], ws, table)
+    _refuses("lse_out", tq.tq_cache8_attention, c, q, start, q, ws, table, lse_out=torch.zeros(4))
+    _refuses("seq_lens is None", tq.tq_cache8_attention, c, q, None, q, ws, table)
+    _refuses("go together", tq.tq_qk_norm_rope, x, None, None, x)
+    _refuses("output as its input", tq.tq_qk_norm_rope, x, None, x[:2], None)
+    _refuses("one dtype", tq.tq_qk_norm_rope, x, None, x.bfloat16(), None)
+    _refuses("weights", tq.tq_qk_norm_rope, x, None, x, None, q_weight=torch.ones(32))
+    _refuses("one of them at least", tq.tq_qk_norm_rope, None, None, None, None)
+    _refuses("CUDA", tq.tq_qk_norm_rope, x, x, x, x)
+    with pytest.raises(TypeError):
+        tq._bind.cache8_rows(1, 2)

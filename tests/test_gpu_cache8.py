@@ -378,6 +378,27 @@ def test_attention_of_many_sequences_without_a_table():
     _check_attention(S, q, lens.tolist(), out, lse, "bf16")
 
 
+def test_binding_refusals_on_the_device():
+    s = Setup(2, [32], 2, 64, 16, "e4m3")
+    x = torch.zeros(4, 2, 64, device="cuda")
+    for cu, start, table in ((_i32([0, 4]).long(), _i32([0]), s.dtable), (_i32([0, 4, 4]), _i32([0]), s.dtable),
+                             (_i32([0, 4]), _i32([0]), s.dtable.t()), (_i32([0, 4]), _i32([0]), s.dtable.cpu()),
+                             (_i32([0, 4]).cpu(), _i32([0]), s.dtable)):
+        with pytest.raises(ValueError):
+            tq.tq_cache8_write(s.cache, x, x, cu, start, block_table=table)
+    with pytest.raises(ValueError):
+        tq.tq_cache8_write(s.cache, x, x, _i32([0, 4]), _i32([0]), block_table=s.dtable, d_status=torch.zeros(1, device="cuda"))
+    with pytest.raises(ValueError):
+        tq.tq_cache8_write(s.cache, x.half(), x.half(), _i32([0, 4]), _i32([0]), block_table=s.dtable)
+    with pytest.raises(tq.TQError):
+        tq.tq_cache8_read(s.cache, x[:, :, :64].expand(4, 2, 64)[:1].expand(4, 2, 64), None, _i32([0, 4]), _i32([0]),
+                          block_table=s.dtable)                      # rows of an output that overlap
+    q = torch.zeros(1, 2, 1, 64, device="cuda")
+    with pytest.raises(tq.TQError) as e:
+        tq.tq_cache8_attention(s.cache, q, _i32([1]), q, torch.zeros(256, dtype=torch.uint8, device="cuda"), block_table=s.dtable)
+    assert e.value.status == tq.TQ_ERR_WORKSPACE
+
+
 # ------------------------------------------------------------------ together
 def test_prompt_then_steps_together_eager_and_in_a_graph():
     """norm + rotation, write, attention over a prompt and three steps; the steps also replayed from one graph on a side
