@@ -42,6 +42,7 @@ constexpr int kAtWarps = kAtThreads / 32;
 constexpr int kAtGrid = kMaxRecs;                    // at most two CTAs per SM
 constexpr int kUnit = 64;                            // keys per unit of the split
 constexpr int kMinUnits = 2;                         // a CTA takes at least this many units
+constexpr int kLead = 8;                             // a segment's start and merge, in units
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -138,37 +139,50 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
   const int u0 = min(static_cast<int>(blockIdx.x) * per, total), u1 = min(u0 + per, total);
   uint32_t used = 0;                                 // groups this warp's ring has carried
   bool dead = false;                                 // a wait gave up
-  for (int u = u0; u < u1;) {
-    int next;
-    const Seg sg = seg_at(a, cum, u, u1, &next);
-    const int k0 = sg.t0 + 16 * w;                   // this warp's groups: k0, k0 + 128, ...
-    const int groups = sg.t1 > k0 ? (sg.t1 - k0 + 16 * kAtWarps - 1) / (16 * kAtWarps) : 0;
-    // Pages and scales of 32 groups at a time, one group per lane, the next 32 loaded ahead.
-    const auto load_page = [&](int i) {
-      return i < groups ? static_cast<int>(page_of(a, sg.b, (k0 + i * 16 * kAtWarps) / a.block)) : 0;
-    };
-    const auto ok = [&](int page) { return page >= 0 && page < a.n_blocks; };
-    const auto load_scale = [&](const float* p, int page) {
-      return ok(page) ? p[static_cast<int64_t>(page) * a.heads + sg.kv] : 0.f;
-    };
-    int pg = load_page(lane), pg_next = load_page(32 + lane);
-    const auto issue = [&](int i, int rel) {         // group i = 32 * (batch of pg) + rel
-      const int page = __shfl_sync(0xffffffffu, rel < 32 ? pg : pg_next, rel & 31);
-      if (lane == 0) {
-        const int key = k0 + i * 16 * kAtWarps;
-        // A bad page's group is masked; page 0 is copied in its place.
-        const int64_t ph = static_cast<int64_t>(ok(page) ? page : 0) * a.heads + sg.kv;
-        const int row = static_cast<int>((ph * a.block + key % a.block) * D / 128);
-        const int st = (used + i) % ST;
-        mbar_expect_tx(bar + st, L::kStage);
-        tma_load_2d(ring + st * L::kStage, &kmap, bar + st, 0, row);
-        tma_load_2d(ring + st * L::kStage + L::kHalfStage, &vmap, bar + st, 0, row);
-      }
-    };
-    int issued = 0;
+  // The segment at hand and what this warp has on its way of it: groups k0, k0 + 128, ..., of which `issued` are
+  // being copied. Pages and scales of 32 groups at a time, one group per lane, the next 32 loaded ahead.
+  Seg sg{};
+  int u = u0, next = u0, k0 = 0, groups = 0, issued = 0, pg = 0, pg_next = 0;
+  float sc_k = 0.f, sc_v = 0.f;
+  const auto load_page = [&](int i) {
+    return i < groups ? static_cast<int>(page_of(a, sg.b, (k0 + i * 16 * kAtWarps) / a.block)) : 0;
+  };
+  const auto ok = [&](int page) { return page >= 0 && page < a.n_blocks; };
+  const auto load_scale = [&](const float* p, int page) {
+    return ok(page) ? p[static_cast<int64_t>(page) * a.heads + sg.kv] : 0.f;
+  };
+  const auto issue = [&](int i, int rel) {           // group i = 32 * (batch of pg) + rel
+    const int page = __shfl_sync(0xffffffffu, rel < 32 ? pg : pg_next, rel & 31);
+    if (lane == 0) {
+      const int key = k0 + i * 16 * kAtWarps;
+      // A bad page's group is masked; page 0 is copied in its place.
+      const int64_t ph = static_cast<int64_t>(ok(page) ? page : 0) * a.heads + sg.kv;
+      const int row = static_cast<int>((ph * a.block + key % a.block) * D / 128);
+      const int st = (used + i) % ST;
+      mbar_expect_tx(bar + st, L::kStage);
+      tma_load_2d(ring + st * L::kStage, &kmap, bar + st, 0, row);
+      tma_load_2d(ring + st * L::kStage + L::kHalfStage, &vmap, bar + st, 0, row);
+    }
+  };
+  // The next segment with keys, if the range has one: its first groups set out.
+  const auto open = [&] {
+    for (u = next; u < u1; u = next) {
+      sg = seg_at(a, cum, u, u1, &next);
+      if (sg.t1 > sg.t0) break;
+    }
+    if (u >= u1) return;
+    k0 = sg.t0 + 16 * w;
+    groups = sg.t1 > k0 ? (sg.t1 - k0 + 16 * kAtWarps - 1) / (16 * kAtWarps) : 0;
+    pg = load_page(lane);
+    pg_next = load_page(32 + lane);
+    issued = 0;
     if (!dead)
       for (; issued < ST && issued < groups; ++issued) issue(issued, issued);
-    float sc_k = load_scale(a.ks, pg), sc_v = load_scale(a.vs, pg);
+    sc_k = load_scale(a.ks, pg);
+    sc_v = load_scale(a.vs, pg);
+  };
+  open();
+  while (u < u1) {
     float nx_k = 0.f, nx_v = 0.f;
     __syncthreads();                                 // the last segment's readers of sm_q and sm_row are done
     // Queries: warp nt prepares the operands of rows 8 nt .. 8 nt + 7; lane (g, t) holds row g's coordinates of its chunks.
@@ -428,6 +442,9 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       for (int i = issued > ST ? issued - ST : 0; i < issued; ++i)
         mbar_wait(bar + (used + i) % ST, ((used + i) / ST) & 1);
     used += groups;
+    const Seg was = sg;                              // merged while the next segment's first groups are on their way
+    const int was_u = u;
+    open();
     // Merge the warps: maxima and sums, then the value sums a piece at a time.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -459,7 +476,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         f[nt][j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - sm_top[nt * 8 + 2 * t + j]) * vrun;
-    float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.head && u != u0 ? 1 : 0)) * kRows * (kRecHead + D);
+    float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (was.head && was_u != u0 ? 1 : 0)) * kRows * (kRecHead + D);
 #pragma unroll
     for (int p0 = 0; p0 < NT * MT; p0 += 2) {
 #pragma unroll
@@ -478,17 +495,17 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         const int nt = (p0 + p) / MT, x = (p0 + p) % MT;
         const int wd = x >> 1, gg = ln >> 2;
         const int dim = (VW >= 4 ? 16 * (gg + 8 * (wd / 4)) + 4 * (wd % 4) : 8 * gg + 4 * wd) + 2 * (x & 1) + (c >> 1);
-        const int row = nt * 8 + 2 * (ln & 3) + (c & 1), r = sg.rt * kRows + row;
+        const int row = nt * 8 + 2 * (ln & 3) + (c & 1), r = was.rt * kRows + row;
         if (r < a.rows) {
           const float M = sm_top[row], sum = sm_top[kRows + row];
-          if (sg.whole) {
-            const int i = r / a.group, hq = sg.kv * a.group + r % a.group;
-            const int64_t at = (a.first_seq + sg.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + dim;
+          if (was.whole) {
+            const int i = r / a.group, hq = was.kv * a.group + r % a.group;
+            const int64_t at = (a.first_seq + was.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + dim;
             const float o = sum == 0.f ? 0.f : val / sum;
             if (OF) static_cast<float*>(a.out)[at] = o;
             else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
             if (a.lse && dim == 0)
-              a.lse[((a.first_seq + sg.b) * a.heads * a.group + hq) * a.nq + i] =
+              a.lse[((a.first_seq + was.b) * a.heads * a.group + hq) * a.nq + i] =
                   sum == 0.f ? -INFINITY : (M - kLift + log2f(sum)) * kLn2;
           } else {
             rec[row * (kRecHead + D) + kRecHead + dim] = val;
@@ -501,7 +518,6 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       }
       __syncthreads();
     }
-    u = next;
   }
 }
 
@@ -620,13 +636,14 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
   const int tile = many ? kChunkRows : rows_of(d, rows, qf || of), row_tiles = (rows + tile - 1) / tile;
   const int unit = many ? kChunkUnit : kUnit;
   // Units of one launch stay below 2^30: batches are cut into slices.
-  const int64_t per_seq = ((table_stride * cache->block + unit - 1) / unit + 1) * cache->heads * row_tiles;
+  const int64_t per_seq = ((table_stride * cache->block + unit - 1) / unit + 1 + kLead) * cache->heads * row_tiles;
   if (per_seq > (1 << 25))
     return fail(TQ_ERR_UNSUPPORTED, "%s: heads x query rows x capacity of one sequence too large", what);
   int64_t slice = (1 << 30) / per_seq;
   if (slice > (many ? kChunkSlice : kC8Slice)) slice = many ? kChunkSlice : kC8Slice;
   AttnArgs a{cache->heads, cache->block, 0, cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
              q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, tile, row_tiles, unit, many ? kChunkMinUnits : kMinUnits,
+             many ? kChunkLead : kLead,
              nullptr, nullptr, table_stride, 0,
              causal ? 1 : 0, window, scale * kLog2e, out, out_batch_stride, out_head_stride, out_row_stride, lse_out,
              reinterpret_cast<float*>(static_cast<char*>(workspace) + kCumBytes), static_cast<int*>(workspace), pipeline_wait_ns(), d_status};

@@ -32,6 +32,7 @@ struct AttnArgs {
   int group, nq, rows;                               // rows = group * nq per KV head, row r: position r / group
   int tile_rows, row_tiles;                          // rows a CTA takes together
   int unit, min_units;                               // keys per unit of the split, units a CTA takes at least
+  int lead;                                          // what a stream costs beside its keys, in units
   const int32_t* lens;                               // of this slice
   const int32_t* table;
   int64_t table_stride;
@@ -74,25 +75,29 @@ __device__ __forceinline__ KeyRange tile_range(const AttnArgs& a, int n, int rt)
   r.units = r.hi > r.lo ? (r.hi + a.unit - 1) / a.unit - r.lo / a.unit : 0;
   return r;
 }
-// Units of one KV head of a sequence.
+// A stream costs its units and a lead (operands, the merge of the warps); a
+// stream without keys costs nothing.
+__device__ __forceinline__ int stream_cost(const AttnArgs& a, const KeyRange& r) { return r.units > 0 ? r.units + a.lead : 0; }
+// Cost of one KV head of a sequence.
 __device__ __forceinline__ int head_units(const AttnArgs& a, int n) {
   int u = 0;
   if (n > 0)
-    for (int rt = 0; rt < a.row_tiles; ++rt) u += tile_range(a, n, rt).units;
+    for (int rt = 0; rt < a.row_tiles; ++rt) u += stream_cost(a, tile_range(a, n, rt));
   return u;
 }
 
-// The units of all (sequence, KV head, row tile) streams, in that order, are
-// dealt to the CTAs in equal contiguous ranges.
+// The costs of all (sequence, KV head, row tile) streams, in that order, are
+// dealt to the CTAs in equal contiguous ranges (a stream's lead comes first).
 __device__ __forceinline__ int units_per_cta(const AttnArgs& a, int total, int grid) {
   return max((total + grid - 1) / grid, a.min_units);
 }
 
 // One stream's part of a CTA's range.
 struct Seg {
-  int b, kv, rt, n, t0, t1;                          // keys [t0, t1); t0 is a multiple of 16
+  int b, kv, rt, n, t0, t1;                          // keys [t0, t1); t0 is a multiple of 16; none where t1 <= t0
   bool whole;                                        // all keys of the stream
   bool head;                                         // the stream's first keys
+  int start, units;                                  // of the whole stream: where its cost begins, its units
 };
 __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, int uend, int* next) {
   Seg s;
@@ -104,17 +109,32 @@ __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, 
   rel -= s.kv * per_head;
   s.rt = 0;
   KeyRange r = tile_range(a, s.n, 0);
-  while (rel >= r.units) {
-    rel -= r.units;
+  while (rel >= stream_cost(a, r)) {
+    rel -= stream_cost(a, r);
     r = tile_range(a, s.n, ++s.rt);
   }
-  const int nu = min(r.units - rel, uend - u);
-  s.head = rel == 0;
-  s.whole = nu == r.units;
-  s.t0 = s.head ? r.lo / 16 * 16 : (r.lo / a.unit + rel) * a.unit;
-  s.t1 = min((r.lo / a.unit + rel + nu) * a.unit, r.hi);
-  *next = u + nu;
+  s.start = u - rel;
+  s.units = r.units;
+  const int take = min(stream_cost(a, r) - rel, uend - u);
+  const int from = max(rel - a.lead, 0), to = rel + take - a.lead;       // units of the stream
+  s.head = from == 0;
+  s.whole = s.head && to == r.units;
+  s.t0 = s.head ? r.lo / 16 * 16 : (r.lo / a.unit + from) * a.unit;
+  s.t1 = to > from ? min((r.lo / a.unit + to) * a.unit, r.hi) : s.t0;
+  *next = u + take;
   return s;
+}
+// The CTAs that take a stream's units, and whether the first of them keeps its record in its second slot: it does
+// where its range holds an earlier stream's end.
+struct Cut {
+  int first, last, slot;
+};
+__device__ __forceinline__ Cut stream_cut(const AttnArgs& a, int start, int units, int per) {
+  Cut c;
+  c.first = (start + a.lead) / per;
+  c.last = (start + a.lead + units - 1) / per;
+  c.slot = start > c.first * per ? 1 : 0;
+  return c;
 }
 
 __device__ __forceinline__ int64_t page_of(const AttnArgs& a, int b, int blk) {
@@ -187,18 +207,17 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
   if (r >= a.rows) return;
   const int c0 = a.cum_out[b], per_head = (a.cum_out[b + 1] - c0) / a.heads;
   const int per = units_per_cta(a, a.cum_out[a.batch], grid);
-  int u0 = c0 + kv * per_head, units = 0;
+  int start = c0 + kv * per_head, units = 0;
   if (per_head > 0) {
-    const int n = seq_len(a, b, false);
-    for (int x = 0; x < rt; ++x) u0 += tile_range(a, n, x).units;
-    units = tile_range(a, n, rt).units;
+    const int len = seq_len(a, b, false);
+    for (int x = 0; x < rt; ++x) start += stream_cost(a, tile_range(a, len, x));
+    units = tile_range(a, len, rt).units;
   }
-  const int first = u0 / per, last = units > 0 ? (u0 + units - 1) / per : first;
-  if (units > 0 && first == last) return;            // one CTA had it all and wrote the rows
-  const int n = units > 0 ? last - first + 1 : 0;
+  const Cut cut = stream_cut(a, start, units, per);
+  if (units > 0 && cut.first == cut.last) return;    // one CTA had it all and wrote the rows
+  const int n = units > 0 ? cut.last - cut.first + 1 : 0;
   const auto record = [&](int k) {
-    const int c = first + k, slot = k == 0 && u0 != c * per ? 1 : 0;
-    return a.rec + ((static_cast<int64_t>(c) * 2 + slot) * a.tile_rows + row) * (kRecHead + D);
+    return a.rec + ((static_cast<int64_t>(cut.first + k) * 2 + (k == 0 ? cut.slot : 0)) * a.tile_rows + row) * (kRecHead + D);
   };
   float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;    // n <= kMaxRecs <= 2 * kCbThreads
   if (tid < n) {
@@ -279,6 +298,7 @@ cudaError_t launch_combine(const AttnArgs& a, int grid, cudaStream_t st) {
 constexpr int kChunkRows = 256;                      // rows a CTA takes together
 constexpr int kChunkUnit = 128;                      // keys per unit
 constexpr int kChunkMinUnits = 4;
+constexpr int kChunkLead = 4;                        // a segment's start and end, in units
 constexpr int kChunkSlice = 256;                     // sequences per launch
 bool chunk_supported(int d, bool f32, int rows);
 size_t chunk_record_bytes(int d);

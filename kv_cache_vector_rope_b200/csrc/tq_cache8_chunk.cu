@@ -252,6 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
     for (int u = u0; alive && u < u1;) {
       int next;
       const Seg sg = seg_at(a, cum, u, u1, &next);
+      if (sg.t1 <= sg.t0) {
+        u = next;
+        continue;
+      }
       const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
       const int r0 = sg.rt * kChunkRows + 128 * q, r = r0 + wr;
       if (r0 >= a.rows) {                            // this query tile has no row
@@ -425,6 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
     for (int u = u0; alive && u < u1;) {
       int next;
       const Seg sg = seg_at(a, cum, u, u1, &next);
+      if (sg.t1 <= sg.t0) {
+        u = next;
+        continue;
+      }
       const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
       for (int j = 0; alive && j < tiles; ++j, ++it) {
         const uint32_t st = it & 1, parity = (it >> 1) & 1;
@@ -504,6 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
       for (int u = u0; alive && u < u1;) {
         int next;
         const Seg sg = seg_at(a, cum, u, u1, &next);
+        if (sg.t1 <= sg.t0) {
+          u = next;
+          continue;
+        }
         const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
         const int nq = __shfl_sync(0xffffffffu, a.rows - sg.rt * kChunkRows > 128 ? 2 : 1, 0);
         const int steps = __shfl_sync(0xffffffffu, tiles, 0);
@@ -550,6 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
       for (int u = u0; alive && u < u1;) {
         int next;
         const Seg sg = seg_at(a, cum, u, u1, &next);
+        if (sg.t1 <= sg.t0) {
+          u = next;
+          continue;
+        }
         const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
         float vref = 0.f;
         // -1: keys the segment does not reach, -2: a page outside the cache.
@@ -652,14 +668,14 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid)
     }
     return;
   }
-  const int cut = (blockIdx.x + 1) * per;
-  if (cut >= total) return;
+  const int border = (blockIdx.x + 1) * per;
+  if (border >= total) return;
   int next;
-  const Seg sg = seg_at(a, a.cum_out, cut, total, &next);
-  const int units = tile_range(a, sg.n, sg.rt).units, u0 = next - units;
-  if (u0 == cut || u0 < static_cast<int>(blockIdx.x) * per) return;   // cut at its start, or cut before as well
-  const int first = blockIdx.x, n = (u0 + units - 1) / per - first + 1;
-  const int slot0 = u0 != first * per ? 1 : 0;
+  const Seg sg = seg_at(a, a.cum_out, border, total, &next);
+  const Cut cut = stream_cut(a, sg.start, sg.units, per);
+  // Not cut (the border is at its start or in its lead), or cut before as well.
+  if (cut.first != static_cast<int>(blockIdx.x) || cut.last == cut.first) return;
+  const int first = cut.first, n = cut.last - cut.first + 1, slot0 = cut.slot;
   for (int row = row0; row < row0 + kMergeRows; ++row) {
     const int r = sg.rt * a.tile_rows + row;
     if (r >= a.rows) return;
