@@ -36,6 +36,7 @@ struct RowsArgs {
 // Threads of a CTA whose warps (G = 32) or all of whose threads take an item.
 __host__ __device__ constexpr int cta_threads(int G) { return G == 32 ? 64 : 256; }
 constexpr int kGroup = 256;                          // G where a CTA takes an item
+constexpr int kWriteCtas = 4, kWriteCtasF32 = 2, kReadCtas = 4;   // such CTAs per SM
 
 __device__ __forceinline__ void report(int32_t* d_status, int bit) {
   if (d_status) atomicOr(d_status, bit);
@@ -200,24 +201,20 @@ __device__ __forceinline__ uint32_t encode4_finite(const float* x, float inv) {
 // looks at each value run.
 constexpr int kKeep = 4;
 template <typename T, bool INT8, int G>
-__global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : sizeof(T) == 2 ? 3 : 2) cache8_write_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : sizeof(T) == 2 ? kWriteCtas : kWriteCtasF32) cache8_write_kernel(RowsArgs a) {
   __shared__ Spans spans;
   __shared__ uint2 red[cta_threads(G) / 32];
   const int gt = threadIdx.x % G;                    // thread of the group
   scan_spans<cta_threads(G)>(a, spans);
   const int units = spans.cum[a.batch], step = gridDim.x * (cta_threads(G) / G), head = blockIdx.y;
   const int per_row = a.d / 8;
-  int u = blockIdx.x * (cta_threads(G) / G) + threadIdx.x / G, b = 0;
+  int u = blockIdx.x * (cta_threads(G) / G) + threadIdx.x / G;
+  int b = u < units ? find_seq(spans.cum, a.batch, u) : 0;
   Unit next;
   if (u < units) next = unit_at(a, spans, u, b);
   for (; u < units; u += step) {
     const Unit it = next;
     if (u + step < units) next = unit_at(a, spans, u + step, b);         // its page is on the way meanwhile
-    if (it.page < 0) {
-      if (gt == 0 && head == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
-      continue;
-    }
-    const int64_t ph = static_cast<int64_t>(it.page) * a.heads + head;
     const int chunks = (it.r1 - it.r0) * per_row;
     const T* x[2];
 #pragma unroll
@@ -233,6 +230,12 @@ __global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : sizeof(T) == 2 ?
 #pragma unroll
       for (int k = 0; k < kKeep; ++k)
         if (gt + k * G < chunks) raw[kv][k].load(where(kv, gt + k * G));
+    // The rows do not wait for the page, which a step's one item has just asked for.
+    if (it.page < 0) {
+      if (gt == 0 && head == 0) report(a.d_status, TQ_DEV_BAD_BLOCK);
+      continue;
+    }
+    const int64_t ph = static_cast<int64_t>(it.page) * a.heads + head;
     float old[2] = {0.f, 0.f};
     if (it.r0 > 0) {
       old[0] = a.scale[0][ph];
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : sizeof(T) == 2 ?
 // for fp32), so that a warp's loads and stores are both contiguous; 4 KB of
 // codes of K and of V are in flight per CTA and pass.
 template <typename T, bool INT8, int G>
-__global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : 4) cache8_read_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : kReadCtas) cache8_read_kernel(RowsArgs a) {
   constexpr int P = 16 / sizeof(T);
   constexpr int kPieces = 32 / P;                    // 32 codes a thread
   using Raw = typename std::conditional<P == 8, uint2, uint32_t>::type;
@@ -341,7 +344,8 @@ __global__ void __launch_bounds__(cta_threads(G), G == 32 ? 1 : 4) cache8_read_k
   scan_spans<cta_threads(G)>(a, spans);
   const int units = spans.cum[a.batch], step = gridDim.x * (cta_threads(G) / G), head = blockIdx.y;
   const int per_row = a.d / P;
-  int u = blockIdx.x * (cta_threads(G) / G) + threadIdx.x / G, b = 0;
+  int u = blockIdx.x * (cta_threads(G) / G) + threadIdx.x / G;
+  int b = u < units ? find_seq(spans.cum, a.batch, u) : 0;
   Unit next;
   if (u < units) next = unit_at(a, spans, u, b);
   for (; u < units; u += step) {
@@ -401,9 +405,11 @@ cudaError_t launch_rows(const tq_cache8* c, tq_dtype dtype, RowsArgs a, int64_t 
   const int32_t *cu = a.cu, *start = a.start, *table = a.table;
   const int per_row = a.d / (WRITE || dtype == TQ_BF16 ? 8 : 4);
   a.row_magic = (1 << 20) / per_row + 1;
-  // A warp per item where the call's sequences bring so few tokens that a warp
-  // holds an item's new rows in registers; else a CTA per item.
-  const bool warps = a.n / batch * (a.d / 8) <= 32 * kKeep;
+  // A warp per item where a warp holds an item's new rows in registers, since blocks are that small or the call's
+  // sequences bring so few tokens; else a CTA per item. (1000 tokens in blocks 
+  // of 16, 20 heads of 64, read back: 4.3 us against 8.3 with a CTA per item.)
+  const int64_t tokens = a.n / batch < c->block ? a.n / batch : c->block;
+  const bool warps = tokens * a.d <= 32 * kKeep * 8;
   for (int64_t b0 = 0; b0 < batch; b0 += kC8Slice) {
     const int64_t nb = batch - b0 < kC8Slice ? batch - b0 : kC8Slice;
     a.batch = static_cast<int>(nb);
@@ -414,7 +420,8 @@ cudaError_t launch_rows(const tq_cache8* c, tq_dtype dtype, RowsArgs a, int64_t 
     // Blocks touched: at most one per token, and two partial ones per sequence beside the full ones.
     const int64_t full = a.n / c->block + 2 * nb, units = a.n < full ? a.n : full;
     const int64_t ctas = warps ? (units + cta_threads(32) / 32 - 1) / (cta_threads(32) / 32) : units;
-    const int64_t most = (148 * 8 + c->heads - 1) / c->heads;
+    // About three waves of CTAs, a few blocks each (at three CTAs per SM a prompt write took 50.4 us, with 1, 2 and 8 waves 67, 52 and 55).
+    const int64_t most = (148 * 12 + c->heads - 1) / c->heads;
     const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(c->heads));
     if (dtype == TQ_F32) {
       if (c->code == TQ_INT8) launch_group<WRITE, float, true>(warps, grid, a, st);

@@ -50,6 +50,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same into fresh sums.
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -134,6 +142,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
   });
   if (blockIdx.x == 0)
     for (int b = tid; b <= a.batch; b += kAtThreads) a.cum_out[b] = cum[b];
+  let_next_start();
   const int total = cum[a.batch];
   const int per = units_per_cta(a, total, gridDim.x);
   const int u0 = min(static_cast<int>(blockIdx.x) * per, total), u1 = min(u0 + per, total);
@@ -327,8 +336,6 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       }
       float s[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-#pragma unroll
       for (int k = 0; k < KS; ++k) {
         const uint32_t w0 = (&kw[0][k / 4].x)[k % 4], w1 = (&kw[1][k / 4].x)[k % 4];
         const uint32_t a0 = two_halves<INT8, false>(w0), a2 = two_halves<INT8, true>(w0);
@@ -340,11 +347,13 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
           if (QF) {
             // Each step's products are added in fp32: the matrix unit's own sums are cut, not rounded.
             const uint2 b2 = kQRegs ? qr[at + (QL - 1) * KS] : sm_q[(at + (QL - 1) * KS) * 32 + lane];
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(x, a0, a1, a2, a3, b2.x, b2.y);
+            float x[4];
+            mma_f16_new(x, a0, a1, a2, a3, b2.x, b2.y);
             mma_f16(x, a0, a1, a2, a3, b.x, b.y);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] += x[e];
+            for (int e = 0; e < 4; ++e) s[nt][e] = k == 0 ? x[e] : s[nt][e] + x[e];
+          } else if (k == 0) {
+            mma_f16_new(s[nt], a0, a1, a2, a3, b.x, b.y);
           } else {
             mma_f16(s[nt], a0, a1, a2, a3, b.x, b.y);
           }
@@ -425,8 +434,8 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if (OF) {
-              float y[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(y, a0, a1, a2, a3, ph1[nt][0], ph1[nt][1]);
+              float y[4];
+              mma_f16_new(y, a0, a1, a2, a3, ph1[nt][0], ph1[nt][1]);
               mma_f16(y, a0, a1, a2, a3, ph0[nt][0], ph0[nt][1]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[nt][2 * x + h][e] += y[e];

@@ -20,6 +20,10 @@ constexpr float kSlack = 8.f;
 constexpr int kRecHead = 4;
 constexpr int kMaxRecs = 2 * kSms;                   // CTAs that may leave records of one stream
 
+// Programmatic launches: a kernel lets the one behind it be set up, and waits for the end of the one before it.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct AttnArgs {
   int heads, block, batch;
   int64_t n_blocks;
@@ -203,6 +207,7 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
   __shared__ float red[2][kCbThreads / 32];
   __shared__ float4 sums[kParts][D / 4];
   const int b = blockIdx.z, stream = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+  wait_before();
   const int kv = stream / a.row_tiles, rt = stream % a.row_tiles, r = rt * a.tile_rows + row;
   if (r >= a.rows) return;
   const int c0 = a.cum_out[b], per_head = (a.cum_out[b + 1] - c0) / a.heads;
@@ -282,13 +287,31 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
         L == 0.f ? -INFINITY : (M - kLift + log2f(L)) * kLn2;
 }
 
+// Launches a kernel that begins while the one before it on the stream ends: its
+// CTAs are set up meanwhile and wait_before() lets them on once that one's
+// results are there.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Rows that one tile of tile_rows can have, for the combine kernel's grid.
 template <int D, bool OF>
 cudaError_t launch_combine(const AttnArgs& a, int grid, cudaStream_t st) {
   const int rows = a.rows < a.tile_rows ? a.rows : a.tile_rows;
-  cache8_combine_kernel<D, OF><<<dim3(a.heads * a.row_tiles, rows, a.batch), kCbThreads, 0, st>>>(a, grid);
+  const cudaError_t e = launch_behind(cache8_combine_kernel<D, OF>, dim3(a.heads * a.row_tiles, rows, a.batch), kCbThreads,
+                                      st, a, grid);
   count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace c8

@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_at, 0);
+  let_next_start();
   const int total = cum[a.batch];
   const int per = units_per_cta(a, total, gridDim.x);
   const int u0 = min(static_cast<int>(blockIdx.x) * per, total), u1 = min(u0 + per, total);
@@ -645,6 +646,7 @@ constexpr int kMergeEmpty = 8, kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = (blockIdx.y * 8 + w) * kMergeRows;
+  wait_before();
   const auto put = [&](int b, int kv, int r, const float* y, float inv, float lse) {
     const int i = r / a.group, hq = kv * a.group + r % a.group;
     const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs;
@@ -715,9 +717,9 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cache8_merge_kernel<D><<<dim3(kSms - 1 + kMergeEmpty, kChunkRows / 8 / kMergeRows), 256, 0, st>>>(a, kSms);
+  e = launch_behind(cache8_merge_kernel<D>, dim3(kSms - 1 + kMergeEmpty, kChunkRows / 8 / kMergeRows), 256, st, a, kSms);
   count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

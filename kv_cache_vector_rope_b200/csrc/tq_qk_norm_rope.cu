@@ -15,6 +15,8 @@
 // once by the warp (fp64 turns pos * base^(-2i/rot) / 2 pi, whose remainder goes
 // through sincospif: far positions lose whole turns only) and stay in registers
 // as products with the weights while the warp walks the token's heads.
+#include <cmath>
+
 #include "tq_device.cuh"
 #include "tq_cache8.h"
 
@@ -37,12 +39,12 @@ struct NormRopeArgs {
   const float* kw;
   float eps;
   const int32_t* pos;
-  double base;
+  double log2_base;
   int32_t* d_status;
   int parts, rows_per_part;                          // a token's rows are dealt to this many warps
 };
 
-constexpr int kNrThreads = 256;
+constexpr int kNrThreads = 256, kNrCtas = 3;         // resident CTAs per SM
 
 // Four values as loaded.
 template <typename T>
@@ -161,7 +163,7 @@ __device__ __forceinline__ void side_rows(const T* src, int hs, T* dst, int ohs,
 }
 
 template <typename T, int LPR>
-__global__ void __launch_bounds__(kNrThreads, 3) qk_norm_rope_kernel(NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrThreads, kNrCtas) qk_norm_rope_kernel(NormRopeArgs a) {
   __shared__ float2 turn[kNrThreads / 32][128];      // (cos, sin) of pair i of each warp's token
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, part_lane = lane & (LPR - 1);
   const int half = a.rot / 2, pass = (a.d - a.rot) / 2;
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kNrThreads, 3) qk_norm_rope_kernel(NormRopeArg
   const bool turned = rope && first;
   __shared__ double freq[128];                       // turns per position of each pair
   for (int i = threadIdx.x; rope && i < half; i += blockDim.x)
-    freq[i] = pow(a.base, -2.0 * i / a.rot) * 0.15915494309189533577;
+    freq[i] = exp2(-2.0 * i / a.rot * a.log2_base) * 0.15915494309189533577;
   __syncthreads();
   const float inv_d = 1.f / a.d;
   const int64_t units = a.n * a.parts;
@@ -229,7 +231,8 @@ cudaError_t launch_norm_rope(NormRopeArgs a, cudaStream_t st) {
   // Small calls take two warps per CTA, so that they reach every SM.
   const int threads = units <= 148 * 8 ? 64 : kNrThreads;
   const int64_t ctas = (units + threads / 32 - 1) / (threads / 32);
-  const unsigned grid = static_cast<unsigned>(ctas < 148 * 8 ? ctas : 148 * 8);
+  const int cap = 148 * (threads == kNrThreads ? kNrCtas : 16);   // as many as are resident at once
+  const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
   switch (lpr) {
     case 1: qk_norm_rope_kernel<T, 1><<<grid, threads, 0, st>>>(a); break;
     case 2: qk_norm_rope_kernel<T, 2><<<grid, threads, 0, st>>>(a); break;
@@ -295,7 +298,7 @@ extern "C" tq_status tq_qk_norm_rope(int32_t d, int32_t rot_dim, int64_t n_token
   const auto head_stride = [&](int i) { return static_cast<int>(sides[i].hs); };
   NormRopeArgs a{d, rot_dim, n_tokens, hq, hkv, q, k, q_token_stride, k_token_stride, head_stride(0), head_stride(1),
                  q_out, k_out, q_out_token_stride, k_out_token_stride, head_stride(2), head_stride(3), q_weight,
-                 k_weight, eps, rope ? positions : nullptr, static_cast<double>(rope_base), d_status, 0, 0};
+                 k_weight, eps, rope ? positions : nullptr, rope ? std::log2(static_cast<double>(rope_base)) : 0.0, d_status, 0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == TQ_F32 ? launch_norm_rope<float>(a, st) : launch_norm_rope<__nv_bfloat16>(a, st);
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "tq_qk_norm_rope launch: %s", cudaGetErrorString(e));
