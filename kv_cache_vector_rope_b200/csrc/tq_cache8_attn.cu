@@ -58,6 +58,21 @@ __device__ __forceinline__ void mma_f16_new(float (&c)[4], uint32_t a0, uint32_t
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// D = A B (+ C) of signed bytes, 16x8x32, in whole numbers.
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8_new(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -82,18 +97,18 @@ struct Plan<256> {
 };
 
 // Dynamic shared memory: the warps' rings first (1024-byte aligned).
-template <int D, int NT, int QL>
+// ROWS: query rows; QN: 8-byte query operands per lane.
+template <int D, int ROWS, int QN>
 struct Smem {
   static constexpr int kHalfStage = 16 * D;          // 16 keys (or values)
   static constexpr int kStage = 2 * kHalfStage;
   static constexpr int kRing = kStage * Plan<D>::kStages;
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kKS = D / 16;
-  // uint2 [NT][QL][kKS][32], the query operands, while keys are walked; float4
+  static constexpr int kRows = ROWS;
+  // uint2 [QN][32], the query operands, while keys are walked; float4
   // [warps][2][32], a piece of the value sums, while the warps are merged.
   static constexpr int kOffQ = kAtWarps * kRing;
   static constexpr int kOffAcc = kOffQ;
-  static constexpr int kQBytes = NT * QL * kKS * 32 * 8, kAccBytes = kAtWarps * 2 * 32 * 16;
+  static constexpr int kQBytes = QN * 32 * 8, kAccBytes = kAtWarps * 2 * 32 * 16;
   static constexpr int kOffM = kOffQ + (kQBytes > kAccBytes ? kQBytes : kAccBytes);
   static constexpr int kOffL = kOffM + 4 * kAtWarps * kRows;
   static constexpr int kOffTop = kOffL + 4 * kAtWarps * kRows;   // float [2][kRows]: merged maximum and sum
@@ -107,18 +122,28 @@ struct Smem {
 // Where byte `at` of a half stage lies: 16-byte chunk c of 128-byte row r sits at chunk c ^ (r % 8).
 __device__ __forceinline__ int swizzled(int at) { return at ^ ((at >> 3) & 0x70); }
 
-// NT: eight-row query tiles a CTA handles together. QF / OF: fp32 queries /
-// outputs, two half limbs each.
-template <int D, bool INT8, int NT, bool QF, bool OF>
+// NT: query tiles a CTA handles together, of eight rows, or of four with two
+// limbs each (QUAD). QF / OF: fp32 queries / outputs, two half limbs each.
+template <int D, bool QUAD, int NT, bool QF>
+struct Tiling {
+  static constexpr int kTile = QUAD ? 4 : 8;         // rows of a tile
+  static constexpr int kCols = QUAD ? 1 : 2;         // rows of a tile that a lane's columns belong to
+  static constexpr int kRows = kTile * NT;
+  static constexpr int kOps = QUAD || !QF ? D / 16 : D / 8;      // query operands per tile: k-steps x limbs (x pairs of limbs)
+  using Plan = Smem<D, kRows, NT * kOps>;
+};
+template <int D, bool INT8, bool QUAD, int NT, bool QF, bool OF>
 __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     cache8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a) {
   constexpr int KC = Plan<D>::kK, KS = KC * 4;       // 16-byte chunks, k-steps of the score product
   constexpr int VW = Plan<D>::kVWords, MT = VW * 2;  // words per value row of a lane, 16-row tiles of the value product
   constexpr int ST = Plan<D>::kStages;
-  constexpr int QL = QF ? 2 : 1;
-  constexpr int kRows = 8 * NT;
-  constexpr bool kQRegs = NT * QL * KS <= 8;         // few enough to hold in registers
-  using L = Smem<D, NT, QL>;
+  static_assert(INT8 || !QUAD, "byte products are for int8 codes");
+  using T = Tiling<D, QUAD, NT, QF>;
+  constexpr int QL = QF ? 2 : 1, QN = T::kOps, NJ = T::kCols, kTile = T::kTile, kRows = T::kRows;
+  constexpr int NE = 2 * NJ;                         // scores of a lane per tile: keys g and g + 8
+  constexpr bool kQRegs = NT * QN <= 8;              // few enough to hold in registers
+  using L = typename T::Plan;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   uint2* sm_q = reinterpret_cast<uint2*>(smem + L::kOffQ);
@@ -194,14 +219,15 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
   while (u < u1) {
     float nx_k = 0.f, nx_v = 0.f;
     __syncthreads();                                 // the last segment's readers of sm_q and sm_row are done
-    // Queries: warp nt prepares the operands of rows 8 nt .. 8 nt + 7; lane (g, t) holds row g's coordinates of its chunks.
+    // Queries: warp nt prepares the operands of tile nt; lane (g, t) holds column g's coordinates of its chunks.
     if (w < NT) {
-      const int r = sg.rt * kRows + w * 8 + g;
+      const int row = w * kTile + (QUAD ? g >> 1 : g), r = sg.rt * kRows + row;
       const bool live = r < a.rows;
       const int i = live ? r / a.group : 0, hq = sg.kv * a.group + (live ? r % a.group : 0);
       const int64_t base = (a.first_seq + sg.b) * a.q_bs + hq * a.q_hs + i * a.q_rs;
       float x[KC][16];
       float amax = 0.f;
+      bool finite = true;
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
         if (live) load_q16<QF>(a.q, base + 16 * (t + 4 * c), x[c]);
@@ -209,13 +235,15 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         for (int e = 0; e < 16; ++e) {
           if (!live) x[c][e] = 0.f;
           amax = fmaxf(amax, fabsf(x[c][e]));
+          finite &= fabsf(x[c][e]) < INFINITY;
         }
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // Times a power of two: the largest coordinate lands in [2^14, 2^15).
+      // Times a power of two: the largest coordinate lands in [2^14, 2^15), or for limbs of bytes in [2^5, 2^6).
+      constexpr int kTop = QUAD ? 5 : 14;
       const int E = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-      const float up = __uint_as_float(static_cast<uint32_t>(14 - min(E, 127) + 127) << 23);
+      const float up = __uint_as_float(static_cast<uint32_t>(kTop - min(E, 127) + 127) << 23);
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -223,23 +251,44 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
           float* y = x[c] + 4 * s;
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] *= up;
-          sm_q[((w * QL + 0) * KS + 4 * c + s) * 32 + lane] = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
-          if (QF) {
+          if constexpr (QUAD) {
+            // y = l0 + l1 / 2^7 + l2 / 2^14 + l3 / 2^21: column g takes limbs g % 2 and 2 + g % 2 of its row.
+            uint32_t limb[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] -= __half2float(__float2half_rn(y[e]));
-            sm_q[((w * QL + QL - 1) * KS + 4 * c + s) * 32 + lane] = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float z = rintf(y[e]);
+                limb[k] |= (static_cast<uint32_t>(static_cast<int>(z)) & 0xffu) << (8 * e);
+                y[e] = (y[e] - z) * 128.f;
+              }
+            uint32_t* to = reinterpret_cast<uint32_t*>(sm_q + (w * QN + 2 * c + (s >> 1)) * 32 + lane) + (s & 1);
+            to[0] = g & 1 ? limb[1] : limb[0];
+            to[KS / 2 * 64] = g & 1 ? limb[3] : limb[2];
+          } else {
+            sm_q[(w * QN + 4 * c + s) * 32 + lane] = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+            if (QF) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] -= __half2float(__float2half_rn(y[e]));
+              sm_q[(w * QN + (QL - 1) * KS + 4 * c + s) * 32 + lane] =
+                  make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+            }
           }
         }
-      if (t == 0) {
+      // Bytes cannot carry an infinity or NaN of q: the score factor does.
+      finite = __shfl_xor_sync(0xffffffffu, finite, 1) && finite;
+      finite = __shfl_xor_sync(0xffffffffu, finite, 2) && finite;
+      if (t == 0 && (!QUAD || !(g & 1))) {
         const int end = live ? row_hi(a, sg.n, i) : 0;
-        sm_cq[w * 8 + g] = a.scale2 / up;
-        sm_hi[w * 8 + g] = end;
-        sm_lo[w * 8 + g] = row_lo(a, end);
+        sm_cq[row] = QUAD && !finite ? __uint_as_float(0x7fffffffu) : a.scale2 / up * (QUAD ? 1.f / 128.f : 1.f);
+        sm_hi[row] = end;
+        sm_lo[row] = row_lo(a, end);
       }
     }
     __syncthreads();
-    float cq[NT][2];
-    int lo[NT][2], hi[NT][2];
+    const auto row_of = [&](int nt, int j) { return nt * kTile + (QUAD ? t : 2 * t + j); };   // of a lane's columns
+    float cq[NT][NJ];
+    int lo[NT][NJ], hi[NT][NJ];
     int lo_max = 0, hi_min = 0x7fffffff;             // keys in [lo_max, hi_min) are seen by every row
     for (int r = 0; r < kRows && sg.rt * kRows + r < a.rows; ++r) {
       lo_max = max(lo_max, sm_lo[r]);
@@ -248,24 +297,27 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {                  // the score columns of this lane are rows 2t and 2t + 1
-        cq[nt][j] = sm_cq[nt * 8 + 2 * t + j];
-        lo[nt][j] = sm_lo[nt * 8 + 2 * t + j];
-        hi[nt][j] = sm_hi[nt * 8 + 2 * t + j];
+      for (int j = 0; j < NJ; ++j) {
+        cq[nt][j] = sm_cq[row_of(nt, j)];
+        lo[nt][j] = sm_lo[row_of(nt, j)];
+        hi[nt][j] = sm_hi[row_of(nt, j)];
       }
-    uint2 qr[kQRegs ? NT * QL * KS : 1];
+    uint2 qr[kQRegs ? NT * QN : 1];
     if (kQRegs) {
 #pragma unroll
-      for (int x = 0; x < NT * QL * KS; ++x) qr[x] = sm_q[x * 32 + lane];
+      for (int x = 0; x < NT * QN; ++x) qr[x] = sm_q[x * 32 + lane];
     }
     float acc[NT][MT][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][NJ], l[NT][NJ];
     float vrun = 1.17549435e-38f;                    // the sums are in units of this value scale
     float vinv = 0.f;                                // 1 / vrun, once a group has set it
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        m[nt][j] = -INFINITY;
+        l[nt][j] = 0.f;
+      }
 #pragma unroll
       for (int x = 0; x < MT; ++x) acc[nt][x][0] = acc[nt][x][1] = acc[nt][x][2] = acc[nt][x][3] = 0.f;
     }
@@ -334,28 +386,53 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
             for (int x = 0; x < VW; ++x) vw[j][x] = 0u;
       }
-      float s[NT][4];
+      float s[NT][NE];
+      if constexpr (QUAD) {
+        int c[NT][2][4];
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint32_t w0 = (&kw[0][k / 4].x)[k % 4], w1 = (&kw[1][k / 4].x)[k % 4];
-        const uint32_t a0 = two_halves<INT8, false>(w0), a2 = two_halves<INT8, true>(w0);
-        const uint32_t a1 = two_halves<INT8, false>(w1), a3 = two_halves<INT8, true>(w1);
+        for (int k = 0; k < KS / 2; ++k) {
+          const uint32_t* w0 = &kw[0][k / 2].x + 2 * (k % 2);
+          const uint32_t* w1 = &kw[1][k / 2].x + 2 * (k % 2);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int at = nt * QL * KS + k;
-          const uint2 b = kQRegs ? qr[at] : sm_q[at * 32 + lane];
-          if (QF) {
-            // Each step's products are added in fp32: the matrix unit's own sums are cut, not rounded.
-            const uint2 b2 = kQRegs ? qr[at + (QL - 1) * KS] : sm_q[(at + (QL - 1) * KS) * 32 + lane];
-            float x[4];
-            mma_f16_new(x, a0, a1, a2, a3, b2.x, b2.y);
-            mma_f16(x, a0, a1, a2, a3, b.x, b.y);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = k == 0 ? x[e] : s[nt][e] + x[e];
-          } else if (k == 0) {
-            mma_f16_new(s[nt], a0, a1, a2, a3, b.x, b.y);
-          } else {
-            mma_f16(s[nt], a0, a1, a2, a3, b.x, b.y);
+            for (int h = 0; h < 2; ++h) {
+              const int at = nt * QN + h * (KS / 2) + k;
+              const uint2 b = kQRegs ? qr[at] : sm_q[at * 32 + lane];
+              if (k == 0) mma_s8_new(c[nt][h], w0[0], w1[0], w0[1], w1[1], b.x, b.y);
+              else mma_s8(c[nt][h], w0[0], w1[0], w0[1], w1[1], b.x, b.y);
+            }
+        }
+        // Of each key the four limbs' sums: exact but for the two conversions (|128 c0 + c1| < 2^29).
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            s[nt][e] = fmaf(static_cast<float>(c[nt][1][2 * e] * 128 + c[nt][1][2 * e + 1]), 1.f / 16384.f,
+                            static_cast<float>(c[nt][0][2 * e] * 128 + c[nt][0][2 * e + 1]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t w0 = (&kw[0][k / 4].x)[k % 4], w1 = (&kw[1][k / 4].x)[k % 4];
+          const uint32_t a0 = two_halves<INT8, false>(w0), a2 = two_halves<INT8, true>(w0);
+          const uint32_t a1 = two_halves<INT8, false>(w1), a3 = two_halves<INT8, true>(w1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int at = nt * QN + k;
+            const uint2 b = kQRegs ? qr[at] : sm_q[at * 32 + lane];
+            if (QF) {
+              // Each step's products are added in fp32: the matrix unit's own sums are cut, not rounded.
+              const uint2 b2 = kQRegs ? qr[at + (QL - 1) * KS] : sm_q[(at + (QL - 1) * KS) * 32 + lane];
+              float x[4];
+              mma_f16_new(x, a0, a1, a2, a3, b2.x, b2.y);
+              mma_f16(x, a0, a1, a2, a3, b.x, b.y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[nt][e] = k == 0 ? x[e] : s[nt][e] + x[e];
+            } else if (k == 0) {
+              mma_f16_new(s[nt], a0, a1, a2, a3, b.x, b.y);
+            } else {
+              mma_f16(s[nt], a0, a1, a2, a3, b.x, b.y);
+            }
           }
         }
       }
@@ -364,13 +441,13 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[nt][e] *= cq[nt][e & 1] * ks;
+        for (int e = 0; e < NE; ++e) {
+          s[nt][e] *= cq[nt][e % NJ] * ks;
           if (!full) {
-            const int key = key0 + g + 8 * (e >> 1);
-            if (key < lo[nt][e & 1] || key >= hi[nt][e & 1]) s[nt][e] = -INFINITY;
+            const int key = key0 + g + 8 * (e / NJ);
+            if (key < lo[nt][e % NJ] || key >= hi[nt][e % NJ]) s[nt][e] = -INFINITY;
           }
-          rise |= s[nt][e] > m[nt][e & 1] + kSlack;
+          rise |= s[nt][e] > m[nt][e % NJ] + kSlack;
         }
       }
       if (__any_sync(0xffffffffu, rise || vs > vrun)) {
@@ -379,10 +456,10 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         vinv = 1.f / vrun;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float f[2];
+          float f[NJ];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float x = fmaxf(s[nt][j], s[nt][j + 2]);
+          for (int j = 0; j < NJ; ++j) {
+            float x = fmaxf(s[nt][j], s[nt][j + NJ]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
             const float mn = fmaxf(m[nt][j], x);
@@ -393,10 +470,8 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
           }
 #pragma unroll
           for (int x = 0; x < MT; ++x) {
-            acc[nt][x][0] *= f[0];
-            acc[nt][x][1] *= f[1];
-            acc[nt][x][2] *= f[0];
-            acc[nt][x][3] *= f[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][x][e] *= f[e % NJ];
           }
         }
       }
@@ -404,22 +479,29 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       uint32_t ph0[NT][2], ph1[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+        float p[NE];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < NE; ++e) {
           // A row that has seen no key yet has m = -inf: its weights are 0, not e^(-inf + inf).
-          p[e] = s[nt][e] == -INFINITY ? 0.f : fast_exp2(s[nt][e] - m[nt][e & 1] + kLift);
-          l[nt][e & 1] += p[e];
+          p[e] = s[nt][e] == -INFINITY ? 0.f : fast_exp2(s[nt][e] - m[nt][e % NJ] + kLift);
+          l[nt][e % NJ] += p[e];
           p[e] *= vr;
         }
-        const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
-        ph0[nt][0] = transpose8(h0);
-        ph0[nt][1] = transpose8(h1);
-        if (OF) {
-          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-          ph1[nt][0] = transpose8(pack_half(p[0] - x.x, p[1] - x.y));
-          ph1[nt][1] = transpose8(pack_half(p[2] - y.x, p[3] - y.y));
+        if constexpr (QUAD) {
+          // A row's two columns: the weight and what its half leaves of it.
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            ph0[nt][e] = transpose8(pack_half(p[e], OF ? p[e] - __half2float(__float2half_rn(p[e])) : 0.f));
+        } else {
+          const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
+          ph0[nt][0] = transpose8(h0);
+          ph0[nt][1] = transpose8(h1);
+          if (OF) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+            ph1[nt][0] = transpose8(pack_half(p[0] - x.x, p[1] - x.y));
+            ph1[nt][1] = transpose8(pack_half(p[2] - y.x, p[3] - y.y));
+          }
         }
       }
 #pragma unroll
@@ -435,8 +517,12 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
           for (int nt = 0; nt < NT; ++nt) {
             if (OF) {
               float y[4];
-              mma_f16_new(y, a0, a1, a2, a3, ph1[nt][0], ph1[nt][1]);
-              mma_f16(y, a0, a1, a2, a3, ph0[nt][0], ph0[nt][1]);
+              if constexpr (QUAD) {
+                mma_f16_new(y, a0, a1, a2, a3, ph0[nt][0], ph0[nt][1]);
+              } else {
+                mma_f16_new(y, a0, a1, a2, a3, ph1[nt][0], ph1[nt][1]);
+                mma_f16(y, a0, a1, a2, a3, ph0[nt][0], ph0[nt][1]);
+              }
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[nt][2 * x + h][e] += y[e];
             } else {
@@ -458,13 +544,13 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         float x = l[nt][j];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (g == 0) {
-          sm_m[w * kRows + nt * 8 + 2 * t + j] = m[nt][j];
-          sm_l[w * kRows + nt * 8 + 2 * t + j] = x;
+          sm_m[w * kRows + row_of(nt, j)] = m[nt][j];
+          sm_l[w * kRows + row_of(nt, j)] = x;
         }
       }
     __syncthreads();
@@ -479,32 +565,40 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       sm_top[kRows + tid] = sum;
     }
     __syncthreads();
-    float f[NT][2];
+    float f[NT][NJ];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        f[nt][j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - sm_top[nt * 8 + 2 * t + j]) * vrun;
+      for (int j = 0; j < NJ; ++j)
+        f[nt][j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - sm_top[row_of(nt, j)]) * vrun;
     float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (was.head && was_u != u0 ? 1 : 0)) * kRows * (kRecHead + D);
+    constexpr int kPieces = 4 / NJ, kVals = 2 * NJ;  // 16-row tiles at a time, and values of a lane in each
+    static_assert(NT * MT % kPieces == 0, "whole pieces");
+    float* sums = reinterpret_cast<float*>(sm_acc);
 #pragma unroll
-    for (int p0 = 0; p0 < NT * MT; p0 += 2) {
+    for (int p0 = 0; p0 < NT * MT; p0 += kPieces) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
+      for (int p = 0; p < kPieces; ++p) {
         const int nt = (p0 + p) / MT, x = (p0 + p) % MT;
-        sm_acc[(w * 2 + p) * 32 + lane] = make_float4(acc[nt][x][0] * f[nt][0], acc[nt][x][1] * f[nt][1],
-                                                      acc[nt][x][2] * f[nt][0], acc[nt][x][3] * f[nt][1]);
+        float* to = sums + ((w * kPieces + p) * 32 + lane) * kVals;
+        if constexpr (QUAD)                          // the two limbs' columns are one row's
+          *reinterpret_cast<float2*>(to) = make_float2((acc[nt][x][0] + acc[nt][x][1]) * f[nt][0],
+                                                       (acc[nt][x][2] + acc[nt][x][3]) * f[nt][0]);
+        else
+          *reinterpret_cast<float4*>(to) = make_float4(acc[nt][x][0] * f[nt][0], acc[nt][x][1] * f[nt][NJ - 1],
+                                                       acc[nt][x][2] * f[nt][0], acc[nt][x][3] * f[nt][NJ - 1]);
       }
       __syncthreads();
       {
-        // One value per thread: coordinate + c / 2, row 2 t' + c % 2.
-        const int p = tid >> 7, ln = (tid & 127) >> 2, c = tid & 3;
+        // One value per thread: coordinate + c / NJ, the c % NJ-th of its lane's rows.
+        const int p = tid / (32 * kVals), ln = tid % (32 * kVals) / kVals, c = tid % kVals;
         float val = 0.f;
 #pragma unroll
-        for (int k = 0; k < kAtWarps; ++k) val += reinterpret_cast<const float*>(sm_acc + (k * 2 + p) * 32 + ln)[c];
+        for (int k = 0; k < kAtWarps; ++k) val += sums[((k * kPieces + p) * 32 + ln) * kVals + c];
         const int nt = (p0 + p) / MT, x = (p0 + p) % MT;
         const int wd = x >> 1, gg = ln >> 2;
-        const int dim = (VW >= 4 ? 16 * (gg + 8 * (wd / 4)) + 4 * (wd % 4) : 8 * gg + 4 * wd) + 2 * (x & 1) + (c >> 1);
-        const int row = nt * 8 + 2 * (ln & 3) + (c & 1), r = was.rt * kRows + row;
+        const int dim = (VW >= 4 ? 16 * (gg + 8 * (wd / 4)) + 4 * (wd % 4) : 8 * gg + 4 * wd) + 2 * (x & 1) + c / NJ;
+        const int row = nt * kTile + (QUAD ? ln & 3 : 2 * (ln & 3) + c % NJ), r = was.rt * kRows + row;
         if (r < a.rows) {
           const float M = sm_top[row], sum = sm_top[kRows + row];
           if (was.whole) {
@@ -554,11 +648,11 @@ tq_status encode_maps(const tq_cache8* c, Maps* m, const char* what) {
   return TQ_OK;
 }
 
-template <int D, bool INT8, int NT, bool QF, bool OF>
+template <int D, bool INT8, bool QUAD, int NT, bool QF, bool OF>
 cudaError_t launch_attn(const Maps& maps, const AttnArgs& a, cudaStream_t st) {
-  constexpr int smem = Smem<D, NT, QF ? 2 : 1>::kBytes;
+  constexpr int smem = Tiling<D, QUAD, NT, QF>::Plan::kBytes;
   static_assert(smem * Plan<D>::kCtas <= 233472 - 1024 * Plan<D>::kCtas, "shared memory plan exceeds an SM's");
-  auto kernel = cache8_attn_kernel<D, INT8, NT, QF, OF>;
+  auto kernel = cache8_attn_kernel<D, INT8, QUAD, NT, QF, OF>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   constexpr int grid = kSms * Plan<D>::kCtas;         // every CTA resident at once
@@ -569,17 +663,32 @@ cudaError_t launch_attn(const Maps& maps, const AttnArgs& a, cudaStream_t st) {
   return e != cudaSuccess ? e : launch_combine<D, OF>(a, grid, st);
 }
 
-template <int D, bool INT8, int NT>
+template <int D, bool INT8, bool QUAD, int NT>
 cudaError_t launch_types(bool qf, bool of, const Maps& m, const AttnArgs& a, cudaStream_t st) {
-  if (qf && of) return launch_attn<D, INT8, NT, true, true>(m, a, st);
-  if (qf) return launch_attn<D, INT8, NT, true, false>(m, a, st);
-  if (of) return launch_attn<D, INT8, NT, false, true>(m, a, st);
-  return launch_attn<D, INT8, NT, false, false>(m, a, st);
+  if (qf && of) return launch_attn<D, INT8, QUAD, NT, true, true>(m, a, st);
+  if (qf) return launch_attn<D, INT8, QUAD, NT, true, false>(m, a, st);
+  if (of) return launch_attn<D, INT8, QUAD, NT, false, true>(m, a, st);
+  return launch_attn<D, INT8, QUAD, NT, false, false>(m, a, st);
 }
 
-// Query rows a CTA takes together: 8, or 16 where a KV head has more and the
-// sums of 16 rows fit the registers (d up to 128, not both fp32).
-int rows_of(int d, int rows, bool f32) { return rows > 8 && d <= 128 && !f32 ? 16 : 8; }
+// Query rows a CTA takes together. Up to eight over int8 codes: 4 or 8, by byte
+// products. Otherwise 8, or 16 where a KV head has more and the sums of 16 rows
+// fit the registers (d up to 128, not fp32).
+bool quad_rows(bool int8, int rows) { return int8 && rows <= 8; }
+int rows_of(int d, int rows, bool f32, bool int8) {
+  if (quad_rows(int8, rows)) return rows <= 4 ? 4 : 8;
+  return rows > 8 && d <= 128 && !f32 ? 16 : 8;
+}
+
+template <int D>
+cudaError_t launch_few(bool int8, int tile, bool qf, bool of, const Maps& m, const AttnArgs& a, cudaStream_t st) {
+  if (quad_rows(int8, a.rows))
+    return tile == 4 ? launch_types<D, true, true, 1>(qf, of, m, a, st) : launch_types<D, true, true, 2>(qf, of, m, a, st);
+  if constexpr (D <= 128)
+    if (tile == 16)                                  // bf16 queries and outputs
+      return int8 ? launch_attn<D, true, false, 2, false, false>(m, a, st) : launch_attn<D, false, false, 2, false, false>(m, a, st);
+  return int8 ? launch_types<D, true, false, 1>(qf, of, m, a, st) : launch_types<D, false, false, 1>(qf, of, m, a, st);
+}
 
 constexpr size_t kCumBytes = (sizeof(int) * (kC8Slice + 1) + 255) / 256 * 256;
 
@@ -642,7 +751,7 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
   if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
   const bool qf = q_dtype == TQ_F32, of = out_dtype == TQ_F32;
   const bool many = chunk_supported(d, qf || of, rows);
-  const int tile = many ? kChunkRows : rows_of(d, rows, qf || of), row_tiles = (rows + tile - 1) / tile;
+  const int tile = many ? kChunkRows : rows_of(d, rows, qf || of, cache->code == TQ_INT8), row_tiles = (rows + tile - 1) / tile;
   const int unit = many ? kChunkUnit : kUnit;
   // Units of one launch stay below 2^30: batches are cut into slices.
   const int64_t per_seq = ((table_stride * cache->block + unit - 1) / unit + 1 + kLead) * cache->heads * row_tiles;
@@ -669,12 +778,10 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
     a.lens = seq_lens + b0;
     a.table = block_table ? block_table + b0 * table_stride : nullptr;
     cudaError_t e;
-#define TQ_C8(D, NT) (i8 ? launch_types<D, true, NT>(qf, of, maps, a, s) : launch_types<D, false, NT>(qf, of, maps, a, s))
     if (many) e = launch_chunk(d, i8, a, s);
-    else if (d == 64) e = tile == 16 ? TQ_C8(64, 2) : TQ_C8(64, 1);
-    else if (d == 128) e = tile == 16 ? TQ_C8(128, 2) : TQ_C8(128, 1);
-    else e = TQ_C8(256, 1);
-#undef TQ_C8
+    else if (d == 64) e = launch_few<64>(i8, tile, qf, of, maps, a, s);
+    else if (d == 128) e = launch_few<128>(i8, tile, qf, of, maps, a, s);
+    else e = launch_few<256>(i8, tile, qf, of, maps, a, s);
     if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
   }
   return TQ_OK;
