@@ -27,6 +27,18 @@
 // into half's range (exact for bf16; fp32 queries and fp32 outputs use two
 // half limbs for q and for p). The contraction index of both products is
 // permuted so that a lane's operands are 16 contiguous bytes of the cache.
+//
+// Up to four rows over int8 codes multiply the bytes as they are (16x8x32): q in
+// units of its power of two is four 7-bit limbs, exact to 2^-27 of the largest
+// coordinate, two limbs of each of the four rows in a tile's eight columns, so a
+// score costs a quarter of the keys' conversions and half the instructions.
+//
+// Bound by instruction issue beside the memory: unpacking 8-bit codes for the
+// matrix unit, softmax and the two products take about 300 issue slots for each
+// 16 keys of a warp. Measured, floor of the cache's bytes in brackets: a step of
+// 8 sequences of 32768 keys, 8 KV heads, 4 rows each, d = 128, 98 us (82); one
+// sequence of 131072 keys 56 us (41); four drafted fp32 rows of 32 ragged
+// sequences, 20 KV heads, d = 64, 80 us (40).
 #include <cuda.h>
 
 #include "tq_cache8_attn.cuh"
@@ -42,7 +54,11 @@ constexpr int kAtWarps = kAtThreads / 32;
 constexpr int kAtGrid = kMaxRecs;                    // at most two CTAs per SM
 constexpr int kUnit = 64;                            // keys per unit of the split
 constexpr int kMinUnits = 2;                         // a CTA takes at least this many units
-constexpr int kLead = 8;                             // a segment's start and merge, in units
+// What a segment's start and merge cost a CTA beside its keys, in units. Four drafted fp32 rows of 32 ragged sequences,
+// 20 KV heads, d = 64: 94 us at 8, 86 at 12, 82 at 16, 83 at 24; 8 heads of d = 128: 54.0 at 8, 53.3 at 12, 57 at 24;
+// 4 heads of d = 256: 72 at 4, 65 at 8, 60 at 14.
+constexpr int lead_of(int d) { return d == 64 ? 16 : d == 128 ? 8 : 14; }
+constexpr int kSlice = 512;                          // sequences of one launch
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -79,21 +95,24 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 // Per head dim: 16-byte chunks a lane reads of each of its two keys, 4-byte
-// words it reads of each of its four values, ring stages per warp and CTAs per
-// SM (three stages of 4 KB for each of 16 warps are 192 KB at d = 128).
+// words it reads of each of its four values, groups in a warp's ring (three of
+// 4 KB for each of 16 warps are 192 KB at d = 128), groups it takes together
+// with one query tile (d = 64: two, which share the wait, the look at the
+// maximum and the value sums: 8 x 32768 keys 69 -> 63 us; with two query tiles
+// their operands no longer fit the registers, 91 -> 100 us) and CTAs per SM.
 template <int D>
 struct Plan;
 template <>
 struct Plan<64> {
-  static constexpr int kK = 1, kVWords = 2, kStages = 6, kCtas = 2;
+  static constexpr int kK = 1, kVWords = 2, kGroups = 6, kPair = 2, kCtas = 2;
 };
 template <>
 struct Plan<128> {
-  static constexpr int kK = 2, kVWords = 4, kStages = 3, kCtas = 2;
+  static constexpr int kK = 2, kVWords = 4, kGroups = 3, kPair = 1, kCtas = 2;
 };
 template <>
 struct Plan<256> {
-  static constexpr int kK = 4, kVWords = 8, kStages = 3, kCtas = 1;
+  static constexpr int kK = 4, kVWords = 8, kGroups = 3, kPair = 1, kCtas = 1;
 };
 
 // Dynamic shared memory: the warps' rings first (1024-byte aligned).
@@ -101,26 +120,42 @@ struct Plan<256> {
 template <int D, int ROWS, int QN>
 struct Smem {
   static constexpr int kHalfStage = 16 * D;          // 16 keys (or values)
-  static constexpr int kStage = 2 * kHalfStage;
-  static constexpr int kRing = kStage * Plan<D>::kStages;
+  static constexpr int kGroup = 2 * kHalfStage;
+  static constexpr int kRing = kGroup * Plan<D>::kGroups;
   static constexpr int kRows = ROWS;
-  // uint2 [QN][32], the query operands, while keys are walked; float4
-  // [warps][2][32], a piece of the value sums, while the warps are merged.
+  // uint2 [2][QN][32], the query operands of this segment and the next; float4
+  // [warps][2][32], a piece of the value sums, over this segment's and what
+  // lies between the two, while the warps are merged.
   static constexpr int kOffQ = kAtWarps * kRing;
-  static constexpr int kOffAcc = kOffQ;
   static constexpr int kQBytes = QN * 32 * 8, kAccBytes = kAtWarps * 2 * 32 * 16;
-  static constexpr int kOffM = kOffQ + (kQBytes > kAccBytes ? kQBytes : kAccBytes);
+  static constexpr int kBetween = kQBytes > kAccBytes ? 0 : kAccBytes - kQBytes;
+  static constexpr int kOffM = kOffQ + 2 * kQBytes + kBetween;
   static constexpr int kOffL = kOffM + 4 * kAtWarps * kRows;
   static constexpr int kOffTop = kOffL + 4 * kAtWarps * kRows;   // float [2][kRows]: merged maximum and sum
-  static constexpr int kOffRow = kOffTop + 8 * kRows;            // per row: score factor, first key, end
-  static constexpr int kOffBar = kOffRow + 12 * kRows;
-  static constexpr int kOffPart = kOffBar + 8 * kAtWarps * Plan<D>::kStages;
+  static constexpr int kOffRow = kOffTop + 8 * kRows;            // [2] per row: score factor, first key, end
+  static constexpr int kOffBar = kOffRow + 24 * kRows;
+  static constexpr int kOffPart = kOffBar + 8 * kAtWarps * Plan<D>::kGroups;
   static constexpr int kOffCum = kOffPart + 4 * kAtWarps;
-  static constexpr int kBytes = kOffCum + 4 * (kC8Slice + 1) + 1024;   // and room to align the base
+  static constexpr int kBytes = kOffCum + 4 * (kSlice + 1) + 1024;   // and room to align the base
 };
 
 // Where byte `at` of a half stage lies: 16-byte chunk c of 128-byte row r sits at chunk c ^ (r % 8).
-__device__ __forceinline__ int swizzled(int at) { return at ^ ((at >> 3) & 0x70); }
+__host__ __device__ constexpr int swizzled(int at) { return at ^ ((at >> 3) & 0x70); }
+// The swizzle is linear in the bits of an offset: from the place of `a` that of a + b, with no bit in common, is one
+// XOR and one addition away. The half stages lie on 1024 bytes.
+__device__ __forceinline__ uint32_t swizzled_on(uint32_t place, int b) {
+  return (place ^ (swizzled(b) & 1023)) + (swizzled(b) & ~1023);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 x;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
+  return x;
+}
 
 // NT: query tiles a CTA handles together, of eight rows, or of four with two
 // limbs each (QUAD). QF / OF: fp32 queries / outputs, two half limbs each.
@@ -137,27 +172,27 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     cache8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a) {
   constexpr int KC = Plan<D>::kK, KS = KC * 4;       // 16-byte chunks, k-steps of the score product
   constexpr int VW = Plan<D>::kVWords, MT = VW * 2;  // words per value row of a lane, 16-row tiles of the value product
-  constexpr int ST = Plan<D>::kStages;
+  constexpr int G = NT == 1 ? Plan<D>::kPair : 1;    // groups a warp takes together
+  constexpr int ST = Plan<D>::kGroups / G;           // such turns in its ring
+  constexpr int kStep = 16 * G * kAtWarps;           // keys the warps take together
   static_assert(INT8 || !QUAD, "byte products are for int8 codes");
   using T = Tiling<D, QUAD, NT, QF>;
   constexpr int QL = QF ? 2 : 1, QN = T::kOps, NJ = T::kCols, kTile = T::kTile, kRows = T::kRows;
   constexpr int NE = 2 * NJ;                         // scores of a lane per tile: keys g and g + 8
   constexpr bool kQRegs = NT * QN <= 8;              // few enough to hold in registers
   using L = typename T::Plan;
+  constexpr int kStage = G * L::kGroup;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-  uint2* sm_q = reinterpret_cast<uint2*>(smem + L::kOffQ);
-  float4* sm_acc = reinterpret_cast<float4*>(smem + L::kOffAcc);
   float* sm_m = reinterpret_cast<float*>(smem + L::kOffM);
   float* sm_l = reinterpret_cast<float*>(smem + L::kOffL);
   float* sm_top = reinterpret_cast<float*>(smem + L::kOffTop);
-  float* sm_cq = reinterpret_cast<float*>(smem + L::kOffRow);
-  int* sm_lo = reinterpret_cast<int*>(sm_cq + kRows);
-  int* sm_hi = sm_lo + kRows;
   int* cum = reinterpret_cast<int*>(smem + L::kOffCum);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   unsigned char* ring = smem + w * L::kRing;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar) + w * ST;
+  const uint32_t k_first = smem_u32(ring) + swizzled(g * D + 16 * t);
+  const uint32_t v_first = smem_u32(ring) + L::kHalfStage + swizzled(2 * t * D + (VW == 2 ? 8 : 16) * g);
   if (lane == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(bar + s, 1);
     mbar_fence_init();
@@ -171,31 +206,40 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
   const int total = cum[a.batch];
   const int per = units_per_cta(a, total, gridDim.x);
   const int u0 = min(static_cast<int>(blockIdx.x) * per, total), u1 = min(u0 + per, total);
-  uint32_t used = 0;                                 // groups this warp's ring has carried
+  int at = 0;                                        // ring stage of the next group
+  uint32_t phase = 0;                                // of stage `at`
   bool dead = false;                                 // a wait gave up
-  // The segment at hand and what this warp has on its way of it: groups k0, k0 + 128, ..., of which `issued` are
-  // being copied. Pages and scales of 32 groups at a time, one group per lane, the next 32 loaded ahead.
+  // The segment at hand and what this warp has on its way of it: `turns` times G groups at k0, k0 + kStep, ..., of
+  // which `issued` are being copied. Pages and scales of 32 groups at a time, one per lane, the next 32 loaded ahead.
   Seg sg{};
-  int u = u0, next = u0, k0 = 0, groups = 0, issued = 0, pg = 0, pg_next = 0;
+  int u = u0, next = u0, k0 = 0, turns = 0, issued = 0, pg = 0, pg_next = 0;
   float sc_k = 0.f, sc_v = 0.f;
-  const auto load_page = [&](int i) {
-    return i < groups ? static_cast<int>(page_of(a, sg.b, (k0 + i * 16 * kAtWarps) / a.block)) : 0;
+  const auto key_of = [&](int x) { return k0 + x / G * kStep + x % G * 16; };
+  const auto load_page = [&](int x) {
+    return key_of(x) < sg.t1 ? static_cast<int>(page_of(a, sg.b, key_of(x) >> a.block_log2)) : -1;
   };
   const auto ok = [&](int page) { return page >= 0 && page < a.n_blocks; };
   const auto load_scale = [&](const float* p, int page) {
     return ok(page) ? p[static_cast<int64_t>(page) * a.heads + sg.kv] : 0.f;
   };
-  const auto issue = [&](int i, int rel) {           // group i = 32 * (batch of pg) + rel
-    const int page = __shfl_sync(0xffffffffu, rel < 32 ? pg : pg_next, rel & 31);
+  const auto step = [&](int& st) { return ++st == ST ? (st = 0, true) : false; };
+  const auto issue = [&](int i, int rel, int st) {   // turn i, whose groups' pages are lanes G rel... of pg, then pg_next
+    int page[G];
+#pragma unroll
+    for (int x = 0; x < G; ++x) page[x] = __shfl_sync(0xffffffffu, G * rel < 32 ? pg : pg_next, (G * rel + x) & 31);
     if (lane == 0) {
-      const int key = k0 + i * 16 * kAtWarps;
-      // A bad page's group is masked; page 0 is copied in its place.
-      const int64_t ph = static_cast<int64_t>(ok(page) ? page : 0) * a.heads + sg.kv;
-      const int row = static_cast<int>((ph * a.block + key % a.block) * D / 128);
-      const int st = (used + i) % ST;
-      mbar_expect_tx(bar + st, L::kStage);
-      tma_load_2d(ring + st * L::kStage, &kmap, bar + st, 0, row);
-      tma_load_2d(ring + st * L::kStage + L::kHalfStage, &vmap, bar + st, 0, row);
+      mbar_expect_tx(bar + st, key_of(G * i + G - 1) < sg.t1 ? kStage : L::kGroup);
+#pragma unroll
+      for (int x = 0; x < G; ++x) {
+        const int key = key_of(G * i + x);
+        if (x > 0 && key >= sg.t1) break;
+        // A bad page's group is masked; page 0 is copied in its place.
+        const int64_t ph = static_cast<int64_t>(ok(page[x]) ? page[x] : 0) * a.heads + sg.kv;
+        const int row = static_cast<int>((ph * a.block + (key & (a.block - 1))) * D / 128);
+        unsigned char* to = ring + st * kStage + x * L::kGroup;
+        tma_load_2d(to, &kmap, bar + st, 0, row);
+        tma_load_2d(to + L::kHalfStage, &vmap, bar + st, 0, row);
+      }
     }
   };
   // The next segment with keys, if the range has one: its first groups set out.
@@ -205,90 +249,104 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       if (sg.t1 > sg.t0) break;
     }
     if (u >= u1) return;
-    k0 = sg.t0 + 16 * w;
-    groups = sg.t1 > k0 ? (sg.t1 - k0 + 16 * kAtWarps - 1) / (16 * kAtWarps) : 0;
+    k0 = sg.t0 + 16 * G * w;
+    turns = sg.t1 > k0 ? (sg.t1 - k0 + kStep - 1) / kStep : 0;
     pg = load_page(lane);
     pg_next = load_page(32 + lane);
     issued = 0;
     if (!dead)
-      for (; issued < ST && issued < groups; ++issued) issue(issued, issued);
+      for (int st = at; issued < ST && issued < turns; ++issued) {
+        issue(issued, issued, st);
+        step(st);
+      }
     sc_k = load_scale(a.ks, pg);
     sc_v = load_scale(a.vs, pg);
   };
-  open();
-  while (u < u1) {
-    float nx_k = 0.f, nx_v = 0.f;
-    __syncthreads();                                 // the last segment's readers of sm_q and sm_row are done
-    // Queries: warp nt prepares the operands of tile nt; lane (g, t) holds column g's coordinates of its chunks.
-    if (w < NT) {
-      const int row = w * kTile + (QUAD ? g >> 1 : g), r = sg.rt * kRows + row;
-      const bool live = r < a.rows;
-      const int i = live ? r / a.group : 0, hq = sg.kv * a.group + (live ? r % a.group : 0);
-      const int64_t base = (a.first_seq + sg.b) * a.q_bs + hq * a.q_hs + i * a.q_rs;
-      float x[KC][16];
-      float amax = 0.f;
-      bool finite = true;
+  // Queries of the segment at hand, for buffer `buf`: the last NT warps, which have the fewest keys, prepare a tile's
+  // operands each; lane (g, t) holds column g's coordinates of its chunks.
+  const auto q_of = [&](int buf) { return reinterpret_cast<uint2*>(smem + L::kOffQ + buf * (L::kQBytes + L::kBetween)); };
+  const auto rows_at = [&](int buf) { return reinterpret_cast<float*>(smem + L::kOffRow) + buf * 3 * kRows; };
+  const auto prepare = [&](int buf) {
+    if (w < kAtWarps - NT) return;
+    uint2* sm_q = q_of(buf);
+    float* sm_cq = rows_at(buf);
+    int* sm_lo = reinterpret_cast<int*>(sm_cq + kRows);
+    int* sm_hi = sm_lo + kRows;
+    const int nt = w - (kAtWarps - NT), row = nt * kTile + (QUAD ? g >> 1 : g), r = sg.rt * kRows + row;
+    const bool live = r < a.rows;
+    const int i = live ? r / a.group : 0, hq = sg.kv * a.group + (live ? r % a.group : 0);
+    const int64_t base = (a.first_seq + sg.b) * a.q_bs + hq * a.q_hs + i * a.q_rs;
+    float x[KC][16];
+    float amax = 0.f;
+    bool finite = true;
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        if (live) load_q16<QF>(a.q, base + 16 * (t + 4 * c), x[c]);
+    for (int c = 0; c < KC; ++c) {
+      if (live) load_q16<QF>(a.q, base + 16 * (t + 4 * c), x[c]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (!live) x[c][e] = 0.f;
-          amax = fmaxf(amax, fabsf(x[c][e]));
-          finite &= fabsf(x[c][e]) < INFINITY;
-        }
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // Times a power of two: the largest coordinate lands in [2^14, 2^15), or for limbs of bytes in [2^5, 2^6).
-      constexpr int kTop = QUAD ? 5 : 14;
-      const int E = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-      const float up = __uint_as_float(static_cast<uint32_t>(kTop - min(E, 127) + 127) << 23);
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          float* y = x[c] + 4 * s;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] *= up;
-          if constexpr (QUAD) {
-            // y = l0 + l1 / 2^7 + l2 / 2^14 + l3 / 2^21: column g takes limbs g % 2 and 2 + g % 2 of its row.
-            uint32_t limb[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float z = rintf(y[e]);
-                limb[k] |= (static_cast<uint32_t>(static_cast<int>(z)) & 0xffu) << (8 * e);
-                y[e] = (y[e] - z) * 128.f;
-              }
-            uint32_t* to = reinterpret_cast<uint32_t*>(sm_q + (w * QN + 2 * c + (s >> 1)) * 32 + lane) + (s & 1);
-            to[0] = g & 1 ? limb[1] : limb[0];
-            to[KS / 2 * 64] = g & 1 ? limb[3] : limb[2];
-          } else {
-            sm_q[(w * QN + 4 * c + s) * 32 + lane] = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
-            if (QF) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] -= __half2float(__float2half_rn(y[e]));
-              sm_q[(w * QN + (QL - 1) * KS + 4 * c + s) * 32 + lane] =
-                  make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
-            }
-          }
-        }
-      // Bytes cannot carry an infinity or NaN of q: the score factor does.
-      finite = __shfl_xor_sync(0xffffffffu, finite, 1) && finite;
-      finite = __shfl_xor_sync(0xffffffffu, finite, 2) && finite;
-      if (t == 0 && (!QUAD || !(g & 1))) {
-        const int end = live ? row_hi(a, sg.n, i) : 0;
-        sm_cq[row] = QUAD && !finite ? __uint_as_float(0x7fffffffu) : a.scale2 / up * (QUAD ? 1.f / 128.f : 1.f);
-        sm_hi[row] = end;
-        sm_lo[row] = row_lo(a, end);
+      for (int e = 0; e < 16; ++e) {
+        if (!live) x[c][e] = 0.f;
+        amax = fmaxf(amax, fabsf(x[c][e]));
+        finite &= fabsf(x[c][e]) < INFINITY;
       }
     }
-    __syncthreads();
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // Times a power of two: the largest coordinate lands in [2^14, 2^15), or for limbs of bytes in [2^5, 2^6).
+    constexpr int kTop = QUAD ? 5 : 14;
+    const int E = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+    const float up = __uint_as_float(static_cast<uint32_t>(kTop - min(E, 127) + 127) << 23);
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        float* y = x[c] + 4 * s;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] *= up;
+        if constexpr (QUAD) {
+          // y = l0 + l1 / 2^7 + l2 / 2^14 + l3 / 2^21: column g takes limbs g % 2 and 2 + g % 2 of its row.
+          uint32_t limb[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float z = rintf(y[e]);
+              limb[k] |= (static_cast<uint32_t>(static_cast<int>(z)) & 0xffu) << (8 * e);
+              y[e] = (y[e] - z) * 128.f;
+            }
+          uint32_t* to = reinterpret_cast<uint32_t*>(sm_q + (nt * QN + 2 * c + (s >> 1)) * 32 + lane) + (s & 1);
+          to[0] = g & 1 ? limb[1] : limb[0];
+          to[KS / 2 * 64] = g & 1 ? limb[3] : limb[2];
+        } else {
+          sm_q[(nt * QN + 4 * c + s) * 32 + lane] = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+          if (QF) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] -= __half2float(__float2half_rn(y[e]));
+            sm_q[(nt * QN + (QL - 1) * KS + 4 * c + s) * 32 + lane] =
+                make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+          }
+        }
+      }
+    // Bytes cannot carry an infinity or NaN of q: the score factor does.
+    finite = __shfl_xor_sync(0xffffffffu, finite, 1) && finite;
+    finite = __shfl_xor_sync(0xffffffffu, finite, 2) && finite;
+    if (t == 0 && (!QUAD || !(g & 1))) {
+      const int end = live ? row_hi(a, sg.n, i) : 0;
+      sm_cq[row] = QUAD && !finite ? __uint_as_float(0x7fffffffu) : a.scale2 / up * (QUAD ? 1.f / 128.f : 1.f);
+      sm_hi[row] = end;
+      sm_lo[row] = row_lo(a, end);
+    }
+  };
+  open();
+  if (u < u1) prepare(0);
+  __syncthreads();
+  for (int buf = 0; u < u1; buf ^= 1) {
+    float nx_k = 0.f, nx_v = 0.f;
+    const uint2* sm_q = q_of(buf);
+    const float* sm_cq = rows_at(buf);
+    const int* sm_lo = reinterpret_cast<const int*>(sm_cq + kRows);
+    const int* sm_hi = sm_lo + kRows;
     const auto row_of = [&](int nt, int j) { return nt * kTile + (QUAD ? t : 2 * t + j); };   // of a lane's columns
     float cq[NT][NJ];
-    int lo[NT][NJ], hi[NT][NJ];
     int lo_max = 0, hi_min = 0x7fffffff;             // keys in [lo_max, hi_min) are seen by every row
     for (int r = 0; r < kRows && sg.rt * kRows + r < a.rows; ++r) {
       lo_max = max(lo_max, sm_lo[r]);
@@ -297,11 +355,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        cq[nt][j] = sm_cq[row_of(nt, j)];
-        lo[nt][j] = sm_lo[row_of(nt, j)];
-        hi[nt][j] = sm_hi[row_of(nt, j)];
-      }
+      for (int j = 0; j < NJ; ++j) cq[nt][j] = sm_cq[row_of(nt, j)];
     uint2 qr[kQRegs ? NT * QN : 1];
     if (kQRegs) {
 #pragma unroll
@@ -321,145 +375,174 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
       for (int x = 0; x < MT; ++x) acc[nt][x][0] = acc[nt][x][1] = acc[nt][x][2] = acc[nt][x][3] = 0.f;
     }
-    for (int i = 0; i < groups; ++i) {
-      const int rel = i & 31;
+    for (int i = 0; i < turns; ++i) {
+      constexpr int kBatch = 32 / G;                 // turns of a batch of pages
+      const int rel = i % kBatch;
       if (rel == 0 && i > 0) {
         pg = pg_next;
         sc_k = nx_k;
         sc_v = nx_v;
-        pg_next = load_page(i + 32 + lane);
+        pg_next = load_page(G * i + 32 + lane);
       }
-      if (rel == 8) {
+      if (rel == kBatch / 4) {
         nx_k = load_scale(a.ks, pg_next);
         nx_v = load_scale(a.vs, pg_next);
       }
-      const int st = (used + i) % ST;
-      if (!dead && !mbar_wait(bar + st, ((used + i) / ST) & 1, a.wait_ns)) {
+      if (!dead && !mbar_wait(bar + at, phase, a.wait_ns)) {
         dead = true;
         if (a.d_status) atomicOr(a.d_status, TQ_DEV_TIMEOUT);
       }
       dead = __any_sync(0xffffffffu, dead);
-      if (dead) break;
-      const int key0 = k0 + i * 16 * kAtWarps;
-      const float ks = __shfl_sync(0xffffffffu, sc_k, rel), vs = __shfl_sync(0xffffffffu, sc_v, rel);
-      const int page = __shfl_sync(0xffffffffu, pg, rel);
-      const unsigned char* kp = ring + st * L::kStage;
-      const unsigned char* vp = kp + L::kHalfStage;
-      uint4 kw[2][KC];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < KC; ++c)
-          kw[h][c] = *reinterpret_cast<const uint4*>(kp + swizzled((g + 8 * h) * D + 16 * (t + 4 * c)));
-      uint32_t vw[4][VW];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = 2 * t + (j & 1) + 8 * (j >> 1);
-        if (VW == 2) {
-          const uint2 x = *reinterpret_cast<const uint2*>(vp + swizzled(row * D + 8 * g));
-          vw[j][0] = x.x;
-          vw[j][1] = x.y;
-        } else {
-#pragma unroll
-          for (int c = 0; c < VW / 4; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(vp + swizzled(row * D + 16 * (g + 8 * c)));
-            vw[j][4 * c] = x.x;
-            vw[j][4 * c + 1] = x.y;
-            vw[j][4 * c + 2] = x.z;
-            vw[j][4 * c + 3] = x.w;
-          }
+      if (dead) {                                    // the copies on their way land before the CTA ends
+        for (; i < issued; ++i) {
+          mbar_wait(bar + at, phase);
+          phase ^= step(at) ? 1u : 0u;
         }
+        break;
       }
-      __syncwarp();                                  // every lane has its operands: the stage is free
-      if (issued < groups) {
-        issue(issued, issued - (i - rel));
-        ++issued;
-      }
-      if (!ok(page)) {
-        if (lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_BLOCK);
-        continue;
-      }
-      if (key0 + 16 > sg.n) {                        // what lies behind the sequence may be any byte
+      const int key0 = k0 + i * kStep;               // group x: 16 keys from key0 + 16 x
+      float ks[G], vs[G];
+      int known[G];                                  // the end of the keys that may be read; 0 with a bad page
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (key0 + 2 * t + (j & 1) + 8 * (j >> 1) >= sg.n)
-#pragma unroll
-            for (int x = 0; x < VW; ++x) vw[j][x] = 0u;
+      for (int x = 0; x < G; ++x) {
+        ks[x] = __shfl_sync(0xffffffffu, sc_k, G * rel + x);
+        vs[x] = __shfl_sync(0xffffffffu, sc_v, G * rel + x);
+        const bool good = ok(__shfl_sync(0xffffffffu, pg, G * rel + x));
+        known[x] = good ? sg.n : 0;
+        if (!good && key0 + 16 * x < sg.t1 && lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_BLOCK);
       }
-      float s[NT][NE];
-      if constexpr (QUAD) {
-        int c[NT][2][4];
+      const uint32_t ka = k_first + at * kStage, va = v_first + at * kStage;
+      uint32_t vw[G][4][VW];
+      const auto values = [&] {                      // then every lane has its operands: the stage is free
 #pragma unroll
-        for (int k = 0; k < KS / 2; ++k) {
-          const uint32_t* w0 = &kw[0][k / 2].x + 2 * (k % 2);
-          const uint32_t* w1 = &kw[1][k / 2].x + 2 * (k % 2);
+        for (int x = 0; x < G; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = (j & 1) + 8 * (j >> 1);
+            uint32_t* to = vw[x][j];
+            if constexpr (VW == 2) {
+              const uint2 y = lds64(swizzled_on(va + x * L::kGroup, row * D));
+              to[0] = y.x;
+              to[1] = y.y;
+            } else {
+#pragma unroll
+              for (int c = 0; c < VW / 4; ++c) {
+                const uint4 y = lds128(swizzled_on(va + x * L::kGroup, row * D + 128 * c));
+                to[4 * c] = y.x;
+                to[4 * c + 1] = y.y;
+                to[4 * c + 2] = y.z;
+                to[4 * c + 3] = y.w;
+              }
+            }
+          }
+        const int freed = at;
+        phase ^= step(at) ? 1u : 0u;
+        __syncwarp();
+        if (issued < turns) {
+          issue(issued, issued - (i - rel), freed);
+          ++issued;
+        }
+#pragma unroll
+        for (int x = 0; x < G; ++x)
+          if (key0 + 16 * x + 16 > known[x]) {       // what lies behind the sequence, or in no page, may be any byte
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (key0 + 16 * x + 2 * t + (j & 1) + 8 * (j >> 1) >= known[x])
+#pragma unroll
+                for (int y = 0; y < VW; ++y) vw[x][j][y] = 0u;
+          }
+      };
+      float s[G][NT][NE];
+#pragma unroll
+      for (int x = 0; x < G; ++x) {
+        uint4 kw[2][KC];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < KC; ++c) kw[h][c] = lds128(swizzled_on(ka + x * L::kGroup, 8 * h * D + 64 * c));
+        if constexpr (QUAD) {
+          int c[NT][2][4];
+#pragma unroll
+          for (int k = 0; k < KS / 2; ++k) {
+            const uint32_t* w0 = &kw[0][k / 2].x + 2 * (k % 2);
+            const uint32_t* w1 = &kw[1][k / 2].x + 2 * (k % 2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int at = nt * QN + h * (KS / 2) + k;
+                const uint2 b = kQRegs ? qr[at] : sm_q[at * 32 + lane];
+                if (k == 0) mma_s8_new(c[nt][h], w0[0], w1[0], w0[1], w1[1], b.x, b.y);
+                else mma_s8(c[nt][h], w0[0], w1[0], w0[1], w1[1], b.x, b.y);
+              }
+          }
+          // Of each key the four limbs' sums: exact but for the two conversions (|128 c0 + c1| < 2^29).
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int at = nt * QN + h * (KS / 2) + k;
+            for (int e = 0; e < 2; ++e)
+              s[x][nt][e] = fmaf(static_cast<float>(c[nt][1][2 * e] * 128 + c[nt][1][2 * e + 1]), 1.f / 16384.f,
+                              static_cast<float>(c[nt][0][2 * e] * 128 + c[nt][0][2 * e + 1]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const uint32_t w0 = (&kw[0][k / 4].x)[k % 4], w1 = (&kw[1][k / 4].x)[k % 4];
+            const uint32_t a0 = two_halves<INT8, false>(w0), a2 = two_halves<INT8, true>(w0);
+            const uint32_t a1 = two_halves<INT8, false>(w1), a3 = two_halves<INT8, true>(w1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int at = nt * QN + k;
               const uint2 b = kQRegs ? qr[at] : sm_q[at * 32 + lane];
-              if (k == 0) mma_s8_new(c[nt][h], w0[0], w1[0], w0[1], w1[1], b.x, b.y);
-              else mma_s8(c[nt][h], w0[0], w1[0], w0[1], w1[1], b.x, b.y);
-            }
-        }
-        // Of each key the four limbs' sums: exact but for the two conversions (|128 c0 + c1| < 2^29).
+              if (QF) {
+                // Each step's products are added in fp32: the matrix unit's own sums are cut, not rounded.
+                const uint2 b2 = kQRegs ? qr[at + (QL - 1) * KS] : sm_q[(at + (QL - 1) * KS) * 32 + lane];
+                float y[4];
+                mma_f16_new(y, a0, a1, a2, a3, b2.x, b2.y);
+                mma_f16(y, a0, a1, a2, a3, b.x, b.y);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            s[nt][e] = fmaf(static_cast<float>(c[nt][1][2 * e] * 128 + c[nt][1][2 * e + 1]), 1.f / 16384.f,
-                            static_cast<float>(c[nt][0][2 * e] * 128 + c[nt][0][2 * e + 1]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint32_t w0 = (&kw[0][k / 4].x)[k % 4], w1 = (&kw[1][k / 4].x)[k % 4];
-          const uint32_t a0 = two_halves<INT8, false>(w0), a2 = two_halves<INT8, true>(w0);
-          const uint32_t a1 = two_halves<INT8, false>(w1), a3 = two_halves<INT8, true>(w1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int at = nt * QN + k;
-            const uint2 b = kQRegs ? qr[at] : sm_q[at * 32 + lane];
-            if (QF) {
-              // Each step's products are added in fp32: the matrix unit's own sums are cut, not rounded.
-              const uint2 b2 = kQRegs ? qr[at + (QL - 1) * KS] : sm_q[(at + (QL - 1) * KS) * 32 + lane];
-              float x[4];
-              mma_f16_new(x, a0, a1, a2, a3, b2.x, b2.y);
-              mma_f16(x, a0, a1, a2, a3, b.x, b.y);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[nt][e] = k == 0 ? x[e] : s[nt][e] + x[e];
-            } else if (k == 0) {
-              mma_f16_new(s[nt], a0, a1, a2, a3, b.x, b.y);
-            } else {
-              mma_f16(s[nt], a0, a1, a2, a3, b.x, b.y);
+                for (int e = 0; e < 4; ++e) s[x][nt][e] = k == 0 ? y[e] : s[x][nt][e] + y[e];
+              } else if (k == 0) {
+                mma_f16_new(s[x][nt], a0, a1, a2, a3, b.x, b.y);
+              } else {
+                mma_f16(s[x][nt], a0, a1, a2, a3, b.x, b.y);
+              }
             }
           }
         }
       }
-      const bool full = key0 >= lo_max && key0 + 16 <= hi_min;
+      values();                                      // behind the scores: the keys' registers are free
       bool rise = false;
+      float vtop = vs[0];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int x = 0; x < G; ++x) {
+        const int key1 = key0 + 16 * x;
+        const bool full = key1 >= lo_max && key1 + 16 <= min(hi_min, known[x]);
+        vtop = fmaxf(vtop, vs[x]);
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-          s[nt][e] *= cq[nt][e % NJ] * ks;
-          if (!full) {
-            const int key = key0 + g + 8 * (e / NJ);
-            if (key < lo[nt][e % NJ] || key >= hi[nt][e % NJ]) s[nt][e] = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < NE; ++e) {
+            s[x][nt][e] *= cq[nt][e % NJ] * ks[x];
+            if (!full) {
+              const int key = key1 + g + 8 * (e / NJ), row = row_of(nt, e % NJ);
+              if (key < sm_lo[row] || key >= min(sm_hi[row], known[x])) s[x][nt][e] = -INFINITY;
+            }
+            rise |= s[x][nt][e] > m[nt][e % NJ] + kSlack;
           }
-          rise |= s[nt][e] > m[nt][e % NJ] + kSlack;
         }
       }
-      if (__any_sync(0xffffffffu, rise || vs > vrun)) {
-        const float fv = vs > vrun ? vrun / vs : 1.f;
-        vrun = fmaxf(vrun, vs);
+      if (__any_sync(0xffffffffu, rise || vtop > vrun)) {
+        const float fv = vtop > vrun ? vrun / vtop : 1.f;
+        vrun = fmaxf(vrun, vtop);
         vinv = 1.f / vrun;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float f[NJ];
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            float x = fmaxf(s[nt][j], s[nt][j + NJ]);
+            float x = fmaxf(s[0][nt][j], s[0][nt][j + NJ]);
+#pragma unroll
+            for (int y = 1; y < G; ++y) x = fmaxf(x, fmaxf(s[y][nt][j], s[y][nt][j + NJ]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
             const float mn = fmaxf(m[nt][j], x);
@@ -475,71 +558,75 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
           }
         }
       }
-      const float vr = vs * vinv;
-      uint32_t ph0[NT][2], ph1[NT][2];
+      uint32_t ph0[G][NT][2], ph1[G][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[NE];
+      for (int x = 0; x < G; ++x) {
+        const float vr = vs[x] * vinv;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-          // A row that has seen no key yet has m = -inf: its weights are 0, not e^(-inf + inf).
-          p[e] = s[nt][e] == -INFINITY ? 0.f : fast_exp2(s[nt][e] - m[nt][e % NJ] + kLift);
-          l[nt][e % NJ] += p[e];
-          p[e] *= vr;
-        }
-        if constexpr (QUAD) {
-          // A row's two columns: the weight and what its half leaves of it.
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[NE];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            ph0[nt][e] = transpose8(pack_half(p[e], OF ? p[e] - __half2float(__float2half_rn(p[e])) : 0.f));
-        } else {
-          const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
-          ph0[nt][0] = transpose8(h0);
-          ph0[nt][1] = transpose8(h1);
-          if (OF) {
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-            ph1[nt][0] = transpose8(pack_half(p[0] - x.x, p[1] - x.y));
-            ph1[nt][1] = transpose8(pack_half(p[2] - y.x, p[3] - y.y));
+          for (int e = 0; e < NE; ++e) {
+            // A row that has seen no key yet has m = -inf: its weights are 0, not e^(-inf + inf).
+            p[e] = s[x][nt][e] == -INFINITY ? 0.f : fast_exp2(s[x][nt][e] - m[nt][e % NJ] + kLift);
+            l[nt][e % NJ] += p[e];
+            p[e] *= vr;
           }
-        }
-      }
+          if constexpr (QUAD) {
+            // A row's two columns: the weight and what its half leaves of it.
 #pragma unroll
-      for (int x = 0; x < VW; ++x) {
-        // Coordinate pairs of two keys side by side: (key 2t, key 2t + 1) per half pair.
-        const uint32_t p0 = __byte_perm(vw[0][x], vw[1][x], 0x5140), p1 = __byte_perm(vw[0][x], vw[1][x], 0x7362);
-        const uint32_t q0 = __byte_perm(vw[2][x], vw[3][x], 0x5140), q1 = __byte_perm(vw[2][x], vw[3][x], 0x7362);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a0 = two_halves<INT8, false>(h ? p1 : p0), a1 = two_halves<INT8, true>(h ? p1 : p0);
-          const uint32_t a2 = two_halves<INT8, false>(h ? q1 : q0), a3 = two_halves<INT8, true>(h ? q1 : q0);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+            for (int e = 0; e < 2; ++e)
+              ph0[x][nt][e] = transpose8(pack_half(p[e], OF ? p[e] - __half2float(__float2half_rn(p[e])) : 0.f));
+          } else {
+            const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
+            ph0[x][nt][0] = transpose8(h0);
+            ph0[x][nt][1] = transpose8(h1);
             if (OF) {
-              float y[4];
-              if constexpr (QUAD) {
-                mma_f16_new(y, a0, a1, a2, a3, ph0[nt][0], ph0[nt][1]);
-              } else {
-                mma_f16_new(y, a0, a1, a2, a3, ph1[nt][0], ph1[nt][1]);
-                mma_f16(y, a0, a1, a2, a3, ph0[nt][0], ph0[nt][1]);
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nt][2 * x + h][e] += y[e];
-            } else {
-              mma_f16(acc[nt][2 * x + h], a0, a1, a2, a3, ph0[nt][0], ph0[nt][1]);
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+              const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+              ph1[x][nt][0] = transpose8(pack_half(p[0] - y.x, p[1] - y.y));
+              ph1[x][nt][1] = transpose8(pack_half(p[2] - z.x, p[3] - z.y));
             }
           }
         }
       }
+#pragma unroll
+      for (int c = 0; c < VW; ++c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float y[NT][4];
+#pragma unroll
+          for (int x = 0; x < G; ++x) {
+            // Coordinate pairs of two keys side by side: (key 2t, key 2t + 1) per half pair.
+            const uint32_t p = __byte_perm(vw[x][0][c], vw[x][1][c], h ? 0x7362 : 0x5140);
+            const uint32_t q = __byte_perm(vw[x][2][c], vw[x][3][c], h ? 0x7362 : 0x5140);
+            const uint32_t a0 = two_halves<INT8, false>(p), a1 = two_halves<INT8, true>(p);
+            const uint32_t a2 = two_halves<INT8, false>(q), a3 = two_halves<INT8, true>(q);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (OF) {
+                const uint32_t(&first)[2] = QUAD ? ph0[x][nt] : ph1[x][nt];
+                if (x == 0) mma_f16_new(y[nt], a0, a1, a2, a3, first[0], first[1]);
+                else mma_f16(y[nt], a0, a1, a2, a3, first[0], first[1]);
+                if (!QUAD) mma_f16(y[nt], a0, a1, a2, a3, ph0[x][nt][0], ph0[x][nt][1]);
+              } else {
+                mma_f16(acc[nt][2 * c + h], a0, a1, a2, a3, ph0[x][nt][0], ph0[x][nt][1]);
+              }
+            }
+          }
+          if (OF) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[nt][2 * c + h][e] += y[nt][e];
+          }
+        }
+      }
     }
-    // Copies that a given-up wait left behind land before the ring is used again or the CTA ends.
-    if (dead)
-      for (int i = issued > ST ? issued - ST : 0; i < issued; ++i)
-        mbar_wait(bar + (used + i) % ST, ((used + i) / ST) & 1);
-    used += groups;
     const Seg was = sg;                              // merged while the next segment's first groups are on their way
     const int was_u = u;
     open();
+    if (u < u1) prepare(buf ^ 1);
     // Merge the warps: maxima and sums, then the value sums a piece at a time.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -574,7 +661,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (was.head && was_u != u0 ? 1 : 0)) * kRows * (kRecHead + D);
     constexpr int kPieces = 4 / NJ, kVals = 2 * NJ;  // 16-row tiles at a time, and values of a lane in each
     static_assert(NT * MT % kPieces == 0, "whole pieces");
-    float* sums = reinterpret_cast<float*>(sm_acc);
+    float* sums = reinterpret_cast<float*>(smem + L::kOffQ + buf * L::kQBytes);
 #pragma unroll
     for (int p0 = 0; p0 < NT * MT; p0 += kPieces) {
 #pragma unroll
@@ -671,26 +758,38 @@ cudaError_t launch_types(bool qf, bool of, const Maps& m, const AttnArgs& a, cud
   return launch_attn<D, INT8, QUAD, NT, false, false>(m, a, st);
 }
 
-// Query rows a CTA takes together. Up to eight over int8 codes: 4 or 8, by byte
-// products. Otherwise 8, or 16 where a KV head has more and the sums of 16 rows
-// fit the registers (d up to 128, not fp32).
-bool quad_rows(bool int8, int rows) { return int8 && rows <= 8; }
-int rows_of(int d, int rows, bool f32, bool int8) {
-  if (quad_rows(int8, rows)) return rows <= 4 ? 4 : 8;
-  return rows > 8 && d <= 128 && !f32 ? 16 : 8;
+// Query rows a CTA takes together: 16 where a KV head has more than 8 and their
+// sums fit the registers (d up to 128, not fp32; twelve rows over 8 x 32768 keys,
+// d = 128: 143 us, by eights 2 x 98). Over int8 codes up to four rows are one
+// tile of byte products with two of q's limbs a column: one step of a decode of
+// 8 x 32768 keys took, against the half products' eight columns, 66 against 75 us
+// (d = 64), 100 against 102 (d = 256), and with fp32 queries 101 against 116 (d =
+// 128); with bf16 queries at d = 128 102 against 96, so there they stay away, as
+// they do from 5 to 8 rows (two such tiles: 125 against 98 us).
+int rows_of(int d, int rows, bool qf, bool of, bool int8) {
+  if (int8 && rows <= 4 && (qf || d != 128)) return 4;
+  return rows > 8 && d <= 128 && !qf && !of ? 16 : 8;
 }
 
 template <int D>
 cudaError_t launch_few(bool int8, int tile, bool qf, bool of, const Maps& m, const AttnArgs& a, cudaStream_t st) {
-  if (quad_rows(int8, a.rows))
-    return tile == 4 ? launch_types<D, true, true, 1>(qf, of, m, a, st) : launch_types<D, true, true, 2>(qf, of, m, a, st);
+  if (tile == 4) {
+    if constexpr (D != 128) return launch_types<D, true, true, 1>(qf, of, m, a, st);
+    else return of ? launch_attn<D, true, true, 1, true, true>(m, a, st) : launch_attn<D, true, true, 1, true, false>(m, a, st);
+  }
   if constexpr (D <= 128)
     if (tile == 16)                                  // bf16 queries and outputs
       return int8 ? launch_attn<D, true, false, 2, false, false>(m, a, st) : launch_attn<D, false, false, 2, false, false>(m, a, st);
   return int8 ? launch_types<D, true, false, 1>(qf, of, m, a, st) : launch_types<D, false, false, 1>(qf, of, m, a, st);
 }
 
-constexpr size_t kCumBytes = (sizeof(int) * (kC8Slice + 1) + 255) / 256 * 256;
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+constexpr size_t kCumBytes = (sizeof(int) * (kSlice + 1) + 255) / 256 * 256;
 
 size_t attn_workspace(int d, int64_t rows) {
   const size_t few = sizeof(float) * kAtGrid * 2 * 16 * static_cast<size_t>(kRecHead + d);
@@ -751,17 +850,17 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
   if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
   const bool qf = q_dtype == TQ_F32, of = out_dtype == TQ_F32;
   const bool many = chunk_supported(d, qf || of, rows);
-  const int tile = many ? kChunkRows : rows_of(d, rows, qf || of, cache->code == TQ_INT8), row_tiles = (rows + tile - 1) / tile;
-  const int unit = many ? kChunkUnit : kUnit;
+  const int tile = many ? kChunkRows : rows_of(d, rows, qf, of, cache->code == TQ_INT8), row_tiles = (rows + tile - 1) / tile;
+  const int unit = many ? kChunkUnit : kUnit, lead = many ? kChunkLead : lead_of(d);
   // Units of one launch stay below 2^30: batches are cut into slices.
-  const int64_t per_seq = ((table_stride * cache->block + unit - 1) / unit + 1 + kLead) * cache->heads * row_tiles;
+  const int64_t per_seq = ((table_stride * cache->block + unit - 1) / unit + 1 + lead) * cache->heads * row_tiles;
   if (per_seq > (1 << 25))
     return fail(TQ_ERR_UNSUPPORTED, "%s: heads x query rows x capacity of one sequence too large", what);
   int64_t slice = (1 << 30) / per_seq;
-  if (slice > (many ? kChunkSlice : kC8Slice)) slice = many ? kChunkSlice : kC8Slice;
-  AttnArgs a{cache->heads, cache->block, 0, cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
+  if (slice > (many ? kChunkSlice : kSlice)) slice = many ? kChunkSlice : kSlice;
+  AttnArgs a{cache->heads, cache->block, 0, log2_of(cache->block), cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
              q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, tile, row_tiles, unit, many ? kChunkMinUnits : kMinUnits,
-             many ? kChunkLead : kLead,
+             lead,
              nullptr, nullptr, table_stride, 0,
              causal ? 1 : 0, window, scale * kLog2e, out, out_batch_stride, out_head_stride, out_row_stride, lse_out,
              reinterpret_cast<float*>(static_cast<char*>(workspace) + kCumBytes), static_cast<int*>(workspace), pipeline_wait_ns(), d_status};

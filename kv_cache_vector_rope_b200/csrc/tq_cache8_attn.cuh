@@ -26,6 +26,7 @@ __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wai
 
 struct AttnArgs {
   int heads, block, batch;
+  int block_log2;
   int64_t n_blocks;
   const uint8_t* k;
   const uint8_t* v;

@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         const auto load_page = [&](int j) {
           const int key = key0 + j * kTile + 16 * lane;
           if (j >= tiles || lane >= 8 || key < sg.t0 || key >= sg.t1) return -1;
-          const int64_t p = page_of(a, sg.b, key / a.block);
+          const int64_t p = page_of(a, sg.b, key >> a.block_log2);
           return p >= 0 && p < a.n_blocks ? static_cast<int>(p) : -2;
         };
         const auto load_scale = [&](const float* p, int page) {
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           if (!(kref > 0.f)) kref = 1.f;             // no page at all
           vref = fmaxf(vref, dev::warp_max(vs));
           const float vr = vref > 0.f ? vref : 1.17549435e-38f;
-          const int64_t at = ((static_cast<int64_t>(page) * a.heads + sg.kv) * a.block + (key0 + j * kTile + 16 * lane) % a.block) * D;
+          const int64_t at = ((static_cast<int64_t>(page) * a.heads + sg.kv) * a.block + ((key0 + j * kTile + 16 * lane) & (a.block - 1))) * D;
           const uint32_t sum = __popc(loaded) * bytes;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
