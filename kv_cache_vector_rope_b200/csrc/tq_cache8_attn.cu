@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     int* sm_hi = sm_lo + kRows;
     const int nt = w - (kAtWarps - NT), row = nt * kTile + (QUAD ? g >> 1 : g), r = sg.rt * kRows + row;
     const bool live = r < a.rows;
-    const int i = live ? r / a.group : 0, hq = sg.kv * a.group + (live ? r % a.group : 0);
+    const int i = live ? a.group_div.of(r) : 0, hq = sg.kv * a.group + (live ? r - i * a.group : 0);
     const int64_t base = (a.first_seq + sg.b) * a.q_bs + hq * a.q_hs + i * a.q_rs;
     float x[KC][16];
     float amax = 0.f;
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         if (r < a.rows) {
           const float M = sm_top[row], sum = sm_top[kRows + row];
           if (was.whole) {
-            const int i = r / a.group, hq = was.kv * a.group + r % a.group;
+            const int i = a.group_div.of(r), hq = was.kv * a.group + r - i * a.group;
             const int64_t at = (a.first_seq + was.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + dim;
             const float o = sum == 0.f ? 0.f : val / sum;
             if (OF) static_cast<float*>(a.out)[at] = o;
@@ -858,8 +858,8 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
     return fail(TQ_ERR_UNSUPPORTED, "%s: heads x query rows x capacity of one sequence too large", what);
   int64_t slice = (1 << 30) / per_seq;
   if (slice > (many ? kChunkSlice : kSlice)) slice = many ? kChunkSlice : kSlice;
-  AttnArgs a{cache->heads, cache->block, 0, log2_of(cache->block), cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
-             q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, tile, row_tiles, unit, many ? kChunkMinUnits : kMinUnits,
+  AttnArgs a{Div(cache->heads), Div(group), Div(row_tiles), cache->heads, cache->block, 0, log2_of(cache->block), cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
+             q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, tile, row_tiles, log2_of(unit), many ? kChunkMinUnits : kMinUnits,
              lead,
              nullptr, nullptr, table_stride, 0,
              causal ? 1 : 0, window, scale * kLog2e, out, out_batch_stride, out_head_stride, out_row_stride, lse_out,

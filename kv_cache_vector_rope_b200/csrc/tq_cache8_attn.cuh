@@ -24,7 +24,23 @@ constexpr int kMaxRecs = 2 * kSms;                   // CTAs that may leave reco
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// x / d for 0 <= x < 2^31 by a product and a shift (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994): the walk over a sequence's row tiles is a chain of them.
+struct Div {
+  int d;
+  uint32_t mul;
+  int shift;
+  explicit Div(int d_) : d(d_), shift(0) {
+    while ((1ll << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - static_cast<uint64_t>(d))) / static_cast<uint64_t>(d) + 1);
+  }
+  __device__ __forceinline__ int of(int x) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(x), mul) + static_cast<uint32_t>(x)) >> shift);
+  }
+};
+
 struct AttnArgs {
+  Div heads_div, group_div, tiles_div;               // of heads, group and row_tiles
   int heads, block, batch;
   int block_log2;
   int64_t n_blocks;
@@ -36,7 +52,7 @@ struct AttnArgs {
   int64_t q_bs, q_hs, q_rs;
   int group, nq, rows;                               // rows = group * nq per KV head, row r: position r / group
   int tile_rows, row_tiles;                          // rows a CTA takes together
-  int unit, min_units;                               // keys per unit of the split, units a CTA takes at least
+  int unit_log2, min_units;                          // keys per unit of the split, units a CTA takes at least
   int lead;                                          // what a stream costs beside its keys, in units
   const int32_t* lens;                               // of this slice
   const int32_t* table;
@@ -68,16 +84,16 @@ __device__ __forceinline__ int row_hi(const AttnArgs& a, int n, int i) { return 
 __device__ __forceinline__ int row_lo(const AttnArgs& a, int hi) { return a.window > 0 ? max(0, hi - a.window) : 0; }
 
 // First key and end of what the rows of row tile rt see together, and how many
-// units of the split that is (units start at multiples of a.unit).
+// units of the split that is (units start at multiples of their size).
 struct KeyRange {
   int lo, hi, units;
 };
 __device__ __forceinline__ KeyRange tile_range(const AttnArgs& a, int n, int rt) {
   KeyRange r;
   const int r0 = rt * a.tile_rows, r1 = min(a.rows, r0 + a.tile_rows) - 1;
-  r.hi = row_hi(a, n, r1 / a.group);
-  r.lo = row_lo(a, row_hi(a, n, r0 / a.group));
-  r.units = r.hi > r.lo ? (r.hi + a.unit - 1) / a.unit - r.lo / a.unit : 0;
+  r.hi = row_hi(a, n, a.group_div.of(r1));
+  r.lo = row_lo(a, row_hi(a, n, a.group_div.of(r0)));
+  r.units = r.hi > r.lo ? ((r.hi + (1 << a.unit_log2) - 1) >> a.unit_log2) - (r.lo >> a.unit_log2) : 0;
   return r;
 }
 // A stream costs its units and a lead (operands, the merge of the warps); a
@@ -108,7 +124,7 @@ __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, 
   Seg s;
   s.b = find_seq(cum, a.batch, u);
   s.n = seq_len(a, s.b, false);
-  const int per_head = (cum[s.b + 1] - cum[s.b]) / a.heads;
+  const int per_head = a.heads_div.of(cum[s.b + 1] - cum[s.b]);
   int rel = u - cum[s.b];
   s.kv = rel / per_head;
   rel -= s.kv * per_head;
@@ -124,8 +140,8 @@ __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, 
   const int from = max(rel - a.lead, 0), to = rel + take - a.lead;       // units of the stream
   s.head = from == 0;
   s.whole = s.head && to == r.units;
-  s.t0 = s.head ? r.lo / 16 * 16 : (r.lo / a.unit + from) * a.unit;
-  s.t1 = to > from ? min((r.lo / a.unit + to) * a.unit, r.hi) : s.t0;
+  s.t0 = s.head ? r.lo / 16 * 16 : ((r.lo >> a.unit_log2) + from) << a.unit_log2;
+  s.t1 = to > from ? min(((r.lo >> a.unit_log2) + to) << a.unit_log2, r.hi) : s.t0;
   *next = u + take;
   return s;
 }
@@ -209,9 +225,9 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
   __shared__ float4 sums[kParts][D / 4];
   const int b = blockIdx.z, stream = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
   wait_before();
-  const int kv = stream / a.row_tiles, rt = stream % a.row_tiles, r = rt * a.tile_rows + row;
+  const int kv = a.tiles_div.of(stream), rt = stream - kv * a.row_tiles, r = rt * a.tile_rows + row;
   if (r >= a.rows) return;
-  const int c0 = a.cum_out[b], per_head = (a.cum_out[b + 1] - c0) / a.heads;
+  const int c0 = a.cum_out[b], per_head = a.heads_div.of(a.cum_out[b + 1] - c0);
   const int per = units_per_cta(a, a.cum_out[a.batch], grid);
   int start = c0 + kv * per_head, units = 0;
   if (per_head > 0) {
@@ -274,7 +290,7 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
     sum.z += y.z;
     sum.w += y.w;
   }
-  const int i = r / a.group, hq = kv * a.group + r % a.group;
+  const int i = a.group_div.of(r), hq = kv * a.group + r - i * a.group;
   const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs + 4 * x;
   const float o[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll

@@ -265,43 +265,42 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         continue;
       }
       const bool live = r < a.rows;
-      const int i = live ? r / a.group : 0, hq = sg.kv * a.group + (live ? r % a.group : 0);
+      const int i = live ? a.group_div.of(r) : 0, hq = sg.kv * a.group + (live ? r - i * a.group : 0);
       float cq;
       {
-        const int64_t at = (a.first_seq + sg.b) * a.q_bs + hq * a.q_hs + i * a.q_rs;
-        float amax = 0.f;
-        if (live)
-#pragma unroll 2
-          for (int c = 0; c < D / 16; ++c) {
-            float x[16];
-            load_q16<false>(a.q, at + 16 * c, x);
+        // The row's halves of words are bf16: read once, all loads in flight, the maximum by its magnitude bits.
+        const uint4* from = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                           (a.first_seq + sg.b) * a.q_bs + hq * a.q_hs + i * a.q_rs);
+        uint4 raw[D / 8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-          }
-        const int E = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+        for (int c = 0; c < D / 8; ++c) raw[c] = live ? from[c] : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t most = 0u;                          // two 16-bit maxima
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          most = __vmaxu2(most, __vmaxu2(__vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu),
+                                         __vmaxu2(raw[c].z & 0x7fff7fffu, raw[c].w & 0x7fff7fffu)));
+        }
+        const int E = max(static_cast<int>(max(most >> 16, most & 0xffffu) >> 7) - 127, -100);
         float up = __uint_as_float(static_cast<uint32_t>(14 - min(E, 127) + 127) << 23);
         cq = fabsf(a.scale2) / up;
         if (a.scale2 < 0.f) up = -up;                // the factor of the scores stays positive
         const uint32_t row = base + L::kOffQ + q * L::kTileBytes + wr * 128;
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          float x[16];
-          if (live) load_q16<false>(a.q, at + 16 * c, x);
-          uint32_t h[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = live ? pack_half(x[2 * e] * up, x[2 * e + 1] * up) : 0u;
-          const uint32_t to = row + (c >> 2) * (128 * 128);
-          const int c0 = (c & 3) * 2;
-          sts128(to + ((c0 ^ (wr & 7)) << 4), h[0], h[1], h[2], h[3]);
-          sts128(to + (((c0 + 1) ^ (wr & 7)) << 4), h[4], h[5], h[6], h[7]);
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[e] = pack_half(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up);
+          sts128(row + (c >> 3) * (128 * 128) + (((c & 7) ^ (wr & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
         fence_proxy_async_smem();
         arrive(kQFull + q);
       }
       const int hi = live ? row_hi(a, sg.n, i) : 0, lo = row_lo(a, hi);
       // Keys in [lo_max, hi_min) are seen by every row of the tile.
-      const int hi_min = row_hi(a, sg.n, r0 / a.group);
-      const int lo_max = row_lo(a, row_hi(a, sg.n, min(r0 + 127, a.rows - 1) / a.group));
+      const int hi_min = row_hi(a, sg.n, a.group_div.of(r0));
+      const int lo_max = row_lo(a, row_hi(a, sg.n, a.group_div.of(min(r0 + 127, a.rows - 1))));
       float m = -INFINITY, l = 0.f, vrun = 0.f;
       for (int j = 0; j < 2 * tiles; ++j) {          // halves of 64 keys
         const int half = j & 1, k0 = key0 + j * 64;
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         const int left = sg.n - (key0 + j * kTile);  // what lies behind the sequence may be any byte
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          alive = __all_sync(0xffffffffu, wait(kRawFull + kv, it) && wait((kv ? kVEmpty : kKEmpty) + st, parity ^ 1));
+          alive = __all_sync(0xffffffffu, wait(kRawFull + kv, it));
           if (!alive) break;
           const TileInfo& inf = info[it & 3];
           const float* ratios = kv ? inf.rv : inf.rk;
@@ -454,6 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           uint4 codes[kPer];
 #pragma unroll
           for (int x = 0; x < kPer; ++x) codes[x] = raw[x * 128];
+          arrive(kRawEmpty + kv);                    // the next tile's codes come while these are converted
+          alive = __all_sync(0xffffffffu, wait((kv ? kVEmpty : kKEmpty) + st, parity ^ 1));
+          if (!alive) break;
 #pragma unroll
           for (int x = 0; x < kPer; ++x) {
             const int group = (x * kStepRows + row) >> 4;
@@ -465,10 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar + kRawEmpty + kv);
-            mbar_arrive(bar + (kv ? kVFull : kKFull) + st);
-          }
+          if (lane == 0) mbar_arrive(bar + (kv ? kVFull : kKFull) + st);
         }
       }
       u = next;
@@ -637,18 +636,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
   if (w == 12) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Merges the records of the streams that the CTAs' ranges cut, a warp per row
-// and four rows per warp, one after another.
+// Merges the records of the streams that the CTAs' ranges cut, a warp for
+// four rows side by side.
 // Block x < grid - 1 looks at the cut between CTAs x and x + 1 and takes the
 // stream it runs through, if it is that stream's first cut; the blocks behind
 // write the rows of streams with no key at all.
-constexpr int kMergeEmpty = 8, kMergeRows = 4;
+constexpr int kMergeEmpty = 8, kMergeRows = 4;       // lanes 8 x + k: kMergeRows x 8 of a warp
 template <int D>
 __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = (blockIdx.y * 8 + w) * kMergeRows;
   wait_before();
   const auto put = [&](int b, int kv, int r, const float* y, float inv, float lse) {
-    const int i = r / a.group, hq = kv * a.group + r % a.group;
+    const int i = a.group_div.of(r), hq = kv * a.group + r - i * a.group;
     const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs;
     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at + lane * (D / 32);
 #pragma unroll
@@ -660,12 +659,16 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid)
   if (static_cast<int>(blockIdx.x) >= grid - 1) {
     for (int b = blockIdx.x - (grid - 1); b < a.batch; b += kMergeEmpty) {
       const int n = seq_len(a, b, false);
-      for (int rt = 0; rt < a.row_tiles; ++rt) {
-        if (n > 0 && tile_range(a, n, rt).units > 0) continue;
-        const float y[D / 32] = {};
-        for (int row = row0; row < row0 + kMergeRows; ++row)
-          if (rt * a.tile_rows + row < a.rows)
-            for (int kv = 0; kv < a.heads; ++kv) put(b, kv, rt * a.tile_rows + row, y, 0.f, -INFINITY);
+      for (int rt0 = 0; rt0 < a.row_tiles; rt0 += 32) {
+        const int mine = rt0 + lane;                 // a row tile per lane is looked at
+        uint32_t none = __ballot_sync(0xffffffffu, mine < a.row_tiles && !(n > 0 && tile_range(a, n, mine).units > 0));
+        for (; none; none &= none - 1) {
+          const int rt = rt0 + __ffs(none) - 1;
+          const float y[D / 32] = {};
+          for (int row = row0; row < row0 + kMergeRows; ++row)
+            if (rt * a.tile_rows + row < a.rows)
+              for (int kv = 0; kv < a.heads; ++kv) put(b, kv, rt * a.tile_rows + row, y, 0.f, -INFINITY);
+        }
       }
     }
     return;
@@ -678,32 +681,45 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid)
   // Not cut (the border is at its start or in its lead), or cut before as well.
   if (cut.first != static_cast<int>(blockIdx.x) || cut.last == cut.first) return;
   const int first = cut.first, n = cut.last - cut.first + 1, slot0 = cut.slot;
-  for (int row = row0; row < row0 + kMergeRows; ++row) {
-    const int r = sg.rt * a.tile_rows + row;
-    if (r >= a.rows) return;
-    const auto record = [&](int k) {
-      return a.rec + ((static_cast<int64_t>(first + k) * 2 + (k == 0 ? slot0 : 0)) * kChunkRows + row) * (kRecHead + D);
-    };
-    float y[D / 32];
+  const auto record = [&](int k, int x) {
+    return a.rec + ((static_cast<int64_t>(first + k) * 2 + (k == 0 ? slot0 : 0)) * kChunkRows + row0 + x) * (kRecHead + D);
+  };
+  // The four rows side by side. Their records' heads first: lane 8 x + k looks at row x's record k, k + 8, ...
+  float M[kMergeRows];
+  {
+    float top = -INFINITY;
+    for (int k = lane & 7; k < n; k += 8) top = fmaxf(top, record(k, lane >> 3)[0]);
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
-    float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, record(k)[0]);
-    M = dev::warp_max(M);
-    float l = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float* p = record(k);
-      const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M);
-      l += f == 0.f ? 0.f : p[1] * f;
+    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+    for (int x = 0; x < kMergeRows; ++x) M[x] = __shfl_sync(0xffffffffu, top, 8 * x);
+  }
+  float y[kMergeRows][D / 32], l[kMergeRows];
+#pragma unroll
+  for (int x = 0; x < kMergeRows; ++x) {
+    l[x] = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) y[x][e] = 0.f;
+  }
+#pragma unroll 2
+  for (int k = 0; k < n; ++k)
+#pragma unroll
+    for (int x = 0; x < kMergeRows; ++x) {
+      const float* p = record(k, x);
+      const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M[x]);
+      l[x] += f == 0.f ? 0.f : p[1] * f;
 #pragma unroll
       for (int e = 0; e < D / 32; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(p + kRecHead + lane * (D / 32) + e);
-        y[e] = fmaf(x.x, f, y[e]);
-        y[e + 1] = fmaf(x.y, f, y[e + 1]);
+        const float2 z = *reinterpret_cast<const float2*>(p + kRecHead + lane * (D / 32) + e);
+        y[x][e] = fmaf(z.x, f, y[x][e]);
+        y[x][e + 1] = fmaf(z.y, f, y[x][e + 1]);
       }
     }
-    put(sg.b, sg.kv, r, y, l == 0.f ? 0.f : 1.f / l, l == 0.f ? -INFINITY : (M - kLift + log2f(l)) * kLn2);
+#pragma unroll
+  for (int x = 0; x < kMergeRows; ++x) {
+    const int r = sg.rt * a.tile_rows + row0 + x;
+    if (r < a.rows)
+      put(sg.b, sg.kv, r, y[x], l[x] == 0.f ? 0.f : 1.f / l[x], l[x] == 0.f ? -INFINITY : (M[x] - kLift + log2f(l[x])) * kLn2);
   }
 }
 
