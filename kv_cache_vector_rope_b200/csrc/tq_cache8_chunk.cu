@@ -642,9 +642,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
 // stream it runs through, if it is that stream's first cut; the blocks behind
 // write the rows of streams with no key at all.
 constexpr int kMergeEmpty = 8, kMergeRows = 4;       // lanes 8 x + k: kMergeRows x 8 of a warp
+constexpr int kMergeSplit = 4;                       // blocks of 8 warps for a tile's rows
 template <int D>
-__global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = (blockIdx.y * 8 + w) * kMergeRows;
+__global__ void __launch_bounds__(256, 4) cache8_merge_kernel(AttnArgs a, int grid) {
+  __shared__ Seg seg;
+  __shared__ Cut of_seg;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int from = (blockIdx.y * 8 + w) * kMergeRows, step = gridDim.y * 8 * kMergeRows;   // rows of a tile
   wait_before();
   const auto put = [&](int b, int kv, int r, const float* y, float inv, float lse) {
     const int i = a.group_div.of(r), hq = kv * a.group + r - i * a.group;
@@ -665,9 +669,10 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid)
         for (; none; none &= none - 1) {
           const int rt = rt0 + __ffs(none) - 1;
           const float y[D / 32] = {};
-          for (int row = row0; row < row0 + kMergeRows; ++row)
-            if (rt * a.tile_rows + row < a.rows)
-              for (int kv = 0; kv < a.heads; ++kv) put(b, kv, rt * a.tile_rows + row, y, 0.f, -INFINITY);
+          for (int row0 = from; row0 < kChunkRows; row0 += step)
+            for (int row = row0; row < row0 + kMergeRows; ++row)
+              if (rt * a.tile_rows + row < a.rows)
+                for (int kv = 0; kv < a.heads; ++kv) put(b, kv, rt * a.tile_rows + row, y, 0.f, -INFINITY);
         }
       }
     }
@@ -675,51 +680,60 @@ __global__ void __launch_bounds__(256) cache8_merge_kernel(AttnArgs a, int grid)
   }
   const int border = (blockIdx.x + 1) * per;
   if (border >= total) return;
-  int next;
-  const Seg sg = seg_at(a, a.cum_out, border, total, &next);
-  const Cut cut = stream_cut(a, sg.start, sg.units, per);
+  if (w == 0) {                                      // one warp looks: the walk is instructions, not data
+    int next;
+    const Seg s = seg_at(a, a.cum_out, border, total, &next);
+    if (lane == 0) {
+      seg = s;
+      of_seg = stream_cut(a, s.start, s.units, per);
+    }
+  }
+  __syncthreads();
+  const Seg sg = seg;
+  const Cut cut = of_seg;
   // Not cut (the border is at its start or in its lead), or cut before as well.
   if (cut.first != static_cast<int>(blockIdx.x) || cut.last == cut.first) return;
   const int first = cut.first, n = cut.last - cut.first + 1, slot0 = cut.slot;
-  const auto record = [&](int k, int x) {
-    return a.rec + ((static_cast<int64_t>(first + k) * 2 + (k == 0 ? slot0 : 0)) * kChunkRows + row0 + x) * (kRecHead + D);
-  };
-  // The four rows side by side. Their records' heads first: lane 8 x + k looks at row x's record k, k + 8, ...
-  float M[kMergeRows];
-  {
-    float top = -INFINITY;
-    for (int k = lane & 7; k < n; k += 8) top = fmaxf(top, record(k, lane >> 3)[0]);
+  for (int row0 = from; row0 < kChunkRows && sg.rt * a.tile_rows + row0 < a.rows; row0 += step) {
+    const auto record = [&](int k, int x) {
+      return a.rec + ((static_cast<int64_t>(first + k) * 2 + (k == 0 ? slot0 : 0)) * kChunkRows + row0 + x) * (kRecHead + D);
+    };
+    // The four rows side by side. Their records' heads first: lane 8 x + k looks at row x's record k, k + 8, ...
+    float M[kMergeRows];
+    {
+      float top = -INFINITY;
+      for (int k = lane & 7; k < n; k += 8) top = fmaxf(top, record(k, lane >> 3)[0]);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
-    for (int x = 0; x < kMergeRows; ++x) M[x] = __shfl_sync(0xffffffffu, top, 8 * x);
-  }
-  float y[kMergeRows][D / 32], l[kMergeRows];
-#pragma unroll
-  for (int x = 0; x < kMergeRows; ++x) {
-    l[x] = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) y[x][e] = 0.f;
-  }
-#pragma unroll 2
-  for (int k = 0; k < n; ++k)
+      for (int x = 0; x < kMergeRows; ++x) M[x] = __shfl_sync(0xffffffffu, top, 8 * x);
+    }
+    float y[kMergeRows][D / 32], l[kMergeRows];
 #pragma unroll
     for (int x = 0; x < kMergeRows; ++x) {
-      const float* p = record(k, x);
-      const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M[x]);
-      l[x] += f == 0.f ? 0.f : p[1] * f;
+      l[x] = 0.f;
 #pragma unroll
-      for (int e = 0; e < D / 32; e += 2) {
-        const float2 z = *reinterpret_cast<const float2*>(p + kRecHead + lane * (D / 32) + e);
-        y[x][e] = fmaf(z.x, f, y[x][e]);
-        y[x][e + 1] = fmaf(z.y, f, y[x][e + 1]);
-      }
+      for (int e = 0; e < D / 32; ++e) y[x][e] = 0.f;
     }
+#pragma unroll 2
+    for (int k = 0; k < n; ++k)
 #pragma unroll
-  for (int x = 0; x < kMergeRows; ++x) {
-    const int r = sg.rt * a.tile_rows + row0 + x;
-    if (r < a.rows)
-      put(sg.b, sg.kv, r, y[x], l[x] == 0.f ? 0.f : 1.f / l[x], l[x] == 0.f ? -INFINITY : (M[x] - kLift + log2f(l[x])) * kLn2);
+      for (int x = 0; x < kMergeRows; ++x) {
+        const float* p = record(k, x);
+        const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M[x]);
+        l[x] += f == 0.f ? 0.f : p[1] * f;
+        float z[D / 32];
+        if constexpr (D == 128) *reinterpret_cast<float4*>(z) = *reinterpret_cast<const float4*>(p + kRecHead + lane * 4);
+        else *reinterpret_cast<float2*>(z) = *reinterpret_cast<const float2*>(p + kRecHead + lane * 2);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) y[x][e] = fmaf(z[e], f, y[x][e]);
+      }
+#pragma unroll
+    for (int x = 0; x < kMergeRows; ++x) {
+      const int r = sg.rt * a.tile_rows + row0 + x;
+      if (r < a.rows)
+        put(sg.b, sg.kv, r, y[x], l[x] == 0.f ? 0.f : 1.f / l[x], l[x] == 0.f ? -INFINITY : (M[x] - kLift + log2f(l[x])) * kLn2);
+    }
   }
 }
 
@@ -733,7 +747,7 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_behind(cache8_merge_kernel<D>, dim3(kSms - 1 + kMergeEmpty, kChunkRows / 8 / kMergeRows), 256, st, a, kSms);
+  e = launch_behind(cache8_merge_kernel<D>, dim3(kSms - 1 + kMergeEmpty, kMergeSplit), 256, st, a, kSms);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
