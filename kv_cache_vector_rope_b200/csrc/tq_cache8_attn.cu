@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
   // The next segment with keys, if the range has one: its first groups set out.
   const auto open = [&] {
     for (u = next; u < u1; u = next) {
-      sg = seg_at(a, cum, u, u1, &next);
+      if (u == u0) sg = seg_at(a, cum, u, u1, &next);
+      else seg_after(a, cum, sg, u, u1, &next);
       if (sg.t1 > sg.t0) break;
     }
     if (u >= u1) return;

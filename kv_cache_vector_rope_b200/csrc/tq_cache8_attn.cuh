@@ -120,6 +120,17 @@ struct Seg {
   bool head;                                         // the stream's first keys
   int start, units;                                  // of the whole stream: where its cost begins, its units
 };
+__device__ __forceinline__ void seg_fill(const AttnArgs& a, Seg& s, const KeyRange& r, int rel, int u, int uend, int* next) {
+  s.start = u - rel;
+  s.units = r.units;
+  const int take = min(stream_cost(a, r) - rel, uend - u);
+  const int from = max(rel - a.lead, 0), to = rel + take - a.lead;       // units of the stream
+  s.head = from == 0;
+  s.whole = s.head && to == r.units;
+  s.t0 = s.head ? r.lo / 16 * 16 : ((r.lo >> a.unit_log2) + from) << a.unit_log2;
+  s.t1 = to > from ? min(((r.lo >> a.unit_log2) + to) << a.unit_log2, r.hi) : s.t0;
+  *next = u + take;
+}
 __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, int uend, int* next) {
   Seg s;
   s.b = find_seq(cum, a.batch, u);
@@ -134,16 +145,25 @@ __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, 
     rel -= stream_cost(a, r);
     r = tile_range(a, s.n, ++s.rt);
   }
-  s.start = u - rel;
-  s.units = r.units;
-  const int take = min(stream_cost(a, r) - rel, uend - u);
-  const int from = max(rel - a.lead, 0), to = rel + take - a.lead;       // units of the stream
-  s.head = from == 0;
-  s.whole = s.head && to == r.units;
-  s.t0 = s.head ? r.lo / 16 * 16 : ((r.lo >> a.unit_log2) + from) << a.unit_log2;
-  s.t1 = to > from ? min(((r.lo >> a.unit_log2) + to) << a.unit_log2, r.hi) : s.t0;
-  *next = u + take;
+  seg_fill(a, s, r, rel, u, uend, next);
   return s;
+}
+// The segment behind `s`, which ends its stream at u < uend: the next stream that costs anything, from its start.
+__device__ __forceinline__ void seg_after(const AttnArgs& a, const int* cum, Seg& s, int u, int uend, int* next) {
+  KeyRange r;
+  do {
+    if (++s.rt == a.row_tiles) {
+      s.rt = 0;
+      if (++s.kv == a.heads) {
+        s.kv = 0;
+        do ++s.b;
+        while (cum[s.b + 1] <= u);
+        s.n = seq_len(a, s.b, false);
+      }
+    }
+    r = tile_range(a, s.n, s.rt);
+  } while (r.units <= 0);
+  seg_fill(a, s, r, 0, u, uend, next);
 }
 // The CTAs that take a stream's units, and whether the first of them keeps its record in its second slot: it does
 // where its range holds an earlier stream's end.

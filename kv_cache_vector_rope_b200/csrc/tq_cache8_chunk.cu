@@ -241,6 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
     if (lane == 0) mbar_arrive(bar + which);
   };
   bool alive = true;
+  const auto walk = [&](Seg& sg, int u, int& next) {
+    if (u == u0) sg = seg_at(a, cum, u, u1, &next);
+    else seg_after(a, cum, sg, u, u1, &next);
+  };
 
   if (w < 8) {
     // ------------------------------------------------------------ weights: one row per thread
@@ -250,9 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
     const uint32_t s_at = tmem + lanes + 128 * q, o_at = tmem + lanes + 256 + D * q;
     uint32_t tiles_seen = 0;                         // tiles of this query tile so far
     uint32_t walked = 0;                             // tiles of all segments: the info ring's count
-    for (int u = u0; alive && u < u1;) {
-      int next;
-      const Seg sg = seg_at(a, cum, u, u1, &next);
+    Seg sg;
+    for (int u = u0, next; alive && u < u1;) {
+      walk(sg, u, next);
       if (sg.t1 <= sg.t0) {
         u = next;
         continue;
@@ -426,9 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
     const uint32_t at0 = to + ((((c & 3) * 2 + (odd ? 1 : 0)) ^ (row & 7)) << 4);
     const uint32_t at1 = to + ((((c & 3) * 2 + (odd ? 0 : 1)) ^ (row & 7)) << 4);
     uint32_t it = 0;
-    for (int u = u0; alive && u < u1;) {
-      int next;
-      const Seg sg = seg_at(a, cum, u, u1, &next);
+    Seg sg;
+    for (int u = u0, next; alive && u < u1;) {
+      walk(sg, u, next);
       if (sg.t1 <= sg.t0) {
         u = next;
         continue;
@@ -509,9 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           if (last) umma_commit(bar + kVEmpty + st);
         }
       };
-      for (int u = u0; alive && u < u1;) {
-        int next;
-        const Seg sg = seg_at(a, cum, u, u1, &next);
+      Seg sg;
+      for (int u = u0, next; alive && u < u1;) {
+        walk(sg, u, next);
         if (sg.t1 <= sg.t0) {
           u = next;
           continue;
@@ -559,9 +563,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
       // ---------------------------------------------------------- codes in: lane g < 8 takes keys 16 g .. of each tile
       uint32_t it = 0;
       const uint32_t bytes = 16 * D;
-      for (int u = u0; alive && u < u1;) {
-        int next;
-        const Seg sg = seg_at(a, cum, u, u1, &next);
+      Seg sg;
+      for (int u = u0, next; alive && u < u1;) {
+        walk(sg, u, next);
         if (sg.t1 <= sg.t0) {
           u = next;
           continue;
