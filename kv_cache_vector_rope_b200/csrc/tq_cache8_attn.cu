@@ -648,7 +648,8 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       for (int k = 0; k < kAtWarps; ++k) M = fmaxf(M, sm_m[k * kRows + tid]);
 #pragma unroll
       for (int k = 0; k < kAtWarps; ++k)
-        if (sm_m[k * kRows + tid] != -INFINITY) sum += sm_l[k * kRows + tid] * fast_exp2(sm_m[k * kRows + tid] - M);
+        if (sm_l[k * kRows + tid] != 0.f)            // also with a NaN in the row, whose maximum is -inf
+          sum += sm_l[k * kRows + tid] * fast_exp2(sm_m[k * kRows + tid] - M);
       sm_top[tid] = M;
       sm_top[kRows + tid] = sum;
     }

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
   const float w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M), w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
   if (tid < n) wt[tid] = w0;
   if (tid + kCbThreads < n) wt[tid + kCbThreads] = w1;
-  const float lw = dev::warp_sum((w0 == 0.f ? 0.f : l0 * w0) + (w1 == 0.f ? 0.f : l1 * w1));
+  const float lw = dev::warp_sum(l0 * w0 + l1 * w1);   // a NaN of a row, whose maximum is -inf, stays
   if ((tid & 31) == 0) red[1][tid >> 5] = lw;
   __syncthreads();
   float L = 0.f;

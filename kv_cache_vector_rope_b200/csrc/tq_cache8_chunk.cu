@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(256, 4) cache8_merge_kernel(AttnArgs a, int gr
       for (int x = 0; x < kMergeRows; ++x) {
         const float* p = record(k, x);
         const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M[x]);
-        l[x] += f == 0.f ? 0.f : p[1] * f;
+        l[x] = fmaf(p[1], f, l[x]);                    // a NaN of a row, whose maximum is -inf, stays
         float z[D / 32];
         if constexpr (D == 128) *reinterpret_cast<float4*>(z) = *reinterpret_cast<const float4*>(p + kRecHead + lane * 4);
         else *reinterpret_cast<float2*>(z) = *reinterpret_cast<const float2*>(p + kRecHead + lane * 2);
