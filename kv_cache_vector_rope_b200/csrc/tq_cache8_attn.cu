@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       }
       const uint32_t ka = k_first + at * kStage, va = v_first + at * kStage;
       uint32_t vw[G][4][VW];
-      const auto values = [&] {                      // then every lane has its operands: the stage is free
+      const auto values = [&] {
 #pragma unroll
         for (int x = 0; x < G; ++x)
 #pragma unroll
@@ -436,13 +436,6 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
               }
             }
           }
-        const int freed = at;
-        phase ^= step(at) ? 1u : 0u;
-        __syncwarp();
-        if (issued < turns) {
-          issue(issued, issued - (i - rel), freed);
-          ++issued;
-        }
 #pragma unroll
         for (int x = 0; x < G; ++x)
           if (key0 + 16 * x + 16 > known[x]) {       // what lies behind the sequence, or in no page, may be any byte
@@ -622,6 +615,15 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
               for (int e = 0; e < 4; ++e) acc[nt][2 * c + h][e] += y[nt][e];
           }
         }
+      }
+      // Every lane's operands have gone into products: the stage is free. (Right behind the loads, with nothing in
+      // between that waits for their data, a copy could overtake them.)
+      const int freed = at;
+      phase ^= step(at) ? 1u : 0u;
+      __syncwarp();
+      if (issued < turns) {
+        issue(issued, issued - (i - rel), freed);
+        ++issued;
       }
     }
     const Seg was = sg;                              // merged while the next segment's first groups are on their way

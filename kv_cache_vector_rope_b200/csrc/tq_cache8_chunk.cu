@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         const int left = sg.n - (key0 + j * kTile);  // what lies behind the sequence may be any byte
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          alive = __all_sync(0xffffffffu, wait(kRawFull + kv, it));
+          alive = __all_sync(0xffffffffu, wait(kRawFull + kv, it) && wait((kv ? kVEmpty : kKEmpty) + st, parity ^ 1));
           if (!alive) break;
           const TileInfo& inf = info[it & 3];
           const float* ratios = kv ? inf.rv : inf.rk;
@@ -457,9 +457,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           uint4 codes[kPer];
 #pragma unroll
           for (int x = 0; x < kPer; ++x) codes[x] = raw[x * 128];
-          arrive(kRawEmpty + kv);                    // the next tile's codes come while these are converted
-          alive = __all_sync(0xffffffffu, wait((kv ? kVEmpty : kKEmpty) + st, parity ^ 1));
-          if (!alive) break;
 #pragma unroll
           for (int x = 0; x < kPer; ++x) {
             const int group = (x * kStepRows + row) >> 4;
@@ -471,7 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar + (kv ? kVFull : kKFull) + st);
+          // The raw codes are given back only here, when what was read has been used: an arrival right behind the
+          // loads, with nothing that waits for their data, let the next copy overwrite codes not yet read.
+          if (lane == 0) {
+            mbar_arrive(bar + kRawEmpty + kv);
+            mbar_arrive(bar + (kv ? kVFull : kKFull) + st);
+          }
         }
       }
       u = next;

@@ -269,3 +269,64 @@ def test_pages_beyond_32_bits():
         tq.tq_cache8_attention(small, q, _i32([400]), b, ws, block_table=_i32([[0, 1, 2, 3]]), d_status=st)
         assert torch.equal(a, b)
     assert int(st.item()) == 0
+
+
+def _check_large(cache, table, q, lens, out, lse, od, causal=True, window=0):
+    """Against 64 bits on the device, over the codes read back (exact, as tested by themselves); a sequence and a KV head
+    at a time."""
+    b, hq, nq, d = q.shape
+    h = cache.k.shape[1]
+    g = hq // h
+    for i in range(b):
+        n = lens[i]
+        kv = [torch.empty(n, h, d, device="cuda") for _ in range(2)]
+        tq.tq_cache8_read(cache, kv[0], kv[1], _i32([0, n]), _i32([0]), block_table=table[i:i + 1].contiguous())
+        at = torch.arange(n, device="cuda")
+        pos = n - nq + torch.arange(nq, device="cuda") if causal else torch.full((nq,), n - 1, device="cuda")
+        see = at[None] <= pos[:, None]
+        if window:
+            see &= at[None] > pos[:, None] - window
+        for j in range(h):
+            k, v = kv[0][:, j].double(), kv[1][:, j].double()
+            x = q[i, j * g:j * g + g].double()
+            s = (x @ k.T / d ** 0.5).masked_fill(~see, -torch.inf)
+            m = s.amax(-1, keepdim=True)
+            p = (s - torch.where(torch.isinf(m), 0.0, m)).exp()
+            tot = p.sum(-1, keepdim=True)
+            some = tot > 0
+            ref = torch.where(some, p @ v / tot, 0.0)
+            A = torch.where(some, p @ v.abs() / tot, 0.0)
+            B = (x.abs() @ k.abs().T / d ** 0.5).masked_fill(~see, 0.0).amax(-1, keepdim=True)
+            es = ((2 * d / 16 + 8) * 2.0 ** -23 + 2.0 ** -22) * B
+            ew = es + 2.0 ** -22 + 2 * (2 * B + 20) * 2.0 ** -24
+            ew = ew + (2.0 ** -21 if od == "f32" else 2.0 ** -12) + (n / 16 + 40) * 2.0 ** -23
+            most = {"e4m3": 448.0, "int8": 127.0}[cache.code] * cache.v_scale[table[i, :-(-n // cache.k.shape[2])].long(), j].max()
+            tol = HALF[od] * ref.abs() + 2 * ew * A + n * 2.0 ** -30 * float(most)
+            err = (out[i, j * g:j * g + g].double() - ref).abs()
+            assert bool((err <= tol).all()), (i, j, float((err / tol).max()))
+            want = torch.where(some, m + tot.log(), -torch.inf)[..., 0]
+            got = lse[i, j * g:j * g + g].double()
+            assert torch.equal(torch.isneginf(got), torch.isneginf(want))
+            fine = ~torch.isneginf(want)
+            assert bool(((got - want).abs() <= ew[..., 0] + 2.0 ** -22 * (1 + want.abs()))[fine].all())
+
+
+@pytest.mark.parametrize("b,hkv,group,nq,n,d,block,code,window,dtype", [
+    (2, 8, 4, 600, 4096, 128, 64, "e4m3", 0, "bf16"), (4, 4, 4, 1024, 1024, 128, 16, "int8", 0, "bf16"),
+    (3, 6, 1, 700, 3001, 64, 32, "e4m3", 513, "bf16"), (9, 8, 2, 129, 2500, 64, 128, "int8", 0, "bf16"),
+    (16, 8, 4, 1, 5000, 128, 64, "e4m3", 0, "bf16"), (16, 12, 1, 4, 3000, 64, 16, "int8", 1000, "f32"),
+    (16, 8, 4, 3, 4000, 128, 32, "e4m3", 0, "bf16"), (9, 4, 4, 2, 3000, 256, 16, "int8", 0, "f32")])
+def test_ranges_of_several_streams_a_cta(b, hkv, group, nq, n, d, block, code, window, dtype):
+    # More streams than CTAs: a CTA ends one, starts the next, and their copies, products and merges overlap.
+    rg = np.random.default_rng(n)
+    lens = [n] + [int(x) for x in rg.integers(1, n + 1, b - 1)] if nq < 600 else [n] * b
+    s = Setup(n + d, lens, hkv, d, block, code)
+    s.write(lens, [0] * b, scale=2.0)
+    q = _queries(s, b, nq, hkv * group, d, dtype)
+    ws = tq.cache8_attention_workspace(s.cache, b, hkv * group, nq)
+    out, lse = _attend(s, q, lens, dtype, ws=ws, window=window)
+    assert int(s.status.item()) == 0
+    _check_large(s.cache, s.dtable, q, lens, out, lse, dtype, window=window)
+    for _ in range(3):
+        again, _ = _attend(s, q, lens, dtype, ws=ws, window=window)
+        assert torch.equal(again, out)
