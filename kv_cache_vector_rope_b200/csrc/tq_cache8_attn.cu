@@ -797,7 +797,9 @@ constexpr size_t kCumBytes = (sizeof(int) * (kSlice + 1) + 255) / 256 * 256;
 
 size_t attn_workspace(int d, int64_t rows) {
   const size_t few = sizeof(float) * kAtGrid * 2 * 16 * static_cast<size_t>(kRecHead + d);
-  const size_t many = chunk_supported(d, false, static_cast<int>(rows)) ? chunk_record_bytes(d) : 0;
+  const size_t chunk = chunk_supported(d, false, static_cast<int>(rows)) ? chunk_record_bytes(d) : 0;
+  const size_t wide = rows_supported(d, true, static_cast<int>(rows)) ? rows_record_bytes(d) : 0;
+  const size_t many = chunk > wide ? chunk : wide;
   return kCumBytes + (few > many ? few : many);
 }
 
@@ -853,23 +855,25 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
     return fail(TQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, workspace_bytes, attn_workspace(d, rows));
   if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
   const bool qf = q_dtype == TQ_F32, of = out_dtype == TQ_F32;
-  const bool many = chunk_supported(d, qf || of, rows);
-  const int tile = many ? kChunkRows : rows_of(d, rows, qf, of, cache->code == TQ_INT8), row_tiles = (rows + tile - 1) / tile;
-  const int unit = many ? kChunkUnit : kUnit, lead = many ? kChunkLead : lead_of(d);
+  const bool chunk = chunk_supported(d, qf || of, rows), wide = rows_supported(d, qf || of, rows);
+  const int tile = chunk ? kChunkRows : wide ? kRowsTile : rows_of(d, rows, qf, of, cache->code == TQ_INT8);
+  const int row_tiles = (rows + tile - 1) / tile;
+  const int unit = chunk ? kChunkUnit : wide ? kRowsUnit : kUnit, lead = chunk ? kChunkLead : wide ? kRowsLead : lead_of(d);
+  const int most = chunk ? kChunkSlice : wide ? kRowsSlice : kSlice;
   // Units of one launch stay below 2^30: batches are cut into slices.
   const int64_t per_seq = ((table_stride * cache->block + unit - 1) / unit + 1 + lead) * cache->heads * row_tiles;
   if (per_seq > (1 << 25))
     return fail(TQ_ERR_UNSUPPORTED, "%s: heads x query rows x capacity of one sequence too large", what);
   int64_t slice = (1 << 30) / per_seq;
-  if (slice > (many ? kChunkSlice : kSlice)) slice = many ? kChunkSlice : kSlice;
-  AttnArgs a{Div(cache->heads), Div(group), Div(row_tiles), cache->heads, cache->block, 0, log2_of(cache->block), cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q,
-             q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, tile, row_tiles, log2_of(unit), many ? kChunkMinUnits : kMinUnits,
+  if (slice > most) slice = most;
+  AttnArgs a{Div(cache->heads), Div(group), Div(row_tiles), cache->heads, cache->block, 0, log2_of(cache->block), cache->n_blocks, cache->k, cache->v, cache->k_scale, cache->v_scale, q, qf, of,
+             q_batch_stride, q_head_stride, q_row_stride, group, nq, rows, tile, row_tiles, log2_of(unit), chunk ? kChunkMinUnits : wide ? kRowsMinUnits : kMinUnits,
              lead,
              nullptr, nullptr, table_stride, 0,
              causal ? 1 : 0, window, scale * kLog2e, out, out_batch_stride, out_head_stride, out_row_stride, lse_out,
              reinterpret_cast<float*>(static_cast<char*>(workspace) + kCumBytes), static_cast<int*>(workspace), pipeline_wait_ns(), d_status};
   Maps maps;
-  if (!many) {
+  if (!chunk && !wide) {
     st = encode_maps(cache, &maps, what);
     if (st != TQ_OK) return st;
   }
@@ -881,7 +885,8 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
     a.lens = seq_lens + b0;
     a.table = block_table ? block_table + b0 * table_stride : nullptr;
     cudaError_t e;
-    if (many) e = launch_chunk(d, i8, a, s);
+    if (chunk) e = launch_chunk(d, i8, a, s);
+    else if (wide) e = launch_rows(d, i8, a, s);
     else if (d == 64) e = launch_few<64>(i8, tile, qf, of, maps, a, s);
     else if (d == 128) e = launch_few<128>(i8, tile, qf, of, maps, a, s);
     else e = launch_few<256>(i8, tile, qf, of, maps, a, s);

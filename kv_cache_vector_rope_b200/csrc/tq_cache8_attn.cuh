@@ -49,6 +49,7 @@ struct AttnArgs {
   const float* ks;
   const float* vs;
   const void* q;
+  bool q_f32, out_f32;
   int64_t q_bs, q_hs, q_rs;
   int group, nq, rows;                               // rows = group * nq per KV head, row r: position r / group
   int tile_rows, row_tiles;                          // rows a CTA takes together
@@ -363,5 +364,15 @@ constexpr int kChunkSlice = 256;                     // sequences per launch
 bool chunk_supported(int d, bool f32, int rows);
 size_t chunk_record_bytes(int d);
 cudaError_t launch_chunk(int d, bool int8, const c8::AttnArgs& a, cudaStream_t st);
+
+// The kernel for many query rows that are fp32, or d = 256 (tq_cache8_rows.cu).
+constexpr int kRowsTile = 128;                       // rows a CTA takes together
+constexpr int kRowsUnit = 64;                        // keys per unit
+constexpr int kRowsMinUnits = 4;
+constexpr int kRowsLead = 4;                         // a segment's start and end, in units
+constexpr int kRowsSlice = 512;                      // sequences per launch
+bool rows_supported(int d, bool f32, int rows);
+size_t rows_record_bytes(int d);
+cudaError_t launch_rows(int d, bool int8, const c8::AttnArgs& a, cudaStream_t st);
 
 }  // namespace tq

@@ -170,10 +170,10 @@ def test_many_sequences_of_many_rows():
     _check_attention(s, q, lens, out, lse, "bf16")
 
 
-@pytest.mark.parametrize("nq,code,d", [(1, "e4m3", 128), (1, "int8", 64), (80, "e4m3", 128)])
+@pytest.mark.parametrize("nq,code,d", [(1, "e4m3", 128), (1, "int8", 256), (80, "e4m3", 128)])
 def test_waits_that_run_out_are_reported_and_leave_nothing_behind(monkeypatch, nq, code, d):
     monkeypatch.delenv("TQ_TEST_WAIT_NS", raising=False)
-    # Long enough that every warp's ring goes round several times: only then has a copy to be waited for.
+    # Long enough that every warp's ring goes round many times, and bound by the copies: only then are they waited for.
     lens = [200000, 40, 700] if nq < 9 else [60000, 40, 700]
     s = Setup(7, lens, 8, d, 64, code)
     for x in (s.cache.k, s.cache.v):
@@ -186,7 +186,9 @@ def test_waits_that_run_out_are_reported_and_leave_nothing_behind(monkeypatch, n
     assert int(s.status.item()) == 0
     monkeypatch.setenv("TQ_TEST_WAIT_NS", "0")
     seen = False
-    for _ in range(5):
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        flush.zero_()
         s.status.zero_()
         _attend(s, q, lens, ws=ws)
         seen |= bool(int(s.status.item()) & tq.TQ_DEV_TIMEOUT)
