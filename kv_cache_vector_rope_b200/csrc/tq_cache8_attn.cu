@@ -34,11 +34,11 @@
 // score costs a quarter of the keys' conversions and half the instructions.
 //
 // Bound by instruction issue beside the memory: unpacking 8-bit codes for the
-// matrix unit, softmax and the two products take about 300 issue slots for each
-// 16 keys of a warp. Measured, floor of the cache's bytes in brackets: a step of
+// matrix unit, softmax and the two products fill 56% of the issue slots and 47%
+// of the integer pipe where streams are short. Measured, floor of the cache's bytes in brackets: a step of
 // 8 sequences of 32768 keys, 8 KV heads, 4 rows each, d = 128, 98 us (82); one
-// sequence of 131072 keys 56 us (41); four drafted fp32 rows of 32 ragged
-// sequences, 20 KV heads, d = 64, 80 us (40).
+// sequence of 131072 keys 54 us (41); four drafted fp32 rows of 32 ragged
+// sequences, 20 KV heads, d = 64, 71 us (40).
 #include <cuda.h>
 
 #include "tq_cache8_attn.cuh"
@@ -200,8 +200,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
   scan_counts<kAtThreads>(cum, reinterpret_cast<int*>(smem + L::kOffPart), a.batch, [&](int b) {
     return head_units(a, seq_len(a, b, blockIdx.x == 0)) * a.heads;
   });
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= a.batch; b += kAtThreads) a.cum_out[b] = cum[b];
+  if (tid == 0) a.cuts[blockIdx.x].n = 0;
   let_next_start();
   const int total = cum[a.batch];
   const int per = units_per_cta(a, total, gridDim.x);
@@ -662,7 +661,9 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
         f[nt][j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - sm_top[row_of(nt, j)]) * vrun;
-    float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (was.head && was_u != u0 ? 1 : 0)) * kRows * (kRecHead + D);
+    const bool second = was.head && was_u != u0;     // the record's slot
+    if (tid == 0 && was.head && !was.whole) a.cuts[blockIdx.x] = cut_of(a, was, second, per);
+    float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (second ? 1 : 0)) * kRows * (kRecHead + D);
     constexpr int kPieces = 4 / NJ, kVals = 2 * NJ;  // 16-row tiles at a time, and values of a lane in each
     static_assert(NT * MT % kPieces == 0, "whole pieces");
     float* sums = reinterpret_cast<float*>(smem + L::kOffQ + buf * L::kQBytes);
@@ -793,14 +794,14 @@ int log2_of(int x) {
   return n;
 }
 
-constexpr size_t kCumBytes = (sizeof(int) * (kSlice + 1) + 255) / 256 * 256;
+constexpr size_t kCutBytes = (sizeof(CutInfo) * kMaxRecs + 255) / 256 * 256;
 
 size_t attn_workspace(int d, int64_t rows) {
   const size_t few = sizeof(float) * kAtGrid * 2 * 16 * static_cast<size_t>(kRecHead + d);
   const size_t chunk = chunk_supported(d, false, static_cast<int>(rows)) ? chunk_record_bytes(d) : 0;
   const size_t wide = rows_supported(d, true, static_cast<int>(rows)) ? rows_record_bytes(d) : 0;
   const size_t many = chunk > wide ? chunk : wide;
-  return kCumBytes + (few > many ? few : many);
+  return kCutBytes + (few > many ? few : many);
 }
 
 }  // namespace
@@ -871,7 +872,7 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
              lead,
              nullptr, nullptr, table_stride, 0,
              causal ? 1 : 0, window, scale * kLog2e, out, out_batch_stride, out_head_stride, out_row_stride, lse_out,
-             reinterpret_cast<float*>(static_cast<char*>(workspace) + kCumBytes), static_cast<int*>(workspace), pipeline_wait_ns(), d_status};
+             reinterpret_cast<float*>(static_cast<char*>(workspace) + kCutBytes), reinterpret_cast<CutInfo*>(workspace), pipeline_wait_ns(), d_status};
   Maps maps;
   if (!chunk && !wide) {
     st = encode_maps(cache, &maps, what);

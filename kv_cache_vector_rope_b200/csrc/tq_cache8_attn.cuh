@@ -66,7 +66,7 @@ struct AttnArgs {
   int64_t o_bs, o_hs, o_rs;
   float* lse;                                        // [batch][hq][nq] or NULL
   float* rec;                                        // [grid][2][tile_rows][kRecHead + d]
-  int* cum_out;                                      // [batch + 1], for the combine kernel
+  struct CutInfo* cuts;                              // [grid], for the merge
   uint64_t wait_ns;
   int32_t* d_status;
 };
@@ -166,16 +166,18 @@ __device__ __forceinline__ void seg_after(const AttnArgs& a, const int* cum, Seg
   } while (r.units <= 0);
   seg_fill(a, s, r, 0, u, uend, next);
 }
-// The CTAs that take a stream's units, and whether the first of them keeps its record in its second slot: it does
-// where its range holds an earlier stream's end.
-struct Cut {
-  int first, last, slot;
+// What a CTA whose range ends inside a stream that it began leaves for the merge: the CTAs from this one on that hold a
+// record of the stream (0: there is no such stream), whether its own is in its second slot, and which stream it is.
+struct CutInfo {
+  int n, slot, b, kv, rt;
 };
-__device__ __forceinline__ Cut stream_cut(const AttnArgs& a, int start, int units, int per) {
-  Cut c;
-  c.first = (start + a.lead) / per;
-  c.last = (start + a.lead + units - 1) / per;
-  c.slot = start > c.first * per ? 1 : 0;
+__device__ __forceinline__ CutInfo cut_of(const AttnArgs& a, const Seg& s, bool second, int per) {
+  CutInfo c;
+  c.n = (s.start + a.lead + s.units - 1) / per - static_cast<int>(blockIdx.x) + 1;
+  c.slot = second;
+  c.b = s.b;
+  c.kv = s.kv;
+  c.rt = s.rt;
   return c;
 }
 
@@ -231,12 +233,37 @@ __device__ __forceinline__ void load_q16(const void* p, int64_t i, float* x) {
   }
 }
 
+// A warp's part of the rows without a key: it looks at kEmptyPairs (sequence, row tile) pairs from `pair` on and writes
+// zeros for rows row0, row0 + step, ... of those where no row sees a key, all heads.
+constexpr int kEmptyPairs = 4;
+template <int D>
+__device__ __forceinline__ void put_empty(const AttnArgs& a, int pair, int row0, int step) {
+  const int lane = threadIdx.x & 31;
+  for (int end = min(pair + kEmptyPairs, a.batch * a.row_tiles); pair < end; ++pair) {
+    const int b = a.tiles_div.of(pair), rt = pair - b * a.row_tiles;
+    const int n = seq_len(a, b, false);
+    if (n > 0 && tile_range(a, n, rt).units > 0) continue;
+    const int pieces = a.out_f32 ? D / 4 : D / 8, log2 = 31 - __clz(pieces);     // of 16 bytes
+    for (int row = row0; row < a.tile_rows && rt * a.tile_rows + row < a.rows; row += step) {
+      const int r = rt * a.tile_rows + row, i = a.group_div.of(r);
+      for (int x = lane; x < a.heads * pieces; x += 32) {
+        const int hq = (x >> log2) * a.group + r - i * a.group, piece = x & (pieces - 1);
+        const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs;
+        char* to = static_cast<char*>(a.out) + at * (a.out_f32 ? 4 : 2);
+        reinterpret_cast<uint4*>(to)[piece] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse && piece == 0) a.lse[((a.first_seq + b) * a.heads * a.group + hq) * a.nq + i] = -INFINITY;
+      }
+    }
+  }
+}
+
 // Merges the records of every stream that more than one CTA worked on, and
-// writes the rows of streams with no key at all. One CTA per (sequence, KV
-// head, row tile) and row: the records' maxima and sums are read side by side,
-// then D / 4 lanes walk the coordinates with the other threads dealing the
-// records out among themselves, so that a stream in hundreds of records (one
-// long sequence) costs a few rounds of loads, not one per record.
+// writes the rows of streams with no key at all. Block x < grid - 1 takes the
+// stream that CTA x began and others ended, if there is one, and a row of it:
+// the records' maxima and sums are read side by side, then D / 4 lanes walk the
+// coordinates with the other threads dealing the records out among themselves,
+// so that a stream in hundreds of records (one long sequence) costs a few rounds
+// of loads, not one per record. The blocks behind look for rows without keys.
 constexpr int kCbThreads = 256;
 template <int D, bool OF>
 __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, int grid) {
@@ -244,23 +271,14 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
   __shared__ float wt[kMaxRecs];
   __shared__ float red[2][kCbThreads / 32];
   __shared__ float4 sums[kParts][D / 4];
-  const int b = blockIdx.z, stream = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+  const int x0 = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
   wait_before();
-  const int kv = a.tiles_div.of(stream), rt = stream - kv * a.row_tiles, r = rt * a.tile_rows + row;
-  if (r >= a.rows) return;
-  const int c0 = a.cum_out[b], per_head = a.heads_div.of(a.cum_out[b + 1] - c0);
-  const int per = units_per_cta(a, a.cum_out[a.batch], grid);
-  int start = c0 + kv * per_head, units = 0;
-  if (per_head > 0) {
-    const int len = seq_len(a, b, false);
-    for (int x = 0; x < rt; ++x) start += stream_cost(a, tile_range(a, len, x));
-    units = tile_range(a, len, rt).units;
-  }
-  const Cut cut = stream_cut(a, start, units, per);
-  if (units > 0 && cut.first == cut.last) return;    // one CTA had it all and wrote the rows
-  const int n = units > 0 ? cut.last - cut.first + 1 : 0;
+  if (x0 >= grid - 1) return put_empty<D>(a, ((x0 - (grid - 1)) * (kCbThreads / 32) + tid / 32) * kEmptyPairs, row, a.tile_rows);
+  const CutInfo cut = a.cuts[x0];
+  const int b = cut.b, kv = cut.kv, r = cut.rt * a.tile_rows + row, n = cut.n;
+  if (n == 0 || r >= a.rows) return;
   const auto record = [&](int k) {
-    return a.rec + ((static_cast<int64_t>(cut.first + k) * 2 + (k == 0 ? cut.slot : 0)) * a.tile_rows + row) * (kRecHead + D);
+    return a.rec + ((static_cast<int64_t>(x0 + k) * 2 + (k == 0 ? cut.slot : 0)) * a.tile_rows + row) * (kRecHead + D);
   };
   float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;    // n <= kMaxRecs <= 2 * kCbThreads
   if (tid < n) {
@@ -342,12 +360,90 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStre
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
-// Rows that one tile of tile_rows can have, for the combine kernel's grid.
+// Blocks that look for rows without keys, `pairs` (sequence, row tile) pairs each.
+inline int empty_blocks(const AttnArgs& a, int pairs) { return (a.batch * a.row_tiles + pairs - 1) / pairs; }
 template <int D, bool OF>
 cudaError_t launch_combine(const AttnArgs& a, int grid, cudaStream_t st) {
   const int rows = a.rows < a.tile_rows ? a.rows : a.tile_rows;
-  const cudaError_t e = launch_behind(cache8_combine_kernel<D, OF>, dim3(a.heads * a.row_tiles, rows, a.batch), kCbThreads,
-                                      st, a, grid);
+  const cudaError_t e = launch_behind(cache8_combine_kernel<D, OF>, dim3(grid - 1 + empty_blocks(a, kCbThreads / 32 * kEmptyPairs), rows),
+                                      kCbThreads, st, a, grid);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The same for tiles of 128 or 256 rows: block x looks at CTA x's stream and a part of its rows, a warp at four rows side
+// by side (lanes 8 y + k: row y's record k).
+constexpr int kMergeThreads = 256, kMergeRows = 4, kMergeSplit = 4;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads, D == 256 ? 3 : 4) cache8_merge_kernel(AttnArgs a, int grid) {
+  constexpr int E = D / 32;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int x0 = blockIdx.x, from = (blockIdx.y * 8 + w) * kMergeRows, step = gridDim.y * 8 * kMergeRows;
+  wait_before();
+  if (x0 >= grid - 1) return put_empty<D>(a, (x0 - (grid - 1)) * kEmptyPairs, blockIdx.y * 8 + w, gridDim.y * 8);
+  const CutInfo cut = a.cuts[x0];
+  const int n = cut.n;
+  if (n == 0) return;
+  for (int row0 = from; row0 < a.tile_rows && cut.rt * a.tile_rows + row0 < a.rows; row0 += step) {
+    const auto record = [&](int k, int x) {
+      return a.rec + ((static_cast<int64_t>(x0 + k) * 2 + (k == 0 ? cut.slot : 0)) * a.tile_rows + row0 + x) * (kRecHead + D);
+    };
+    float M[kMergeRows];
+    {
+      float top = -INFINITY;
+      for (int k = lane & 7; k < n; k += 8) top = fmaxf(top, record(k, lane >> 3)[0]);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+      for (int x = 0; x < kMergeRows; ++x) M[x] = __shfl_sync(0xffffffffu, top, 8 * x);
+    }
+    float y[kMergeRows][E], l[kMergeRows];
+#pragma unroll
+    for (int x = 0; x < kMergeRows; ++x) {
+      l[x] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[x][e] = 0.f;
+    }
+#pragma unroll 2
+    for (int k = 0; k < n; ++k)
+#pragma unroll
+      for (int x = 0; x < kMergeRows; ++x) {
+        const float* p = record(k, x);
+        const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M[x]);
+        l[x] = fmaf(p[1], f, l[x]);                  // a NaN of a row, whose maximum is -inf, stays
+        float z[E];
+        if constexpr (E == 2) {
+          *reinterpret_cast<float2*>(z) = *reinterpret_cast<const float2*>(p + kRecHead + lane * 2);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 4)
+            *reinterpret_cast<float4*>(z + e) = *reinterpret_cast<const float4*>(p + kRecHead + lane * E + e);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[x][e] = fmaf(z[e], f, y[x][e]);
+      }
+#pragma unroll
+    for (int x = 0; x < kMergeRows; ++x) {
+      const int r = cut.rt * a.tile_rows + row0 + x;
+      if (r >= a.rows) continue;
+      const int i = a.group_div.of(r), hq = cut.kv * a.group + r - i * a.group;
+      const int64_t at = (a.first_seq + cut.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + lane * E;
+      const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        if (a.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + e) = make_float2(y[x][e] * inv, y[x][e + 1] * inv);
+        else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + at + e) = __floats2bfloat162_rn(y[x][e] * inv, y[x][e + 1] * inv);
+      }
+      if (a.lse && lane == 0)
+        a.lse[((a.first_seq + cut.b) * a.heads * a.group + hq) * a.nq + i] =
+            l[x] == 0.f ? -INFINITY : (M[x] - kLift + log2f(l[x])) * kLn2;
+    }
+  }
+}
+template <int D>
+cudaError_t launch_merge(const AttnArgs& a, int grid, cudaStream_t st) {
+  const cudaError_t e = launch_behind(cache8_merge_kernel<D>, dim3(grid - 1 + empty_blocks(a, kEmptyPairs), kMergeSplit),
+                                      kMergeThreads, st, a, grid);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }

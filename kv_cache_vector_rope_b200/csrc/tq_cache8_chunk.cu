@@ -19,6 +19,13 @@
 // rescaling of O (V). A ratio below 2^-15 loses bits that lie 2^-24 below the
 // largest code of the tile. Queries are scaled by a power of two into half's
 // range (exact), weights are rounded to halves (2^-12).
+//
+// Bound by the wait from a half's weights to its next scores (values, scores,
+// two looks at barriers: about 2100 cycles, of which the other half's weights
+// cover 1400) beside shared memory (about 3000 of 4700 cycles a step). Measured:
+// 1024 tokens of two sequences of 8192, 8 KV heads of 4 query heads, d = 128,
+// 294 us (the products alone 158 at the library's rate), d = 64 246 us; a prompt
+// of 4 x 2048 tokens, d = 128, 250 us.
 #include "tq_cache8_attn.cuh"
 
 namespace tq {
@@ -219,8 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
   scan_counts<kThreads>(cum, reinterpret_cast<int*>(smem + L::kOffPart), a.batch, [&](int b) {
     return head_units(a, seq_len(a, b, blockIdx.x == 0)) * a.heads;
   });
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= a.batch; b += kThreads) a.cum_out[b] = cum[b];
+  if (tid == 0) a.cuts[blockIdx.x].n = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -572,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           u = next;
           continue;
         }
+        if (lane == 0 && sg.head && !sg.whole) a.cuts[blockIdx.x] = cut_of(a, sg, u != u0, per);
         const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
         float vref = 0.f;
         // -1: keys the segment does not reach, -2: a page outside the cache.
@@ -642,107 +649,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
   if (w == 12) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Merges the records of the streams that the CTAs' ranges cut, a warp for
-// four rows side by side.
-// Block x < grid - 1 looks at the cut between CTAs x and x + 1 and takes the
-// stream it runs through, if it is that stream's first cut; the blocks behind
-// write the rows of streams with no key at all.
-constexpr int kMergeEmpty = 8, kMergeRows = 4;       // lanes 8 x + k: kMergeRows x 8 of a warp
-constexpr int kMergeSplit = 4;                       // blocks of 8 warps for a tile's rows
-template <int D>
-__global__ void __launch_bounds__(256, 4) cache8_merge_kernel(AttnArgs a, int grid) {
-  __shared__ Seg seg;
-  __shared__ Cut of_seg;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int from = (blockIdx.y * 8 + w) * kMergeRows, step = gridDim.y * 8 * kMergeRows;   // rows of a tile
-  wait_before();
-  const auto put = [&](int b, int kv, int r, const float* y, float inv, float lse) {
-    const int i = a.group_div.of(r), hq = kv * a.group + r - i * a.group;
-    const int64_t at = (a.first_seq + b) * a.o_bs + hq * a.o_hs + i * a.o_rs;
-    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at + lane * (D / 32);
-#pragma unroll
-    for (int e = 0; e < D / 32; e += 2)
-      *reinterpret_cast<__nv_bfloat162*>(to + e) = __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
-    if (a.lse && lane == 0) a.lse[((a.first_seq + b) * a.heads * a.group + hq) * a.nq + i] = lse;
-  };
-  const int total = a.cum_out[a.batch], per = units_per_cta(a, total, grid);
-  if (static_cast<int>(blockIdx.x) >= grid - 1) {
-    for (int b = blockIdx.x - (grid - 1); b < a.batch; b += kMergeEmpty) {
-      const int n = seq_len(a, b, false);
-      for (int rt0 = 0; rt0 < a.row_tiles; rt0 += 32) {
-        const int mine = rt0 + lane;                 // a row tile per lane is looked at
-        uint32_t none = __ballot_sync(0xffffffffu, mine < a.row_tiles && !(n > 0 && tile_range(a, n, mine).units > 0));
-        for (; none; none &= none - 1) {
-          const int rt = rt0 + __ffs(none) - 1;
-          const float y[D / 32] = {};
-          for (int row0 = from; row0 < kChunkRows; row0 += step)
-            for (int row = row0; row < row0 + kMergeRows; ++row)
-              if (rt * a.tile_rows + row < a.rows)
-                for (int kv = 0; kv < a.heads; ++kv) put(b, kv, rt * a.tile_rows + row, y, 0.f, -INFINITY);
-        }
-      }
-    }
-    return;
-  }
-  const int border = (blockIdx.x + 1) * per;
-  if (border >= total) return;
-  if (w == 0) {                                      // one warp looks: the walk is instructions, not data
-    int next;
-    const Seg s = seg_at(a, a.cum_out, border, total, &next);
-    if (lane == 0) {
-      seg = s;
-      of_seg = stream_cut(a, s.start, s.units, per);
-    }
-  }
-  __syncthreads();
-  const Seg sg = seg;
-  const Cut cut = of_seg;
-  // Not cut (the border is at its start or in its lead), or cut before as well.
-  if (cut.first != static_cast<int>(blockIdx.x) || cut.last == cut.first) return;
-  const int first = cut.first, n = cut.last - cut.first + 1, slot0 = cut.slot;
-  for (int row0 = from; row0 < kChunkRows && sg.rt * a.tile_rows + row0 < a.rows; row0 += step) {
-    const auto record = [&](int k, int x) {
-      return a.rec + ((static_cast<int64_t>(first + k) * 2 + (k == 0 ? slot0 : 0)) * kChunkRows + row0 + x) * (kRecHead + D);
-    };
-    // The four rows side by side. Their records' heads first: lane 8 x + k looks at row x's record k, k + 8, ...
-    float M[kMergeRows];
-    {
-      float top = -INFINITY;
-      for (int k = lane & 7; k < n; k += 8) top = fmaxf(top, record(k, lane >> 3)[0]);
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll
-      for (int x = 0; x < kMergeRows; ++x) M[x] = __shfl_sync(0xffffffffu, top, 8 * x);
-    }
-    float y[kMergeRows][D / 32], l[kMergeRows];
-#pragma unroll
-    for (int x = 0; x < kMergeRows; ++x) {
-      l[x] = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) y[x][e] = 0.f;
-    }
-#pragma unroll 2
-    for (int k = 0; k < n; ++k)
-#pragma unroll
-      for (int x = 0; x < kMergeRows; ++x) {
-        const float* p = record(k, x);
-        const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M[x]);
-        l[x] = fmaf(p[1], f, l[x]);                    // a NaN of a row, whose maximum is -inf, stays
-        float z[D / 32];
-        if constexpr (D == 128) *reinterpret_cast<float4*>(z) = *reinterpret_cast<const float4*>(p + kRecHead + lane * 4);
-        else *reinterpret_cast<float2*>(z) = *reinterpret_cast<const float2*>(p + kRecHead + lane * 2);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) y[x][e] = fmaf(z[e], f, y[x][e]);
-      }
-#pragma unroll
-    for (int x = 0; x < kMergeRows; ++x) {
-      const int r = sg.rt * a.tile_rows + row0 + x;
-      if (r < a.rows)
-        put(sg.b, sg.kv, r, y[x], l[x] == 0.f ? 0.f : 1.f / l[x], l[x] == 0.f ? -INFINITY : (M[x] - kLift + log2f(l[x])) * kLn2);
-    }
-  }
-}
-
 template <int D, bool INT8>
 cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
   constexpr int smem = Smem<D>::kBytes;
@@ -753,9 +659,7 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_behind(cache8_merge_kernel<D>, dim3(kSms - 1 + kMergeEmpty, kMergeSplit), 256, st, a, kSms);
-  count_launch();
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_merge<D>(a, kSms, st);
 }
 
 }  // namespace

@@ -13,7 +13,10 @@
 // do not go the way of tq_cache8_chunk.cu, whose sums stay in tensor memory.
 //
 // Bound by the matrix instructions: 2 x 128 of them a warp and tile at d = 128,
-// fp32, or at d = 256, 1.23 ns each per SM.
+// fp32, or at d = 256, 1.23 ns each per SM, half of the time; the rest is the
+// conversion, the weights and the barriers between them. Measured, 512 rows of
+// two sequences of 8192 tokens: 8 KV heads of 4 fp32 heads, d = 128, 1058 us (by
+// eights of rows 2040); 4 KV heads, d = 256, bf16 615 us, fp32 1037 us.
 #include "tq_cache8_attn.cuh"
 
 namespace tq {
@@ -90,8 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_rows_kernel(AttnArgs a) {
   scan_counts<kThreads>(cum, reinterpret_cast<int*>(smem + L::kOffPart), a.batch, [&](int b) {
     return head_units(a, seq_len(a, b, blockIdx.x == 0)) * a.heads;
   });
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= a.batch; b += kThreads) a.cum_out[b] = cum[b];
+  if (tid == 0) a.cuts[blockIdx.x].n = 0;
   let_next_start();
   const int total = cum[a.batch];
   const int per = units_per_cta(a, total, gridDim.x);
@@ -367,7 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_rows_kernel(AttnArgs a) {
       }
     }
     // Out, or to the record of a stream that other CTAs share.
-    float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.head && u != u0 ? 1 : 0)) * kRowsTile * (kRecHead + D);
+    const bool second = sg.head && u != u0;          // the record's slot
+    if (tid == 0 && sg.head && !sg.whole) a.cuts[blockIdx.x] = cut_of(a, sg, second, per);
+    float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (second ? 1 : 0)) * kRowsTile * (kRecHead + D);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
@@ -408,7 +412,7 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return a.out_f32 ? launch_combine<D, true>(a, kSms, st) : launch_combine<D, false>(a, kSms, st);
+  return launch_merge<D>(a, kSms, st);
 }
 
 template <int D, bool WIDE>
@@ -418,7 +422,10 @@ cudaError_t launch_code(bool int8, const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-bool rows_supported(int d, bool f32, int rows) { return (f32 || d == 256) && rows > 64; }
+// Up to 64 rows the few-row kernel is the faster: two sequences of 8192 tokens, 8 KV heads, d = 128, fp32: 61 us with 64
+// rows against 75 here, and 86 with 68 rows there. d = 256, 4 KV heads: 52 against 64.
+constexpr int kRowsFrom = 64;
+bool rows_supported(int d, bool f32, int rows) { return (f32 || d == 256) && rows > kRowsFrom; }
 
 size_t rows_record_bytes(int d) { return sizeof(float) * kSms * 2 * kRowsTile * static_cast<size_t>(kRecHead + d); }
 
