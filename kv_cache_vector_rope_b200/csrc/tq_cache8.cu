@@ -6,6 +6,17 @@
 // theirs alone, so an item needs nothing from another and no atomics. The
 // blocks follow from prefix sums over the sequences, which every CTA forms for
 // itself from the lengths in device memory (a call needs no host copy of them).
+//
+// The scale is the least power of two that brings the block's largest value
+// into the codes' range, so that a code times its scale is exact in fp32 and
+// bf16 and a block whose values grow is coded anew from its codes alone. New rows stay in registers between the search for the largest
+// value and the rounding: each is read once.
+//
+// Bound by memory, less what the dependent start of an item costs (span, page,
+// old scale, rows). Measured, floor of the bytes at the copy's rate in brackets:
+// bf16 prompt of 8 x 8192 tokens, 8 heads of 128, written 45.6 us (35.7), read
+// back 43.9 us (35.7); one new token of 64 sequences 3.7 us, which is launch and
+// that chain of loads; 1000 tokens of 20 heads of 64 read as fp32 4.2 us (2.0).
 #include <type_traits>
 
 #include "tq_cache8.h"
@@ -406,8 +417,8 @@ cudaError_t launch_rows(const tq_cache8* c, tq_dtype dtype, RowsArgs a, int64_t 
   const int per_row = a.d / (WRITE || dtype == TQ_BF16 ? 8 : 4);
   a.row_magic = (1 << 20) / per_row + 1;
   // A warp per item where a warp holds an item's new rows in registers, since blocks are that small or the call's
-  // sequences bring so few tokens; else a CTA per item. (1000 tokens in blocks 
-  // of 16, 20 heads of 64, read back: 4.3 us against 8.3 with a CTA per item.)
+  // sequences bring so few tokens; else a CTA per item. (1000 tokens in blocks of 16, 20 heads of 64, read back: 4.3 us
+  // against 8.3 with a CTA per item.)
   const int64_t tokens = a.n / batch < c->block ? a.n / batch : c->block;
   const bool warps = tokens * a.d <= 32 * kKeep * 8;
   for (int64_t b0 = 0; b0 < batch; b0 += kC8Slice) {
