@@ -490,7 +490,8 @@ int64_t tq_cache8_bytes(int32_t d, int32_t heads, int32_t block, int64_t n_block
  *  table_stride  blocks of one sequence: a sequence holds at most
  *                table_stride * block tokens
  * Lengths the arrays do not allow set TQ_DEV_BAD_LENGTH; the tokens beyond are
- * left out. No two sequences of a call may write to the same page.
+ * left out. The pages that a call writes to must differ, those of one sequence
+ * among themselves too: a page named twice ends up with either's tokens.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA.
  * ---------------------------------------------------------------------- */
 tq_status tq_cache8_write(const tq_cache8* cache, tq_dtype dtype,
@@ -538,7 +539,12 @@ tq_status tq_cache8_read(const tq_cache8* cache, tq_dtype dtype,
  *  workspace     device scratch of tq_cache8_attention_workspace_bytes()
  *                bytes, 256-byte aligned; needs no initialisation. Calls that
  *                overlap on the GPU need one each.
- * Supported d: 64, 128, 256 (others: TQ_ERR_UNSUPPORTED). Errors:
+ * A NaN in a query makes its row NaN; with an infinity its row is NaN, or zeros
+ * where every score is -inf. Other rows are not touched by either. Waits
+ * inside the kernels are bounded: one that gives up sets TQ_DEV_TIMEOUT, and the
+ * outputs of that call are then undefined. The same call gives the same bits.
+ * Supported d: 64, 128, 256, table_stride * block up to 2^30 (others:
+ * TQ_ERR_UNSUPPORTED). Errors:
  * TQ_ERR_INVALID_ARG, TQ_ERR_WORKSPACE, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA.
  * ---------------------------------------------------------------------- */
 tq_status tq_cache8_attention(const tq_cache8* cache,

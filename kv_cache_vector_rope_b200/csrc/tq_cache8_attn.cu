@@ -840,6 +840,8 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
   if (!q || !out || !seq_lens) return fail(TQ_ERR_INVALID_ARG, "%s: NULL q, out or seq_lens", what);
   st = check_table8(cache, batch, table_stride, what);
   if (st != TQ_OK) return st;
+  if (table_stride * cache->block > (1 << 30))       // keys ahead of the last one are counted in 32 bits
+    return fail(TQ_ERR_UNSUPPORTED, "%s: sequences beyond 2^30 tokens", what);
   if (!block_table && table_stride * batch > cache->n_blocks)
     return fail(TQ_ERR_INVALID_ARG, "%s: without a block table the cache needs batch * table_stride blocks", what);
   if (!aligned(q, 16) || !aligned(out, 16) || !stride_ok(batch, q_batch_stride, 8) || !stride_ok(hq, q_head_stride, 8) ||

@@ -72,6 +72,11 @@ def test_attention_host_validation():
     assert "workspace" in tq.tq_last_error_string()
 
 
+def test_attention_refuses_sequences_that_32_bits_cannot_count():
+    assert _attend(_cache(block=128, n=1 << 24), stride=(1 << 23) + 1) == UNSUPPORTED
+    assert "2^30" in tq.tq_last_error_string()
+
+
 def test_sizes():
     assert tq.tq_cache8_bytes(128, 8, 64, 10) == 2 * 10 * 8 * (64 * 128 + 4)
     assert tq.tq_cache8_bytes(100, 8, 64, 10) == -1
