@@ -11,14 +11,14 @@
 //
 // A lane holds four consecutive values of a row and the four they are paired
 // with, so no value changes lanes. A warp takes the rows of one token, several
-// side by side and four sets of them in flight: the token's angles are formed
+// side by side and several sets of them in flight: the token's angles are formed
 // once by the warp (fp64 turns pos * base^(-2i/rot) / 2 pi, whose remainder goes
 // through sincospif: far positions lose whole turns only) and stay in registers
 // as products with the weights while the warp walks the token's heads.
 //
-// Bound by memory: 16384 tokens of 40 bf16 heads of 128 68.3 us (51.3 at the
-// copy's rate; two or three sets in flight 71 and 76, more CTAs 72 to 91), 1021
-// tokens of 40 fp32 heads of 64 5.6 us (3.2), 8 tokens 3.4 us, which is launch,
+// Bound by memory: 16384 tokens of 40 bf16 heads of 128 64.2 us (51.3 at the
+// copy's rate; more CTAs per SM 72 to 91 us), 1021
+// tokens of 40 fp32 heads of 64 6.0 us (3.2), 8 tokens 2.9 us, which is launch,
 // one load, the angles and one store, each waiting for the last.
 #include <cmath>
 
@@ -102,7 +102,11 @@ __device__ __forceinline__ void side_rows(const T* src, int hs, T* dst, int ohs,
                                           float eps, float inv_d, int e0, int e1, bool on, const float2 (&c)[2],
                                           const float2 (&sn)[2]) {
   constexpr int kRows = 32 / LPR;                    // rows of a warp side by side
-  constexpr int kSets = 4;
+  // bf16: two sets of rows while the next two are on their way; fp32, with twice the registers a set: four at once.
+  // (A prompt of 16384 tokens, 40 heads of 128: bf16 64.2 us against 68.3 with four at once; 8192 fp32 ones 64 us against
+  // 72 with two ahead.)
+  constexpr bool kAhead = sizeof(T) == 2;
+  constexpr int kSets = kAhead ? 2 : 4;
   const int sub = (threadIdx.x & 31) / LPR;
   float2 uc[2], vs[2], us[2], vc[2];
 #pragma unroll
@@ -120,18 +124,29 @@ __device__ __forceinline__ void side_rows(const T* src, int hs, T* dst, int ohs,
   src += e0;
   dst += e0;
   const int gap = e1 - e0;
-#pragma unroll 1
-  for (int r = r0 + sub; r - sub < r1; r += kRows * kSets) {
-    Vec<T> a[kSets], b[kSets];
+  Vec<T> na[kSets], nb[kSets];
+  const auto load = [&](int r) {
 #pragma unroll
     for (int s = 0; s < kSets; ++s) {
       const int row = r + s * kRows;
       if (on && row < r1) {
         const T* p = src + row * hs;
-        a[s].load(p);
-        b[s].load(p + gap);
+        na[s].load(p);
+        nb[s].load(p + gap);
       }
     }
+  };
+  if (kAhead) load(r0 + sub);
+#pragma unroll 1
+  for (int r = r0 + sub; r - sub < r1; r += kRows * kSets) {
+    if (!kAhead) load(r);
+    Vec<T> a[kSets], b[kSets];
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+      a[s] = na[s];
+      b[s] = nb[s];
+    }
+    if (kAhead) load(r + kRows * kSets);
 #pragma unroll
     for (int s = 0; s < kSets; ++s) {
       const int row = r + s * kRows;
