@@ -29,6 +29,10 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kTile = kRowsUnit;                     // keys at a time
 static_assert(kTile == 64 && kRowsTile == 16 * kWarps, "four groups of 16 keys, 16 rows a warp");
 
+// CTAs per SM: at d = 64 two, whose barriers and products overlap (512 fp32 rows of 2 x 8192 tokens 657 -> 559 us,
+// though 128 registers spill 200 bytes); at d = 128 two do not fit shared memory.
+constexpr int rows_ctas(int d) { return d <= 64 ? 2 : 1; }
+
 template <int D, bool WIDE>
 struct Smem {
   static constexpr int kOffQ = 0;                    // [limbs][128][D] halves
@@ -77,7 +81,7 @@ __device__ __forceinline__ int chunk_at(int row, int c) {
 }
 
 template <int D, bool INT8, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1) cache8_rows_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(AttnArgs a) {
   using L = Smem<D, WIDE>;
   constexpr int kLimbs = WIDE ? 2 : 1;
   constexpr int kPer = D / 64;                       // 16-byte pieces of K (and of V) a thread copies of a tile
@@ -405,14 +409,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_rows_kernel(AttnArgs a) {
 template <int D, bool INT8, bool WIDE>
 cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
   constexpr int smem = Smem<D, WIDE>::kBytes;
-  static_assert(smem <= 232448, "shared memory plan exceeds 227 KB");
+  static_assert(smem * rows_ctas(D) <= 233472 - 1024 * rows_ctas(D), "shared memory plan exceeds an SM's");
+  constexpr int grid = kSms * rows_ctas(D);
+  static_assert(grid <= kMaxRecs, "CTAs that the merge knows");
   cudaError_t e = cudaFuncSetAttribute(cache8_rows_kernel<D, INT8, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cache8_rows_kernel<D, INT8, WIDE><<<kSms, kThreads, smem, st>>>(a);
+  cache8_rows_kernel<D, INT8, WIDE><<<grid, kThreads, smem, st>>>(a);
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_merge<D>(a, kSms, st);
+  return launch_merge<D>(a, grid, st);
 }
 
 template <int D, bool WIDE>
@@ -427,7 +433,7 @@ cudaError_t launch_code(bool int8, const AttnArgs& a, cudaStream_t st) {
 constexpr int kRowsFrom = 64;
 bool rows_supported(int d, bool f32, int rows) { return (f32 || d == 256) && rows > kRowsFrom; }
 
-size_t rows_record_bytes(int d) { return sizeof(float) * kSms * 2 * kRowsTile * static_cast<size_t>(kRecHead + d); }
+size_t rows_record_bytes(int d) { return sizeof(float) * kSms * rows_ctas(d) * 2 * kRowsTile * static_cast<size_t>(kRecHead + d); }
 
 cudaError_t launch_rows(int d, bool int8, const AttnArgs& a, cudaStream_t st) {
   if (d == 64) return launch_code<64, true>(int8, a, st);
