@@ -61,6 +61,7 @@ struct AttnArgs {
   int64_t first_seq;
   int causal;
   int window;
+  bool alone;                                        // a CTA per stream, whole
   float scale2;                                      // softmax scale * log2 e
   void* out;
   int64_t o_bs, o_hs, o_rs;
@@ -149,6 +150,18 @@ __device__ __forceinline__ Seg seg_at(const AttnArgs& a, const int* cum, int u, 
   seg_fill(a, s, r, rel, u, uend, next);
   return s;
 }
+// All of stream x, in the order of (sequence, KV head, row tile).
+__device__ __forceinline__ Seg seg_alone(const AttnArgs& a, int x) {
+  Seg s;
+  int next;
+  const int h = a.tiles_div.of(x);
+  s.rt = x - h * a.row_tiles;
+  s.b = a.heads_div.of(h);
+  s.kv = h - s.b * a.heads;
+  s.n = seq_len(a, s.b, s.kv == 0 && s.rt == 0);
+  seg_fill(a, s, tile_range(a, s.n, s.rt), 0, 0, 0x7fffffff, &next);
+  return s;
+}
 // The segment behind `s`, which ends its stream at u < uend: the next stream that costs anything, from its start.
 __device__ __forceinline__ void seg_after(const AttnArgs& a, const int* cum, Seg& s, int u, int uend, int* next) {
   KeyRange r;
@@ -233,13 +246,13 @@ __device__ __forceinline__ void load_q16(const void* p, int64_t i, float* x) {
   }
 }
 
-// A warp's part of the rows without a key: it looks at kEmptyPairs (sequence, row tile) pairs from `pair` on and writes
+// A warp's part of the rows without a key: it looks at `pairs` (sequence, row tile) pairs from `pair` on and writes
 // zeros for rows row0, row0 + step, ... of those where no row sees a key, all heads.
 constexpr int kEmptyPairs = 4;
 template <int D>
-__device__ __forceinline__ void put_empty(const AttnArgs& a, int pair, int row0, int step) {
+__device__ __forceinline__ void put_empty(const AttnArgs& a, int pair, int row0, int step, int pairs = kEmptyPairs) {
   const int lane = threadIdx.x & 31;
-  for (int end = min(pair + kEmptyPairs, a.batch * a.row_tiles); pair < end; ++pair) {
+  for (int end = min(pair + pairs, a.batch * a.row_tiles); pair < end; ++pair) {
     const int b = a.tiles_div.of(pair), rt = pair - b * a.row_tiles;
     const int n = seq_len(a, b, false);
     if (n > 0 && tile_range(a, n, rt).units > 0) continue;

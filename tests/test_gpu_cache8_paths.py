@@ -65,9 +65,13 @@ def test_rows_and_types(code, d, group, nq, qd, od):
     lens = [321, 1, 0, 16, 47, 128, 2]
     s = _filled(lens, 2, d, 16, code, nq)
     q = _queries(s, len(lens), nq, 2 * group, d, qd)
-    for window in (0, 37):
-        out, lse = _attend(s, q, lens, od, window=window)
-        _check_attention(s, q, lens, out, lse, od, window=window)
+    # Once with a table that cannot hold longer sequences, once with room, where the streams are split between CTAs.
+    room = np.full((len(lens), 80), -1, np.int32)
+    room[:, :s.table.shape[1]] = s.table
+    for table in (s.table, room):
+        for window in (0, 37):
+            out, lse = _attend(s, q, lens, od, table=table, window=window)
+            _check_attention(s, q, lens, out, lse, od, window=window)
     assert int(s.status.item()) == 0
 
 
