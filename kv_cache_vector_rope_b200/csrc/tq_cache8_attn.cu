@@ -785,12 +785,13 @@ int rows_of(int d, int rows, bool qf, bool of, bool int8) {
   return rows > 8 && d <= 128 && !qf && !of ? 16 : 8;
 }
 
-// Whether each CTA takes one stream by itself, without the lengths' sums before it and the merge behind: where the
-// streams have CTAs enough and cannot be long. One token, d = 128, 8 streams of 100 keys: 5.6 us against 8.6 split over
-// the CTAs, of 400 8.4 against 9.5, of 777 11.4 against 9.7; 240 streams of 1000 keys 19 against 25.
+// Whether each CTA takes one stream by itself, without the lengths' sums before it and the merge behind: where there are
+// a few streams per CTA at most and none can be long. One token, d = 128, 8 streams of 100 keys: 5.6 us against 8.6 split
+// over the CTAs, of 400 8.4 against 9.5, of 777 11.4 against 9.7; 240 streams of 1000 keys 19 against 25; 512 of 100 12
+// against 16, of 1000 35 against 38; 2048 streams of 60 keys 41 against 40.
 bool streams_alone(int d, int64_t streams, int64_t most_keys) {
   const int ctas = kSms * (d == 256 ? Plan<256>::kCtas : Plan<128>::kCtas);
-  return streams <= ctas && most_keys * d <= (2 * streams > ctas ? 1024 : 512) * 128;
+  return streams <= 4 * ctas && most_keys * d <= (2 * streams > ctas ? 1024 : 512) * 128;
 }
 
 template <int D>

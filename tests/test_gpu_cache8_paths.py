@@ -174,6 +174,18 @@ def test_many_sequences_of_many_rows():
     _check_attention(s, q, lens, out, lse, "bf16")
 
 
+@pytest.mark.parametrize("b", [700, 1300])
+def test_many_sequences_of_one_row(b):
+    # More than one launch takes, each a CTA's own and dealt out.
+    lens = [int(x) for x in np.random.default_rng(b).integers(0, 40, b)]
+    s = Setup(b, [max(n, 1) for n in lens], 1, 128, 16, "e4m3")
+    s.write(lens, [0] * b)
+    q = _queries(s, b, 1, 3, 128, "bf16")
+    out, lse = _attend(s, q, lens)
+    assert int(s.status.item()) == 0
+    _check_attention(s, q, lens, out, lse, "bf16")
+
+
 @pytest.mark.parametrize("nq,code,d", [(1, "e4m3", 128), (1, "int8", 256), (80, "e4m3", 128)])
 def test_waits_that_run_out_are_reported_and_leave_nothing_behind(monkeypatch, nq, code, d):
     monkeypatch.delenv("TQ_TEST_WAIT_NS", raising=False)
