@@ -25,7 +25,7 @@
 // eight query rows as the columns, which suits the few rows of a step: every
 // 8-bit code is exactly a half, and a query row is scaled by a power of two
 // into half's range (exact for bf16; fp32 queries and fp32 outputs use two
-// half limbs for q and for p). The contraction index of both products is
+// half limbs for q and for p). Weights carry the octaves of the value scale over a unit of the row's own (Weigh). The contraction index of both products is
 // permuted so that a lane's operands are 16 contiguous bytes of the cache.
 //
 // Up to four rows over int8 codes multiply the bytes as they are (16x8x32): q in
@@ -131,8 +131,9 @@ struct Smem {
   static constexpr int kBetween = kQBytes > kAccBytes ? 0 : kAccBytes - kQBytes;
   static constexpr int kOffM = kOffQ + 2 * kQBytes + kBetween;
   static constexpr int kOffL = kOffM + 4 * kAtWarps * kRows;
-  static constexpr int kOffTop = kOffL + 4 * kAtWarps * kRows;   // float [2][kRows]: merged maximum and sum
-  static constexpr int kOffRow = kOffTop + 8 * kRows;            // [2] per row: score factor, first key, end
+  static constexpr int kOffUnit = kOffL + 4 * kAtWarps * kRows;  // bytes [kRows][warps]: octaves of the sums' units, and 128
+  static constexpr int kOffTop = kOffUnit + kAtWarps * kRows;    // float [3][kRows]: merged maximum, sum and unit
+  static constexpr int kOffRow = kOffTop + 12 * kRows;           // [2] per row: score factor, first key, end
   static constexpr int kOffBar = kOffRow + 24 * kRows;
   static constexpr int kOffPart = kOffBar + 8 * kAtWarps * Plan<D>::kGroups;
   static constexpr int kOffCum = kOffPart + 4 * kAtWarps;
@@ -180,12 +181,14 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
   constexpr int QL = QF ? 2 : 1, QN = T::kOps, NJ = T::kCols, kTile = T::kTile, kRows = T::kRows;
   constexpr int NE = 2 * NJ;                         // scores of a lane per tile: keys g and g + 8
   constexpr bool kQRegs = NT * QN <= 8;              // few enough to hold in registers
+  constexpr uint32_t kMagnitude = INT8 ? 0xffffffffu : 0x7f7f7f7fu;      // the bits that say whether a code is zero
   using L = typename T::Plan;
   constexpr int kStage = G * L::kGroup;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   float* sm_m = reinterpret_cast<float*>(smem + L::kOffM);
   float* sm_l = reinterpret_cast<float*>(smem + L::kOffL);
+  unsigned char* sm_unit = smem + L::kOffUnit;       // octaves within [-127, 122]
   float* sm_top = reinterpret_cast<float*>(smem + L::kOffTop);
   int* cum = reinterpret_cast<int*>(smem + L::kOffCum);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
   // which `issued` are being copied. Pages and scales of 32 groups at a time, one per lane, the next 32 loaded ahead.
   Seg sg{};
   int u = u0, next = u0, k0 = 0, turns = 0, issued = 0, pg = 0, pg_next = 0;
-  float sc_k = 0.f, sc_v = 0.f;
+  float sc_k = 0.f, sc_v = 0.f;                      // the value scale as its octaves
   const auto key_of = [&](int x) { return k0 + x / G * kStep + x % G * 16; };
   const auto load_page = [&](int x) {
     return key_of(x) < sg.t1 ? static_cast<int>(page_of(a, sg.b, key_of(x) >> a.block_log2)) : -1;
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         step(st);
       }
     sc_k = load_scale(a.ks, pg);
-    sc_v = load_scale(a.vs, pg);
+    sc_v = octaves(load_scale(a.vs, pg));
   };
   // Queries of the segment at hand, for buffer `buf`: the last NT warps, which have the fewest keys, prepare a tile's
   // operands each; lane (g, t) holds column g's coordinates of its chunks.
@@ -371,19 +374,48 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       for (int x = 0; x < NT * QN; ++x) qr[x] = sm_q[x * 32 + lane];
     }
     float acc[NT][MT][4];
-    float m[NT][NJ], l[NT][NJ];
-    float vrun = 1.17549435e-38f;                    // the sums are in units of this value scale
-    float vinv = 0.f;                                // 1 / vrun, once a group has set it
+    float l[NT][NJ];
+    // The rows' m and mv, and what follows from them: two tiles' do not fit the registers and lie where the warp's maxima
+    // and sums go at the end (twelve rows over 8 x 32768 keys: 149 us in registers).
+    constexpr bool kHold = NT == 1;
+    float mh[kHold ? NT : 1][kHold ? NJ : 1], mvh[kHold ? NT : 1][kHold ? NJ : 1];
+    const auto m_of = [&](int nt, int j) { return kHold ? mh[kHold ? nt : 0][kHold ? j : 0] : sm_m[w * kRows + row_of(nt, j)]; };
+    const auto mv_of = [&](int nt, int j) { return kHold ? mvh[kHold ? nt : 0][kHold ? j : 0] : sm_l[w * kRows + row_of(nt, j)]; };
+    const auto set_m = [&](int nt, int j, float x, float y) {
+      if (kHold) {
+        mh[kHold ? nt : 0][kHold ? j : 0] = x;
+        mvh[kHold ? nt : 0][kHold ? j : 0] = y;
+      } else if (g == 0) {
+        sm_m[w * kRows + row_of(nt, j)] = x;
+        sm_l[w * kRows + row_of(nt, j)] = y;
+      }
+    };
+    Weigh wg[kHold ? G : 1][kHold ? NT : 1][kHold ? NJ : 1];     // for value scales of 2^lv
+    float lv[G];
+    const auto weigh_of = [&](int x, int nt, int j) { return kHold ? wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] : weigh(m_of(nt, j), mv_of(nt, j), lv[x]); };
+    const auto weigh_all = [&] {
+      if (!kHold) return;
+#pragma unroll
+      for (int x = 0; x < G; ++x)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] = weigh(m_of(nt, j), mv_of(nt, j), lv[x]);
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        m[nt][j] = -INFINITY;
+        set_m(nt, j, -INFINITY, -INFINITY);
         l[nt][j] = 0.f;
       }
 #pragma unroll
       for (int x = 0; x < MT; ++x) acc[nt][x][0] = acc[nt][x][1] = acc[nt][x][2] = acc[nt][x][3] = 0.f;
     }
+    if (!kHold) __syncwarp();
+#pragma unroll
+    for (int x = 0; x < G; ++x) lv[x] = 0.f;
+    weigh_all();
     for (int i = 0; i < turns; ++i) {
       constexpr int kBatch = 32 / G;                 // turns of a batch of pages
       const int rel = i % kBatch;
@@ -395,7 +427,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       }
       if (rel == kBatch / 4) {
         nx_k = load_scale(a.ks, pg_next);
-        nx_v = load_scale(a.vs, pg_next);
+        nx_v = octaves(load_scale(a.vs, pg_next));
       }
       if (!dead && !mbar_wait(bar + at, phase, a.wait_ns)) {
         dead = true;
@@ -410,12 +442,15 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         break;
       }
       const int key0 = k0 + i * kStep;               // group x: 16 keys from key0 + 16 x
-      float ks[G], vs[G];
+      float ks[G];
+      bool same = true;
       int known[G];                                  // the end of the keys that may be read; 0 with a bad page
 #pragma unroll
       for (int x = 0; x < G; ++x) {
         ks[x] = __shfl_sync(0xffffffffu, sc_k, G * rel + x);
-        vs[x] = __shfl_sync(0xffffffffu, sc_v, G * rel + x);
+        const float to = __shfl_sync(0xffffffffu, sc_v, G * rel + x);
+        same &= to == lv[x];
+        lv[x] = to;
         const bool good = ok(__shfl_sync(0xffffffffu, pg, G * rel + x));
         known[x] = good ? sg.n : 0;
         if (!good && key0 + 16 * x < sg.t1 && lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_BLOCK);
@@ -513,15 +548,17 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         }
       }
       values();                                      // behind the scores: the keys' registers are free
+      if (!same) weigh_all();
       bool rise = false;
-      float vtop = vs[0];
 #pragma unroll
       for (int x = 0; x < G; ++x) {
         const int key1 = key0 + 16 * x;
         const bool full = key1 >= lo_max && key1 + 16 <= min(hi_min, known[x]);
-        vtop = fmaxf(vtop, vs[x]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          float lim[NJ];
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) lim[j] = weigh_of(x, nt, j).lim;
 #pragma unroll
           for (int e = 0; e < NE; ++e) {
             s[x][nt][e] *= cq[nt][e % NJ] * ks[x];
@@ -529,29 +566,84 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
               const int key = key1 + g + 8 * (e / NJ), row = row_of(nt, e % NJ);
               if (key < sm_lo[row] || key >= min(sm_hi[row], known[x])) s[x][nt][e] = -INFINITY;
             }
-            rise |= s[x][nt][e] > m[nt][e % NJ] + kSlack;
+            rise |= s[x][nt][e] > lim[e % NJ];
           }
         }
       }
-      if (__any_sync(0xffffffffu, rise || vtop > vrun)) {
-        const float fv = vtop > vrun ? vrun / vtop : 1.f;
-        vrun = fmaxf(vrun, vtop);
-        vinv = 1.f / vrun;
+      if (__any_sync(0xffffffffu, rise)) {
+        // Where each lane finds a code in its part of every value that may be read, no key is without one.
+        bool plain = true;
+#pragma unroll
+        for (int x = 0; x < G; ++x) {
+          plain &= lv[x] == lv[0];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t any = 0u;
+#pragma unroll
+            for (int y = 0; y < VW; ++y) any |= vw[x][j][y];
+            plain &= (any & kMagnitude) != 0u || key0 + 16 * x + 2 * t + (j & 1) + 8 * (j >> 1) >= known[x];
+          }
+        }
+        plain = __all_sync(0xffffffffu, plain);
+        uint32_t none = 0u;                          // bits 2 x + h: the lane's key g + 8 h of group x has no such code
+        if (__builtin_expect(!plain, 0)) {
+#pragma unroll
+          for (int x = 0; x < G; ++x)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t some[2];                        // bit t of some[j]: key 2 t + j + 8 h
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint32_t any = 0u;
+#pragma unroll
+                for (int y = 0; y < VW; ++y) any |= vw[x][2 * h + j][y];
+                some[j] = __ballot_sync(0xffffffffu, (any & kMagnitude) != 0u);
+                some[j] |= some[j] >> 16;
+                some[j] |= some[j] >> 8;
+                some[j] |= some[j] >> 4;
+              }
+              none |= (~(((g & 1) ? some[1] : some[0]) >> (g >> 1)) & 1u) << (2 * x + h);
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float f[NJ];
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            float x = fmaxf(s[0][nt][j], s[0][nt][j + NJ]);
+            float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
-            for (int y = 1; y < G; ++y) x = fmaxf(x, fmaxf(s[y][nt][j], s[y][nt][j + NJ]));
+            for (int x = 0; x < G; ++x)
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            const float mn = fmaxf(m[nt][j], x);
-            f[j] = mn == m[nt][j] ? 1.f : fast_exp2(m[nt][j] - mn);
-            m[nt][j] = mn;
-            l[nt][j] *= f[j];
-            f[j] *= fv;
+              for (int h = 0; h < 2; ++h) {
+                const float y = s[x][nt][j + NJ * h];
+                top = fmaxf(top, y);
+                if (!((none >> (2 * x + h)) & 1)) topv = fmaxf(topv, y + lv[x]);
+              }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (plain) {
+              topv = top + lv[0];
+            } else {
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
+            }
+            const float m = m_of(nt, j), mv = mv_of(nt, j), mn = fmaxf(m, rintf(top)), mvn = fmaxf(mv, rintf(topv));
+            f[j] = unit_step(m, mv, mn, mvn);
+            if (mn != m) l[nt][j] *= fast_exp2(m - mn);
+            if (!kHold) __syncwarp();
+            set_m(nt, j, mn, mvn);
+            // Keys without a value: counted here, then left out.
+            if (none != 0u) {
+#pragma unroll
+              for (int x = 0; x < G; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float& y = s[x][nt][j + NJ * h];
+                  if (!((none >> (2 * x + h)) & 1) || y == -INFINITY) continue;
+                  l[nt][j] += fast_exp2((y - mn) + kLift);
+                  y = -INFINITY;
+                }
+            }
           }
 #pragma unroll
           for (int x = 0; x < MT; ++x) {
@@ -559,26 +651,29 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
             for (int e = 0; e < 4; ++e) acc[nt][x][e] *= f[e % NJ];
           }
         }
+        if (kHold) weigh_all();
+        else __syncwarp();
       }
       uint32_t ph0[G][NT][2], ph1[G][NT][2];
 #pragma unroll
       for (int x = 0; x < G; ++x) {
-        const float vr = vs[x] * vinv;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float p[NE];
 #pragma unroll
-          for (int e = 0; e < NE; ++e) {
-            // A row that has seen no key yet has m = -inf: its weights are 0, not e^(-inf + inf).
-            p[e] = s[x][nt][e] == -INFINITY ? 0.f : fast_exp2(s[x][nt][e] - m[nt][e % NJ] + kLift);
-            l[nt][e % NJ] += p[e];
-            p[e] *= vr;
+          for (int j = 0; j < NJ; ++j) {
+            const Weigh y = weigh_of(x, nt, j);
+#pragma unroll
+            for (int e = j; e < NE; e += NJ) {
+              p[e] = fast_exp2(s[x][nt][e] + y.off);
+              l[nt][j] = fmaf(p[e], y.inv, l[nt][j]);
+            }
           }
           if constexpr (QUAD) {
             // A row's two columns: the weight and what its half leaves of it.
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              ph0[x][nt][e] = transpose8(pack_half(p[e], OF ? p[e] - __half2float(__float2half_rn(p[e])) : 0.f));
+              ph0[x][nt][e] = transpose8(pack_half(p[e], OF ? (p[e] - __half2float(__float2half_rn(p[e]))) * kLimb : 0.f));
           } else {
             const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
             ph0[x][nt][0] = transpose8(h0);
@@ -586,8 +681,8 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
             if (OF) {
               const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h0));
               const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-              ph1[x][nt][0] = transpose8(pack_half(p[0] - y.x, p[1] - y.y));
-              ph1[x][nt][1] = transpose8(pack_half(p[2] - z.x, p[3] - z.y));
+              ph1[x][nt][0] = transpose8(pack_half((p[0] - y.x) * kLimb, (p[1] - y.y) * kLimb));
+              ph1[x][nt][1] = transpose8(pack_half((p[2] - z.x) * kLimb, (p[3] - z.y) * kLimb));
             }
           }
         }
@@ -596,7 +691,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       for (int c = 0; c < VW; ++c) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float y[NT][4];
+          float y[NT][4], z[NT][4];                    // of the weights' halves, and of their second ones
 #pragma unroll
           for (int x = 0; x < G; ++x) {
             // Coordinate pairs of two keys side by side: (key 2t, key 2t + 1) per half pair.
@@ -607,10 +702,12 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               if (OF) {
-                const uint32_t(&first)[2] = QUAD ? ph0[x][nt] : ph1[x][nt];
-                if (x == 0) mma_f16_new(y[nt], a0, a1, a2, a3, first[0], first[1]);
-                else mma_f16(y[nt], a0, a1, a2, a3, first[0], first[1]);
-                if (!QUAD) mma_f16(y[nt], a0, a1, a2, a3, ph0[x][nt][0], ph0[x][nt][1]);
+                if (x == 0) mma_f16_new(y[nt], a0, a1, a2, a3, ph0[x][nt][0], ph0[x][nt][1]);
+                else mma_f16(y[nt], a0, a1, a2, a3, ph0[x][nt][0], ph0[x][nt][1]);
+                if (!QUAD) {
+                  if (x == 0) mma_f16_new(z[nt], a0, a1, a2, a3, ph1[x][nt][0], ph1[x][nt][1]);
+                  else mma_f16(z[nt], a0, a1, a2, a3, ph1[x][nt][0], ph1[x][nt][1]);
+                }
               } else {
                 mma_f16(acc[nt][2 * c + h], a0, a1, a2, a3, ph0[x][nt][0], ph0[x][nt][1]);
               }
@@ -620,7 +717,10 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nt][2 * c + h][e] += y[nt][e];
+              for (int e = 0; e < 4; ++e) {
+                acc[nt][2 * c + h][e] += y[nt][e];
+                if (!QUAD) acc[nt][2 * c + h][e] = fmaf(z[nt][e], 1.f / kLimb, acc[nt][2 * c + h][e]);
+              }
           }
         }
       }
@@ -639,6 +739,15 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     open();
     if (u < u1) prepare(buf ^ 1);
     // Merge the warps: maxima and sums, then the value sums a piece at a time.
+    float m[NT][NJ], unit[NT][NJ];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        m[nt][j] = m_of(nt, j);
+        unit[nt][j] = unit_of(m[nt][j], mv_of(nt, j));
+      }
+    if (!kHold) __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -649,27 +758,39 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         if (g == 0) {
           sm_m[w * kRows + row_of(nt, j)] = m[nt][j];
           sm_l[w * kRows + row_of(nt, j)] = x;
+          sm_unit[row_of(nt, j) * kAtWarps + w] = static_cast<unsigned char>(__float_as_uint(unit[nt][j] + 12583040.f));
         }
       }
     __syncthreads();
     if (tid < kRows) {
-      float M = -INFINITY, sum = 0.f;
+      float M = -INFINITY, MV = -INFINITY, sum = 0.f;
+      const uint2 units = reinterpret_cast<const uint2*>(sm_unit)[tid];
+      static_assert(kAtWarps == 8, "a byte for each warp");
 #pragma unroll
-      for (int k = 0; k < kAtWarps; ++k) M = fmaxf(M, sm_m[k * kRows + tid]);
+      for (int k = 0; k < kAtWarps; ++k) {
+        const float y = sm_m[k * kRows + tid];
+        M = fmaxf(M, y);
+        MV = fmaxf(MV, y + (__uint_as_float(__byte_perm(k < 4 ? units.x : units.y, 0x4b000000u, 0x7550 + k % 4)) - 8388736.f));
+      }
 #pragma unroll
       for (int k = 0; k < kAtWarps; ++k)
         if (sm_l[k * kRows + tid] != 0.f)            // also with a NaN in the row, whose maximum is -inf
           sum += sm_l[k * kRows + tid] * fast_exp2(sm_m[k * kRows + tid] - M);
       sm_top[tid] = M;
       sm_top[kRows + tid] = sum;
+      sm_top[2 * kRows + tid] = unit_of(M, MV);
     }
     __syncthreads();
     float f[NT][NJ];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        f[nt][j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - sm_top[row_of(nt, j)]) * vrun;
+      for (int j = 0; j < NJ; ++j) {
+        const int row = row_of(nt, j);
+        f[nt][j] = m[nt][j] == -INFINITY
+                       ? 0.f
+                       : fast_exp2((m[nt][j] - sm_top[row]) + (unit[nt][j] - sm_top[2 * kRows + row]));
+      }
     const bool second = was.head && was_u != u0;     // the record's slot
     if (tid == 0 && was.head && !was.whole) a.cuts[blockIdx.x] = cut_of(a, was, second, per);
     float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (second ? 1 : 0)) * kRows * (kRecHead + D);
@@ -683,8 +804,8 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         const int nt = (p0 + p) / MT, x = (p0 + p) % MT;
         float* to = sums + ((w * kPieces + p) * 32 + lane) * kVals;
         if constexpr (QUAD)                          // the two limbs' columns are one row's
-          *reinterpret_cast<float2*>(to) = make_float2((acc[nt][x][0] + acc[nt][x][1]) * f[nt][0],
-                                                       (acc[nt][x][2] + acc[nt][x][3]) * f[nt][0]);
+          *reinterpret_cast<float2*>(to) = make_float2(fmaf(acc[nt][x][1], 1.f / kLimb, acc[nt][x][0]) * f[nt][0],
+                                                       fmaf(acc[nt][x][3], 1.f / kLimb, acc[nt][x][2]) * f[nt][0]);
         else
           *reinterpret_cast<float4*>(to) = make_float4(acc[nt][x][0] * f[nt][0], acc[nt][x][1] * f[nt][NJ - 1],
                                                        acc[nt][x][2] * f[nt][0], acc[nt][x][3] * f[nt][NJ - 1]);
@@ -701,11 +822,11 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         const int dim = (VW >= 4 ? 16 * (gg + 8 * (wd / 4)) + 4 * (wd % 4) : 8 * gg + 4 * wd) + 2 * (x & 1) + c / NJ;
         const int row = nt * kTile + (QUAD ? ln & 3 : 2 * (ln & 3) + c % NJ), r = was.rt * kRows + row;
         if (r < a.rows) {
-          const float M = sm_top[row], sum = sm_top[kRows + row];
+          const float M = sm_top[row], sum = sm_top[kRows + row], octaves = sm_top[2 * kRows + row];
           if (was.whole) {
             const int i = a.group_div.of(r), hq = was.kv * a.group + r - i * a.group;
             const int64_t at = (a.first_seq + was.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + dim;
-            const float o = sum == 0.f ? 0.f : val / sum;
+            const float o = sum == 0.f ? 0.f : val / sum * pow2_whole(octaves);
             if (OF) static_cast<float*>(a.out)[at] = o;
             else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
             if (a.lse && dim == 0)
@@ -716,6 +837,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
             if (dim == 0) {
               rec[row * (kRecHead + D)] = M;
               rec[row * (kRecHead + D) + 1] = sum;
+              rec[row * (kRecHead + D) + 2] = octaves;
             }
           }
         }

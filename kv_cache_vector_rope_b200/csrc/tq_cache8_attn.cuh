@@ -16,7 +16,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // running maximum m is moved only when a score exceeds it by kSlack octaves.
 constexpr float kLift = 6.f;
 constexpr float kSlack = 8.f;
-// A partial record: per row its maximum, its sum, two unused floats, d value sums.
+// A partial record: per row its maximum, its sum, the exponent of its value sums' unit, an unused float, d value sums.
 constexpr int kRecHead = 4;
 constexpr int kMaxRecs = 2 * kSms;                   // CTAs that may leave records of one stream
 
@@ -208,6 +208,45 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Value scales. A row's value sums take the weights 2^(s - m + kLift) times the block's value scale, as halves, which
+// end at 2^-24: what a key adds must be small beside the row's largest addend, not beside the largest scale, whose keys
+// may weigh nothing or lie where the row does not look. So the sums are in units of 2^(mv - m): m is the maximum of the
+// scores s (in octaves) over the keys that the row has seen, mv that of s plus the octaves of the value scale over
+// those of them with a code that is not zero (a token behind which others share its block can leave them none), both
+// rounded to whole numbers, whose differences are exact. The largest addend is then about 2^kLift, later ones exceed it
+// by kSlack octaves at most before m and mv are moved, and a key is off by 2^-25 of a unit, 2^-30 of the largest addend
+// with codes of the type's largest. Where a weight has a second half, that is kept times 2^kLimb and ends as far below.
+constexpr float kLimb = 2048.f;                      // 2^11
+constexpr float kNoUnit = -127.f;                    // of sums that have no addend yet: below every other
+__device__ __forceinline__ float octaves(float scale) {          // of a power of two; below all of them for 0
+  return __uint_as_float(0x4b000000u | (__float_as_uint(scale) >> 23)) - (8388608.f + 127.f);
+}
+__device__ __forceinline__ float pow2_whole(float x) {           // 2^x for a whole number x in [-126, 127]
+  return __uint_as_float(__float_as_uint(x + (12582912.f + 127.f)) << 23);
+}
+__device__ __forceinline__ float unit_of(float m, float mv) { return mv == -INFINITY ? kNoUnit : mv - m; }
+// How the weights of keys under a value scale of 2^lv are formed: 2^(s + off) goes into the value sums and, times inv,
+// into the sum of weights (one exponential for both: off carries d, the octaves of the scale over the unit, and inv is
+// 2^-d). d is at least -60, where nothing is left of a half and the weights of keys that count are still normal numbers.
+// A score above lim asks for a new m and mv: before the first addend every score. A row that has seen no key has m =
+// -inf, and every s is -inf too.
+struct Weigh {
+  float off, lim, inv;
+};
+__device__ __forceinline__ Weigh weigh(float m, float mv, float lv) {
+  const float d = fmaxf(lv - unit_of(m, mv), -60.f);
+  Weigh w;
+  w.off = m == -INFINITY ? 0.f : (d + kLift) - m;
+  w.lim = mv == -INFINITY ? -INFINITY : m + (kSlack - fmaxf(d, 0.f));
+  w.inv = pow2_whole(-fminf(d, 126.f));
+  return w;
+}
+// Factor of the value sums where (m, mv) become (mn, mvn).
+__device__ __forceinline__ float unit_step(float m, float mv, float mn, float mvn) {
+  if (mv == -INFINITY) return 1.f;                   // no addend so far
+  return fast_exp2((m == mn ? 0.f : m - mn) + (unit_of(m, mv) - unit_of(mn, mvn)));
+}
+
 // The low / high two codes of a word as two halves.
 template <bool INT8, bool HI>
 __device__ __forceinline__ uint32_t two_halves(uint32_t w) {
@@ -282,7 +321,7 @@ template <int D, bool OF>
 __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, int grid) {
   constexpr int kParts = kCbThreads / (D / 4);       // records in flight side by side
   __shared__ float wt[kMaxRecs];
-  __shared__ float red[2][kCbThreads / 32];
+  __shared__ float red[3][kCbThreads / 32];
   __shared__ float4 sums[kParts][D / 4];
   const int x0 = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
   wait_before();
@@ -293,28 +332,37 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
   const auto record = [&](int k) {
     return a.rec + ((static_cast<int64_t>(x0 + k) * 2 + (k == 0 ? cut.slot : 0)) * a.tile_rows + row) * (kRecHead + D);
   };
-  float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;    // n <= kMaxRecs <= 2 * kCbThreads
-  if (tid < n) {
-    const float* p = record(tid);
-    m0 = p[0];
-    l0 = p[1];
-  }
-  if (tid + kCbThreads < n) {
-    const float* p = record(tid + kCbThreads);
-    m1 = p[0];
-    l1 = p[1];
-  }
-  static_assert(kMaxRecs <= 2 * kCbThreads, "two records per thread");
-  const float mw = dev::warp_max(fmaxf(m0, m1));
-  if ((tid & 31) == 0) red[0][tid >> 5] = mw;
-  __syncthreads();
-  float M = -INFINITY;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, e[2] = {0.f, 0.f};   // n <= kMaxRecs <= 2 * kCbThreads
 #pragma unroll
-  for (int k = 0; k < kCbThreads / 32; ++k) M = fmaxf(M, red[0][k]);
-  const float w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M), w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
-  if (tid < n) wt[tid] = w0;
-  if (tid + kCbThreads < n) wt[tid + kCbThreads] = w1;
-  const float lw = dev::warp_sum(l0 * w0 + l1 * w1);   // a NaN of a row, whose maximum is -inf, stays
+  for (int y = 0; y < 2; ++y)
+    if (tid + y * kCbThreads < n) {
+      const float4 h = *reinterpret_cast<const float4*>(record(tid + y * kCbThreads));
+      m[y] = h.x;
+      l[y] = h.y;
+      e[y] = h.z;
+    }
+  static_assert(kMaxRecs <= 2 * kCbThreads, "two records per thread");
+  const float mw = dev::warp_max(fmaxf(m[0], m[1])), ew = dev::warp_max(fmaxf(m[0] + e[0], m[1] + e[1]));
+  if ((tid & 31) == 0) {
+    red[0][tid >> 5] = mw;
+    red[2][tid >> 5] = ew;
+  }
+  __syncthreads();
+  float M = -INFINITY, MV = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kCbThreads / 32; ++k) {
+    M = fmaxf(M, red[0][k]);
+    MV = fmaxf(MV, red[2][k]);
+  }
+  const float unit = unit_of(M, MV);                 // of the merged sums
+  float lt = 0.f;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const float by = m[y] == -INFINITY ? 0.f : m[y] - M;
+    lt += l[y] * (m[y] == -INFINITY ? 0.f : fast_exp2(by));      // a NaN of a row, whose maximum is -inf, stays
+    if (tid + y * kCbThreads < n) wt[tid + y * kCbThreads] = m[y] == -INFINITY ? 0.f : fast_exp2(by + (e[y] - unit));
+  }
+  const float lw = dev::warp_sum(lt);
   if ((tid & 31) == 0) red[1][tid >> 5] = lw;
   __syncthreads();
   float L = 0.f;
@@ -347,7 +395,7 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
   const float o[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float y = L == 0.f ? 0.f : o[k] / L;
+    const float y = L == 0.f ? 0.f : o[k] / L * pow2_whole(unit);
     if (OF) static_cast<float*>(a.out)[at + k] = y;
     else static_cast<__nv_bfloat16*>(a.out)[at + k] = __float2bfloat16_rn(y);
   }
@@ -401,14 +449,25 @@ __global__ void __launch_bounds__(kMergeThreads, D == 256 ? 3 : 4) cache8_merge_
     const auto record = [&](int k, int x) {
       return a.rec + ((static_cast<int64_t>(x0 + k) * 2 + (k == 0 ? cut.slot : 0)) * a.tile_rows + row0 + x) * (kRecHead + D);
     };
-    float M[kMergeRows];
+    float M[kMergeRows], unit[kMergeRows];
     {
-      float top = -INFINITY;
-      for (int k = lane & 7; k < n; k += 8) top = fmaxf(top, record(k, lane >> 3)[0]);
+      float top = -INFINITY, topv = -INFINITY;
+      for (int k = lane & 7; k < n; k += 8) {
+        const float4 h = *reinterpret_cast<const float4*>(record(k, lane >> 3));
+        top = fmaxf(top, h.x);
+        topv = fmaxf(topv, h.x + h.z);
+      }
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 1; o < 8; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
+      }
+      topv = unit_of(top, topv);
 #pragma unroll
-      for (int x = 0; x < kMergeRows; ++x) M[x] = __shfl_sync(0xffffffffu, top, 8 * x);
+      for (int x = 0; x < kMergeRows; ++x) {
+        M[x] = __shfl_sync(0xffffffffu, top, 8 * x);
+        unit[x] = __shfl_sync(0xffffffffu, topv, 8 * x);
+      }
     }
     float y[kMergeRows][E], l[kMergeRows];
 #pragma unroll
@@ -422,8 +481,9 @@ __global__ void __launch_bounds__(kMergeThreads, D == 256 ? 3 : 4) cache8_merge_
 #pragma unroll
       for (int x = 0; x < kMergeRows; ++x) {
         const float* p = record(k, x);
-        const float m = p[0], f = m == -INFINITY ? 0.f : fast_exp2(m - M[x]);
-        l[x] = fmaf(p[1], f, l[x]);                  // a NaN of a row, whose maximum is -inf, stays
+        const float4 h = *reinterpret_cast<const float4*>(p);
+        const float by = h.x == -INFINITY ? -INFINITY : h.x - M[x], f = fast_exp2(by + (h.z - unit[x]));
+        l[x] = fmaf(h.y, fast_exp2(by), l[x]);       // a NaN of a row, whose maximum is -inf, stays
         float z[E];
         if constexpr (E == 2) {
           *reinterpret_cast<float2*>(z) = *reinterpret_cast<const float2*>(p + kRecHead + lane * 2);
@@ -441,7 +501,7 @@ __global__ void __launch_bounds__(kMergeThreads, D == 256 ? 3 : 4) cache8_merge_
       if (r >= a.rows) continue;
       const int i = a.group_div.of(r), hq = cut.kv * a.group + r - i * a.group;
       const int64_t at = (a.first_seq + cut.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + lane * E;
-      const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];
+      const float inv = l[x] == 0.f ? 0.f : 1.f / l[x] * pow2_whole(unit[x]);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         if (a.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + e) = make_float2(y[x][e] * inv, y[x][e + 1] * inv);

@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         if (!sg.whole) {
           rec[0] = m;
           rec[1] = l;
+          rec[2] = 0.f;
         } else if (a.lse) {
           a.lse[((a.first_seq + sg.b) * a.heads * a.group + hq) * a.nq + i] =
               l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2;

@@ -42,7 +42,8 @@ struct Smem {
   static constexpr int kOffRaw = kOffV + kTile * D * 2;          // K, V: [64][D] codes
   static constexpr int kOffScale = kOffRaw + 2 * kTile * D;      // float [2][K, V][4]
   static constexpr int kOffOk = kOffScale + 64;                  // int [2][4]
-  static constexpr int kOffRow = kOffOk + 32;                    // float [128]: score factors
+  static constexpr int kOffSome = kOffOk + 32;                   // bytes [64]: whether the key has a value code that is not zero
+  static constexpr int kOffRow = kOffSome + kTile;               // float [128]: score factors
   static constexpr int kOffPart = kOffRow + 4 * 128;
   static constexpr int kOffCum = kOffPart + 4 * kWarps;
   static constexpr int kBytes = kOffCum + 4 * (kRowsSlice + 1) + 128;  // and room to align the base
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
   const uint32_t base = smem_u32(smem);
   float* sm_scale = reinterpret_cast<float*>(smem + L::kOffScale);
   int* sm_ok = reinterpret_cast<int*>(smem + L::kOffOk);
+  unsigned char* sm_some = smem + L::kOffSome;
   float* sm_cq = reinterpret_cast<float*>(smem + L::kOffRow);
   int* cum = reinterpret_cast<int*>(smem + L::kOffCum);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -216,8 +218,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
     const int hi_min = any_row ? row_hi(a, sg.n, a.group_div.of(r0)) : 0, hi_max = any_row ? row_hi(a, sg.n, last) : 0;
     const int lo_min = row_lo(a, hi_min), lo_max = row_lo(a, hi_max);
     float acc[D / 8][4];
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float vrun = 1.17549435e-38f, vinv = 0.f;        // the sums are in units of vrun, a value scale
+    float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < D / 8; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
     float cq[2] = {0.f, 0.f};
@@ -240,6 +241,10 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
           uint4 y = *reinterpret_cast<const uint4*>(smem + (raw - base) + i * 4096 + kv * kTile * D);
           if (!real) y = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+          if (kv) {                                  // D / 16 lanes side by side hold a key
+            const uint32_t any = __ballot_sync(0xffffffffu, ((y.x | y.y | y.z | y.w) & (INT8 ? 0xffffffffu : 0x7f7f7f7fu)) != 0u);
+            if (piece == 0) sm_some[row] = ((any >> lane) & ((1u << (D / 16)) - 1u)) != 0u;
+          }
           uint32_t h[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -287,11 +292,9 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
       }
       const bool full = tile0 >= lo_max && tile0 + kTile <= hi_min && good[0] && good[1] && good[2] && good[3];
       bool rise = false;
-      float vtop = 0.f;
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt) {
         const float ks = scale[nt >> 1];
-        vtop = fmaxf(vtop, scale[4 + (nt >> 1)]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[nt][e] *= cq[e >> 1] * ks;
@@ -299,25 +302,43 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
             const int key = tile0 + 8 * nt + 2 * t + (e & 1);
             if (key < lo[e >> 1] || key >= hi[e >> 1] || !good[nt >> 1]) s[nt][e] = -INFINITY;
           }
-          rise |= s[nt][e] > m[e >> 1] + kSlack;
         }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          rise |= fmaxf(s[nt][2 * x], s[nt][2 * x + 1]) > weigh(m[x], mv[x], octaves(scale[4 + (nt >> 1)])).lim;
       }
-      if (__any_sync(0xffffffffu, rise || vtop > vrun)) {
-        const float fv = vtop > vrun ? vrun / vtop : 1.f;
-        vrun = fmaxf(vrun, vtop);
-        vinv = 1.f / vrun;
+      if (__any_sync(0xffffffffu, rise)) {
         float f[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float top = m[x];
+          float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
-          for (int nt = 0; nt < 8; ++nt) top = fmaxf(top, fmaxf(s[nt][2 * x], s[nt][2 * x + 1]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          f[x] = top == m[x] ? 1.f : fast_exp2(m[x] - top);
-          m[x] = top;
-          l[x] *= f[x];
-          f[x] *= fv;
+          for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              top = fmaxf(top, s[nt][2 * x + e]);
+              if (sm_some[8 * nt + 2 * t + e]) topv = fmaxf(topv, s[nt][2 * x + e] + octaves(scale[4 + (nt >> 1)]));
+            }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
+          }
+          const float mn = fmaxf(m[x], rintf(top)), mvn = fmaxf(mv[x], rintf(topv));
+          f[x] = unit_step(m[x], mv[x], mn, mvn);
+          if (mn != m[x]) l[x] *= fast_exp2(m[x] - mn);
+          m[x] = mn;
+          mv[x] = mvn;
+          // Keys without a value: counted here, then left out.
+#pragma unroll
+          for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& y = s[nt][2 * x + e];
+              if (sm_some[8 * nt + 2 * t + e] || y == -INFINITY) continue;
+              l[x] += fast_exp2((y - mn) + kLift);
+              y = -INFINITY;
+            }
         }
 #pragma unroll
         for (int x = 0; x < D / 8; ++x)
@@ -328,14 +349,16 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
       uint32_t pa[kLimbs][4][4];
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt) {
-        const float vr = scale[4 + (nt >> 1)] * vinv;
+        const float lv = octaves(scale[4 + (nt >> 1)]);
         float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // A row that has seen no key yet has m = -inf: its weights are 0, not e^(-inf + inf).
-          p[e] = s[nt][e] == -INFINITY ? 0.f : fast_exp2(s[nt][e] - m[e >> 1] + kLift);
-          l[e >> 1] += p[e];
-          p[e] *= vr;
+        for (int x = 0; x < 2; ++x) {
+          const Weigh y = weigh(m[x], mv[x], lv);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            p[2 * x + e] = fast_exp2(s[nt][2 * x + e] + y.off);
+            l[x] = fmaf(p[2 * x + e], y.inv, l[x]);
+          }
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -343,13 +366,13 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
           pa[0][nt >> 1][2 * (nt & 1) + x] = h;
           if constexpr (WIDE) {
             const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            pa[kLimbs - 1][nt >> 1][2 * (nt & 1) + x] = pack_half(p[2 * x] - y.x, p[2 * x + 1] - y.y);
+            pa[kLimbs - 1][nt >> 1][2 * (nt & 1) + x] = pack_half((p[2 * x] - y.x) * kLimb, (p[2 * x + 1] - y.y) * kLimb);
           }
         }
       }
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {             // 16 coordinates: two tiles of 8
-        float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, z[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           uint32_t vb[4];
@@ -357,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if constexpr (WIDE) {
-              mma(y[x], pa[kLimbs - 1][kk], vb[2 * x], vb[2 * x + 1]);
+              mma(z[x], pa[kLimbs - 1][kk], vb[2 * x], vb[2 * x + 1]);
               mma(y[x], pa[0][kk], vb[2 * x], vb[2 * x + 1]);
             } else {
               mma(acc[2 * c + x], pa[0][kk], vb[2 * x], vb[2 * x + 1]);
@@ -368,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
 #pragma unroll
           for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[2 * c + x][e] += y[x][e];
+            for (int e = 0; e < 4; ++e) acc[2 * c + x][e] = fmaf(z[x][e], 1.f / kLimb, acc[2 * c + x][e] + y[x][e]);
         }
       }
     }
@@ -384,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
       if (r >= a.rows) continue;
       const int i = a.group_div.of(r), hq = sg.kv * a.group + r - i * a.group;
       const int64_t at = (a.first_seq + sg.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + 2 * t;
-      const float by = sg.whole ? (l[x] == 0.f ? 0.f : vrun / l[x]) : vrun;
+      const float unit = unit_of(m[x], mv[x]), by = sg.whole ? (l[x] == 0.f ? 0.f : 1.f / l[x] * pow2_whole(unit)) : 1.f;
       float* to = rec + row * (kRecHead + D);
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -397,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
         if (!sg.whole) {
           to[0] = m[x];
           to[1] = l[x];
+          to[2] = unit;
         } else if (a.lse) {
           a.lse[((a.first_seq + sg.b) * a.heads * a.group + hq) * a.nq + i] =
               l[x] == 0.f ? -INFINITY : (m[x] - kLift + log2f(l[x])) * kLn2;
