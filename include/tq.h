@@ -544,11 +544,12 @@ tq_status tq_cache8_read(const tq_cache8* cache, tq_dtype dtype,
  * inside the kernels are bounded: one that gives up sets TQ_DEV_TIMEOUT, and the
  * outputs of that call are then undefined. The same call gives the same bits.
  * Sums and softmax statistics are fp32. A weight goes into the value sum as one
- * half for bf16 outputs (2^-12 of itself) and as two for fp32 outputs (2^-22).
+ * half for bf16 outputs (2^-11 of itself) and as two for fp32 outputs (2^-22).
  * What a key adds is beside that off by 2^-30 (2^-41) of the row's largest
  * product of a weight and a value scale times the largest code, over the keys
  * that the row sees and whose value codes are not all zero: scales of other
- * keys do not touch a row.
+ * keys do not touch a row. (With more than 64 bf16 rows per KV head, keys with
+ * codes that are all zero count too, unless their scale is 2^5 times the row's.)
  * Supported d: 64, 128, 256, table_stride * block up to 2^30 (others:
  * TQ_ERR_UNSUPPORTED). Errors:
  * TQ_ERR_INVALID_ARG, TQ_ERR_WORKSPACE, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA.

@@ -375,16 +375,16 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     }
     float acc[NT][MT][4];
     float l[NT][NJ];
-    // The rows' m and mv, and what follows from them: two tiles' do not fit the registers and lie where the warp's maxima
+    // The rows' m and e, and what follows from them: two tiles' do not fit the registers and lie where the warp's maxima
     // and sums go at the end (twelve rows over 8 x 32768 keys: 149 us in registers).
     constexpr bool kHold = NT == 1;
-    float mh[kHold ? NT : 1][kHold ? NJ : 1], mvh[kHold ? NT : 1][kHold ? NJ : 1];
+    float mh[kHold ? NT : 1][kHold ? NJ : 1], eh[kHold ? NT : 1][kHold ? NJ : 1];
     const auto m_of = [&](int nt, int j) { return kHold ? mh[kHold ? nt : 0][kHold ? j : 0] : sm_m[w * kRows + row_of(nt, j)]; };
-    const auto mv_of = [&](int nt, int j) { return kHold ? mvh[kHold ? nt : 0][kHold ? j : 0] : sm_l[w * kRows + row_of(nt, j)]; };
+    const auto e_of = [&](int nt, int j) { return kHold ? eh[kHold ? nt : 0][kHold ? j : 0] : sm_l[w * kRows + row_of(nt, j)]; };
     const auto set_m = [&](int nt, int j, float x, float y) {
       if (kHold) {
         mh[kHold ? nt : 0][kHold ? j : 0] = x;
-        mvh[kHold ? nt : 0][kHold ? j : 0] = y;
+        eh[kHold ? nt : 0][kHold ? j : 0] = y;
       } else if (g == 0) {
         sm_m[w * kRows + row_of(nt, j)] = x;
         sm_l[w * kRows + row_of(nt, j)] = y;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     };
     Weigh wg[kHold ? G : 1][kHold ? NT : 1][kHold ? NJ : 1];     // for value scales of 2^lv
     float lv[G];
-    const auto weigh_of = [&](int x, int nt, int j) { return kHold ? wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] : weigh(m_of(nt, j), mv_of(nt, j), lv[x]); };
+    const auto weigh_of = [&](int x, int nt, int j) { return kHold ? wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] : weigh(m_of(nt, j), e_of(nt, j), lv[x]); };
     const auto weigh_all = [&] {
       if (!kHold) return;
 #pragma unroll
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] = weigh(m_of(nt, j), mv_of(nt, j), lv[x]);
+          for (int j = 0; j < NJ; ++j) wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] = weigh(m_of(nt, j), e_of(nt, j), lv[x]);
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -610,28 +610,29 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
           float f[NJ];
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            float top = -INFINITY, topv = -INFINITY;
+            float top = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < G; ++x)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float y = s[x][nt][j + NJ * h];
-                top = fmaxf(top, y);
-                if (!((none >> (2 * x + h)) & 1)) topv = fmaxf(topv, y + lv[x]);
-              }
+            for (int x = 0; x < G; ++x) top = fmaxf(top, fmaxf(s[x][nt][j], s[x][nt][j + NJ]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (plain) {
-              topv = top + lv[0];
-            } else {
+            const float m = m_of(nt, j), e = e_of(nt, j), mn = fmaxf(m, rintf(top)), by = below(m, mn);
+            float topv = top == -INFINITY ? -INFINITY : below(top, mn) + lv[0];
+            if (!plain) {
+              topv = -INFINITY;
+#pragma unroll
+              for (int x = 0; x < G; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (!((none >> (2 * x + h)) & 1) && s[x][nt][j + NJ * h] > -INFINITY)
+                    topv = fmaxf(topv, below(s[x][nt][j + NJ * h], mn) + lv[x]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
             }
-            const float m = m_of(nt, j), mv = mv_of(nt, j), mn = fmaxf(m, rintf(top)), mvn = fmaxf(mv, rintf(topv));
-            f[j] = unit_step(m, mv, mn, mvn);
-            if (mn != m) l[nt][j] *= fast_exp2(m - mn);
+            const float en = fmaxf(e + by, rintf(topv));
+            f[j] = unit_step(m, e, mn, en);
+            l[nt][j] *= fast_exp2(by);
             if (!kHold) __syncwarp();
-            set_m(nt, j, mn, mvn);
+            set_m(nt, j, mn, en);
             // Keys without a value: counted here, then left out.
             if (none != 0u) {
 #pragma unroll
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
                 for (int h = 0; h < 2; ++h) {
                   float& y = s[x][nt][j + NJ * h];
                   if (!((none >> (2 * x + h)) & 1) || y == -INFINITY) continue;
-                  l[nt][j] += fast_exp2((y - mn) + kLift);
+                  l[nt][j] += fast_exp2((y - base_of(mn)) + kLift);
                   y = -INFINITY;
                 }
             }
@@ -663,9 +664,10 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
             const Weigh y = weigh_of(x, nt, j);
+            const float base = base_of(m_of(nt, j));
 #pragma unroll
             for (int e = j; e < NE; e += NJ) {
-              p[e] = fast_exp2(s[x][nt][e] + y.off);
+              p[e] = fast_exp2((s[x][nt][e] - base) + y.lift);
               l[nt][j] = fmaf(p[e], y.inv, l[nt][j]);
             }
           }
@@ -745,7 +747,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         m[nt][j] = m_of(nt, j);
-        unit[nt][j] = unit_of(m[nt][j], mv_of(nt, j));
+        unit[nt][j] = unit_of(e_of(nt, j));
       }
     if (!kHold) __syncwarp();
 #pragma unroll
@@ -763,22 +765,21 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       }
     __syncthreads();
     if (tid < kRows) {
-      float M = -INFINITY, MV = -INFINITY, sum = 0.f;
+      float M = -INFINITY, sum = 0.f, top = kNoUnit;
+#pragma unroll
+      for (int k = 0; k < kAtWarps; ++k) M = fmaxf(M, sm_m[k * kRows + tid]);
       const uint2 units = reinterpret_cast<const uint2*>(sm_unit)[tid];
       static_assert(kAtWarps == 8, "a byte for each warp");
 #pragma unroll
-      for (int k = 0; k < kAtWarps; ++k) {
-        const float y = sm_m[k * kRows + tid];
-        M = fmaxf(M, y);
-        MV = fmaxf(MV, y + (__uint_as_float(__byte_perm(k < 4 ? units.x : units.y, 0x4b000000u, 0x7550 + k % 4)) - 8388736.f));
-      }
-#pragma unroll
       for (int k = 0; k < kAtWarps; ++k)
-        if (sm_l[k * kRows + tid] != 0.f)            // also with a NaN in the row, whose maximum is -inf
-          sum += sm_l[k * kRows + tid] * fast_exp2(sm_m[k * kRows + tid] - M);
+        if (sm_l[k * kRows + tid] != 0.f) {          // also with a NaN in the row, whose maximum is -inf
+          const float by = below(sm_m[k * kRows + tid], M);
+          sum += sm_l[k * kRows + tid] * fast_exp2(by);
+          top = fmaxf(top, by + (__uint_as_float(__byte_perm(k < 4 ? units.x : units.y, 0x4b000000u, 0x7550 + k % 4)) - 8388736.f));
+        }
       sm_top[tid] = M;
       sm_top[kRows + tid] = sum;
-      sm_top[2 * kRows + tid] = unit_of(M, MV);
+      sm_top[2 * kRows + tid] = rintf(top);
     }
     __syncthreads();
     float f[NT][NJ];
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         const int row = row_of(nt, j);
         f[nt][j] = m[nt][j] == -INFINITY
                        ? 0.f
-                       : fast_exp2((m[nt][j] - sm_top[row]) + (unit[nt][j] - sm_top[2 * kRows + row]));
+                       : fast_exp2(below(m[nt][j], sm_top[row]) + (unit[nt][j] - sm_top[2 * kRows + row]));
       }
     const bool second = was.head && was_u != u0;     // the record's slot
     if (tid == 0 && was.head && !was.whole) a.cuts[blockIdx.x] = cut_of(a, was, second, per);

@@ -210,41 +210,45 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 // Value scales. A row's value sums take the weights 2^(s - m + kLift) times the block's value scale, as halves, which
 // end at 2^-24: what a key adds must be small beside the row's largest addend, not beside the largest scale, whose keys
-// may weigh nothing or lie where the row does not look. So the sums are in units of 2^(mv - m): m is the maximum of the
-// scores s (in octaves) over the keys that the row has seen, mv that of s plus the octaves of the value scale over
-// those of them with a code that is not zero (a token behind which others share its block can leave them none), both
-// rounded to whole numbers, whose differences are exact. The largest addend is then about 2^kLift, later ones exceed it
-// by kSlack octaves at most before m and mv are moved, and a key is off by 2^-25 of a unit, 2^-30 of the largest addend
-// with codes of the type's largest. Where a weight has a second half, that is kept times 2^kLimb and ends as far below.
-constexpr float kLimb = 2048.f;                      // 2^11
-constexpr float kNoUnit = -127.f;                    // of sums that have no addend yet: below every other
+// may weigh nothing or lie where the row does not look. So the sums are in units of 2^e: m is the maximum of the scores
+// s (in octaves) over the keys that the row has seen, e that of s - m plus the octaves of the value scale over those of
+// them with a code that is not zero (a large token can leave others of its block none), both rounded to whole numbers,
+// whose differences are exact. The largest addend is then about 2^kLift, later ones exceed it by kSlack octaves at most
+// before m and e are moved, and a key is off by 2^-25 of a unit, 2^-30 of the largest addend with codes of the type's
+// largest. Where a weight has a second half, that is kept times 2^11 and ends as far below. A row that has seen no key
+// has m = -inf, one without an addend e = -inf.
+constexpr float kLimb = 2048.f;
+constexpr float kNoUnit = -127.f;                    // of sums without an addend: below every other
 __device__ __forceinline__ float octaves(float scale) {          // of a power of two; below all of them for 0
   return __uint_as_float(0x4b000000u | (__float_as_uint(scale) >> 23)) - (8388608.f + 127.f);
 }
-__device__ __forceinline__ float pow2_whole(float x) {           // 2^x for a whole number x in [-126, 127]
+__device__ __forceinline__ float pow2_whole(float x) {           // 2^x for a whole number x in [-126, 127], 0 for -127
   return __uint_as_float(__float_as_uint(x + (12582912.f + 127.f)) << 23);
 }
-__device__ __forceinline__ float unit_of(float m, float mv) { return mv == -INFINITY ? kNoUnit : mv - m; }
-// How the weights of keys under a value scale of 2^lv are formed: 2^(s + off) goes into the value sums and, times inv,
-// into the sum of weights (one exponential for both: off carries d, the octaves of the scale over the unit, and inv is
-// 2^-d). d is at least -60, where nothing is left of a half and the weights of keys that count are still normal numbers.
-// A score above lim asks for a new m and mv: before the first addend every score. A row that has seen no key has m =
-// -inf, and every s is -inf too.
+__device__ __forceinline__ float unit_of(float e) { return fmaxf(e, kNoUnit); }
+// How the weights of keys under a value scale of 2^lv are formed: 2^((s - m) + lift) goes into the value sums and, times
+// inv, into the sum of weights (one exponential for both: lift carries d, the octaves of the scale over the unit, and inv
+// is 2^-d). d is at least -60, where nothing is left of a half and the weights of keys that count are still normal
+// numbers. A score above lim asks for a new m and e: before the first addend every score.
 struct Weigh {
-  float off, lim, inv;
+  float lift, lim, inv;
 };
-__device__ __forceinline__ Weigh weigh(float m, float mv, float lv) {
-  const float d = fmaxf(lv - unit_of(m, mv), -60.f);
+__device__ __forceinline__ Weigh weigh(float m, float e, float lv) {
+  const float d = fmaxf(lv - unit_of(e), -60.f);
   Weigh w;
-  w.off = m == -INFINITY ? 0.f : (d + kLift) - m;
-  w.lim = mv == -INFINITY ? -INFINITY : m + (kSlack - fmaxf(d, 0.f));
+  w.lift = d + kLift;
+  w.lim = e == -INFINITY ? -INFINITY : __fadd_rd(m, kSlack - fmaxf(d, 0.f));   // where it is not exact, not too high
   w.inv = pow2_whole(-fminf(d, 126.f));
   return w;
 }
-// Factor of the value sums where (m, mv) become (mn, mvn).
-__device__ __forceinline__ float unit_step(float m, float mv, float mn, float mvn) {
-  if (mv == -INFINITY) return 1.f;                   // no addend so far
-  return fast_exp2((m == mn ? 0.f : m - mn) + (unit_of(m, mv) - unit_of(mn, mvn)));
+// m as it is taken from scores: of a row that has seen no key all are -inf.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+// a - b of two maxima, the first at most the second (which may be -inf too).
+__device__ __forceinline__ float below(float a, float b) { return a == b ? 0.f : a - b; }
+// Factor of the value sums where (m, e) become (mn, en).
+__device__ __forceinline__ float unit_step(float m, float e, float mn, float en) {
+  if (e == -INFINITY) return 1.f;                    // no addend so far
+  return fast_exp2(below(m, mn) + (e - en));
 }
 
 // The low / high two codes of a word as two halves.
@@ -320,7 +324,7 @@ constexpr int kCbThreads = 256;
 template <int D, bool OF>
 __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, int grid) {
   constexpr int kParts = kCbThreads / (D / 4);       // records in flight side by side
-  __shared__ float wt[kMaxRecs];
+  __shared__ float wt[kMaxRecs];                     // octaves of the records' weights
   __shared__ float red[3][kCbThreads / 32];
   __shared__ float4 sums[kParts][D / 4];
   const int x0 = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
@@ -342,37 +346,38 @@ __global__ void __launch_bounds__(kCbThreads) cache8_combine_kernel(AttnArgs a, 
       e[y] = h.z;
     }
   static_assert(kMaxRecs <= 2 * kCbThreads, "two records per thread");
-  const float mw = dev::warp_max(fmaxf(m[0], m[1])), ew = dev::warp_max(fmaxf(m[0] + e[0], m[1] + e[1]));
+  const float mw = dev::warp_max(fmaxf(m[0], m[1]));
+  if ((tid & 31) == 0) red[0][tid >> 5] = mw;
+  __syncthreads();
+  float M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kCbThreads / 32; ++k) M = fmaxf(M, red[0][k]);
+  float lw = 0.f, ew = -INFINITY;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const float by = m[y] == -INFINITY ? -INFINITY : below(m[y], M);
+    lw += l[y] * fast_exp2(by);                      // a NaN of a row, whose maximum is -inf, stays
+    ew = fmaxf(ew, by + e[y]);
+    if (tid + y * kCbThreads < n) wt[tid + y * kCbThreads] = by + e[y];
+  }
+  lw = dev::warp_sum(lw);
+  ew = dev::warp_max(ew);
   if ((tid & 31) == 0) {
-    red[0][tid >> 5] = mw;
+    red[1][tid >> 5] = lw;
     red[2][tid >> 5] = ew;
   }
   __syncthreads();
-  float M = -INFINITY, MV = -INFINITY;
+  float L = 0.f, unit = kNoUnit;                     // of the merged sums
 #pragma unroll
   for (int k = 0; k < kCbThreads / 32; ++k) {
-    M = fmaxf(M, red[0][k]);
-    MV = fmaxf(MV, red[2][k]);
+    L += red[1][k];
+    unit = fmaxf(unit, rintf(red[2][k]));
   }
-  const float unit = unit_of(M, MV);                 // of the merged sums
-  float lt = 0.f;
-#pragma unroll
-  for (int y = 0; y < 2; ++y) {
-    const float by = m[y] == -INFINITY ? 0.f : m[y] - M;
-    lt += l[y] * (m[y] == -INFINITY ? 0.f : fast_exp2(by));      // a NaN of a row, whose maximum is -inf, stays
-    if (tid + y * kCbThreads < n) wt[tid + y * kCbThreads] = m[y] == -INFINITY ? 0.f : fast_exp2(by + (e[y] - unit));
-  }
-  const float lw = dev::warp_sum(lt);
-  if ((tid & 31) == 0) red[1][tid >> 5] = lw;
-  __syncthreads();
-  float L = 0.f;
-#pragma unroll
-  for (int k = 0; k < kCbThreads / 32; ++k) L += red[1][k];
   const int x = tid % (D / 4), part = tid / (D / 4);
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int k = part; k < n; k += kParts) {
-    const float w = wt[k];
+    const float w = fast_exp2(wt[k] - unit);
     const float4 y = reinterpret_cast<const float4*>(record(k) + kRecHead)[x];
     sum.x = fmaf(y.x, w, sum.x);
     sum.y = fmaf(y.y, w, sum.y);
@@ -451,22 +456,26 @@ __global__ void __launch_bounds__(kMergeThreads, D == 256 ? 3 : 4) cache8_merge_
     };
     float M[kMergeRows], unit[kMergeRows];
     {
-      float top = -INFINITY, topv = -INFINITY;
+      float top = -INFINITY, e = -INFINITY;
+      const auto join = [&](float m, float y) {
+        const float mn = fmaxf(top, m);
+        e = fmaxf(e + below(top, mn), y + below(m, mn));
+        top = mn;
+      };
       for (int k = lane & 7; k < n; k += 8) {
         const float4 h = *reinterpret_cast<const float4*>(record(k, lane >> 3));
-        top = fmaxf(top, h.x);
-        topv = fmaxf(topv, h.x + h.z);
+        join(h.x, h.x == -INFINITY ? -INFINITY : h.z);
       }
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
+        const float m = __shfl_xor_sync(0xffffffffu, top, o), y = __shfl_xor_sync(0xffffffffu, e, o);
+        join(m, y);
       }
-      topv = unit_of(top, topv);
+      e = fmaxf(rintf(e), kNoUnit);
 #pragma unroll
       for (int x = 0; x < kMergeRows; ++x) {
         M[x] = __shfl_sync(0xffffffffu, top, 8 * x);
-        unit[x] = __shfl_sync(0xffffffffu, topv, 8 * x);
+        unit[x] = __shfl_sync(0xffffffffu, e, 8 * x);
       }
     }
     float y[kMergeRows][E], l[kMergeRows];
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(kMergeThreads, D == 256 ? 3 : 4) cache8_merge_
       for (int x = 0; x < kMergeRows; ++x) {
         const float* p = record(k, x);
         const float4 h = *reinterpret_cast<const float4*>(p);
-        const float by = h.x == -INFINITY ? -INFINITY : h.x - M[x], f = fast_exp2(by + (h.z - unit[x]));
+        const float by = h.x == -INFINITY ? -INFINITY : below(h.x, M[x]), f = fast_exp2(by + (h.z - unit[x]));
         l[x] = fmaf(h.y, fast_exp2(by), l[x]);       // a NaN of a row, whose maximum is -inf, stays
         float z[E];
         if constexpr (E == 2) {

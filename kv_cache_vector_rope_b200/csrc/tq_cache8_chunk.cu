@@ -12,13 +12,12 @@
 // turn codes into halves, warp 12 issues the products, warp 13 copies codes in
 // (a bulk copy per 16 keys, which lie in one page) and looks pages and scales up.
 //
-// Codes become halves once per CTA for all 256 rows. An 8-bit code is exactly a
-// half; a block's scale is a power of two, and so is its ratio to the largest
-// scale of the 128 keys (K) or so far (V), so the halves carry the ratio and the
-// reference scale goes into the softmax factor (K) or, where it grows, into a
-// rescaling of O (V). A ratio below 2^-15 loses bits that lie 2^-24 below the
-// largest code of the tile. Queries are scaled by a power of two into half's
-// range (exact), weights are rounded to halves (2^-12).
+// Codes become halves once per CTA for all 256 rows; an 8-bit code is exactly a
+// half. The scales stay out of the products: a group's key scale goes into the
+// factor of its scores, its value scale into the exponent of its weights, over a
+// unit of the row's own (Weigh), which rescales O where it moves. Queries are
+// scaled by a power of two into half's range (exact), weights are rounded to
+// halves (2^-11).
 //
 // Bound by the wait from a half's weights to its next scores (values, scores,
 // two looks at barriers: about 2100 cycles, of which the other half's weights
@@ -40,13 +39,11 @@ static_assert(kTile == 128 && kChunkRows == 256, "tiles of 128 x 128");
 constexpr int kRegsWeights = 152, kRegsCodes = 104, kRegsProducts = 104;
 static_assert((2 * kRegsWeights + kRegsCodes + kRegsProducts) * 128 <= 128 * kThreads, "within the launch's registers");
 
-// What the copying warp says of a tile: the reference scales, which groups of
-// 16 keys are in the tile (loaded), which of them lie outside the cache (bad),
-// and each group's scales over the references.
+// What the copying warp says of a tile: each group of 16 keys' key scale and octaves of the value scale, which groups are
+// in the tile (loaded) and which of them lie outside the cache (bad).
 struct TileInfo {
-  float kref, vref;
+  float ks[8], lv[8];
   uint32_t loaded, bad;
-  float rk[8], rv[8];
 };
 
 template <int D>
@@ -117,25 +114,17 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16 codes as halves times `ratio`, to two 16-byte chunks of a tile. Lanes of
-// odd 64-coordinate atoms store their second chunk first (the caller gives the
-// two addresses and words in that order), so that eight lanes meet eight
-// different bank groups.
+// 16 codes as halves, to two 16-byte chunks of a tile. Lanes of odd
+// 64-coordinate atoms store their second chunk first (the caller gives the two
+// addresses and words in that order), so that eight lanes meet eight different
+// bank groups.
 template <bool INT8>
-__device__ __forceinline__ void put_codes(uint32_t at0, uint32_t at1, const uint32_t (&w)[4], bool scaled, float ratio) {
+__device__ __forceinline__ void put_codes(uint32_t at0, uint32_t at1, const uint32_t (&w)[4]) {
   uint32_t h[8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     h[2 * k] = two_halves<INT8, false>(w[k]);
     h[2 * k + 1] = two_halves<INT8, true>(w[k]);
-  }
-  if (scaled) {
-    const __half2 r = __float2half2_rn(ratio);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), r);
-      h[k] = *reinterpret_cast<const uint32_t*>(&x);
-    }
   }
   sts128(at0, h[0], h[1], h[2], h[3]);
   sts128(at1, h[4], h[5], h[6], h[7]);
@@ -157,29 +146,136 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
-// Scores of keys that a row does not see become -inf: those outside [from, end)
-// of the 32, and those of bad groups of 16.
-__device__ __forceinline__ void hide(uint32_t (&x)[32], int from, int end, uint32_t bad) {
+// Which of 32 keys a row sees: those in [from, end), but of bad groups of 16.
+__device__ __forceinline__ uint32_t seen(int from, int end, uint32_t bad) {
   uint32_t see = end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u;
   see &= from >= 32 ? 0u : from <= 0 ? 0xffffffffu : ~((1u << from) - 1u);
-  see &= (bad & 1 ? 0u : 0xffffu) | (bad & 2 ? 0u : 0xffff0000u);
+  return see & ((bad & 1 ? 0u : 0xffffu) | (bad & 2 ? 0u : 0xffff0000u));
+}
+// The others' scores become -inf.
+__device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t see) {
 #pragma unroll
   for (int e = 0; e < 32; ++e)
     if (!(see & (1u << e))) x[e] = 0xff800000u;
 }
-// Weights 2^(x f + off) of 32 scores: their sum, and as halves to 16 columns.
-__device__ __forceinline__ void weights(const uint32_t (&x)[32], float f, float off, float2& sum, uint32_t at) {
+// Weights 2^(x f + off) of 32 scores, two groups of 16: as halves to 16 columns, and their sums times 2^-d to l.
+__device__ __forceinline__ void weights(const uint32_t (&x)[32], const float (&f)[4], const float (&d)[4], float off0, int first,
+                                        float& l, uint32_t at) {
   uint32_t pk[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
-                    make_float2(off, off));
-    y.x = fast_exp2(y.x);
-    y.y = fast_exp2(y.y);
-    sum = add2(sum, y);
-    pk[e] = pack_half(y.x, y.y);
+  for (int h = 0; h < 2; ++h) {
+    const float fk = f[first + h], off = d[first + h] + off0;
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 8 * h; e < 8 * h + 8; ++e) {
+      float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(fk, fk),
+                      make_float2(off, off));
+      y.x = fast_exp2(y.x);
+      y.y = fast_exp2(y.y);
+      sum = add2(sum, y);
+      pk[e] = pack_half(y.x, y.y);
+    }
+    l = fmaf(sum.x + sum.y, pow2_whole(-fminf(d[first + h], 126.f)), l);
   }
   tmem_st16(at, pk);
+}
+// Largest of 16 scores from x[at] on.
+__device__ __forceinline__ float top16(const uint32_t (&x)[32], int at) {
+  float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+  for (int e = at; e < at + 16; e += 4) {
+    t0 = fmaxf(t0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+    t1 = fmaxf(t1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+  }
+  return fmaxf(t0, t1);
+}
+
+constexpr float kSteep = 4194304.f;
+// Keys without a value take no part in a row's unit (Weigh). Which they are is known only with the tile's values, long
+// after its scores, so it is looked up only where a scale lies more than this many octaves above the unit (above another
+// of the half's, before the first addend): short of that they cost a row no more than as many of a half's 25 octaves.
+// (Looked for in every tile, by the converting warps or two idle ones, a prompt of 4 x 2048 tokens took 258 and 245 us
+// against 234.)
+constexpr float kJump = 5.f;
+// A query row's maximum of scores, unit of its value sums (Weigh) and sum of weights. Weights are 2^(s f + (lift - m)),
+// one rounding each, while scores are below 2^22 octaves. Beyond (steep, for the warp) the product, which is not rounded
+// before the sum, may differ from m by more than halves have room for: the scores are made to count from `from` first. by:
+// what the last move scaled O by.
+struct Row {
+  float m, unit, l, from, by;
+  bool steep;
+};
+// A half of a tile: its scores in tensor memory, the factors of their groups, and the keys that the row sees.
+struct Half {
+  uint32_t at;
+  float cq;
+  const float *ks, *lv;                              // of the four groups of 16 keys
+  uint32_t see0, see1;
+  uint32_t v;                                        // its values in shared memory: D / 64 times [64 keys][128 bytes], 16 KB apart
+  uint64_t* v_full;                                  // where they are waited for
+  uint32_t parity;
+  uint64_t wait_ns;
+};
+// The common move's counterpart for a half whose keys without a value count apart, or of steep scores: their weights go
+// into l here and their scores become -inf in tensor memory, where the others count from `from` then, as m does. top: the
+// half's largest score as it comes from the products. Returns whether the values came. A call, so that the hot path stays
+// short.
+template <int D>
+__device__ __noinline__ bool move_row(Row* row, const Half& h, float top) {
+  if (!__all_sync(0xffffffffu, mbar_wait(h.v_full, h.parity, h.wait_ns))) return false;
+  Row r = *row;
+  uint32_t has[2];                                   // the keys with a value code that is not zero
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    uint32_t any = 0u;
+#pragma unroll 1
+    for (int c = 0; c < D / 8; ++c) {
+      uint32_t y[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                   : "r"(h.v + (c >> 3) * (128 * 128) + (32 * x + (threadIdx.x & 31)) * 128 + (c & 7) * 16)
+                   : "memory");
+      any |= y[0] | y[1] | y[2] | y[3];
+    }
+    has[x] = __ballot_sync(0xffffffffu, (any & 0x7fff7fffu) != 0u);
+  }
+  const float mn = fmaxf(r.m, rintf(top - r.from)), by = below(r.m, mn);
+  const bool far = fabsf(mn) > kSteep && fabsf(mn) < INFINITY;
+  const bool steep = __any_sync(0xffffffffu, r.steep || far);
+  const float shift = steep && fabsf(mn) < INFINITY ? mn : 0.f;
+  float en = r.unit + by;
+  r.l *= fast_exp2(by);
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t see = (k < 2 ? h.see0 : h.see1) >> (16 * (k & 1)), some = (k < 2 ? has[0] : has[1]) >> (16 * (k & 1));
+    const float f = fmaxf(h.cq * h.ks[k], 1.17549435e-38f);
+    uint32_t y[16];
+    tmem_ld16(h.at + 16 * k, y);
+    tmem_ld_wait();
+    float top16 = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float z = __fsub_rn(__fmul_rn(__uint_as_float(y[e]), f), r.from);
+      const bool sees = (see >> e) & 1;
+      if ((some >> e) & 1) {
+        if (sees) top16 = fmaxf(top16, z);
+        if (steep) y[e] = __float_as_uint((z - shift) / f);
+      } else {
+        if (sees) r.l += fast_exp2((z - base_of(mn)) + kLift);
+        y[e] = 0xff800000u;
+      }
+    }
+    tmem_st16(h.at + 16 * k, y);
+    if (top16 > -INFINITY) en = fmaxf(en, rintf(below(top16, mn) + h.lv[k]));
+  }
+  tmem_st_wait();
+  r.by = r.unit == -INFINITY ? 1.f : fast_exp2(by + (r.unit - en));
+  r.from += shift;
+  r.m = mn - shift;
+  r.unit = en;
+  r.steep = steep;
+  *row = r;
+  return true;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -311,48 +407,89 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
       // Keys in [lo_max, hi_min) are seen by every row of the tile.
       const int hi_min = row_hi(a, sg.n, a.group_div.of(r0));
       const int lo_max = row_lo(a, row_hi(a, sg.n, a.group_div.of(min(r0 + 127, a.rows - 1))));
-      float m = -INFINITY, l = 0.f, vrun = 0.f;
+      float from = 0.f;                              // what m counts from (steep)
+      bool steep = false, again = false;             // again: a half whose m and unit have been moved
+      float m = -INFINITY, unit = kNoUnit, l = 0.f;
       for (int j = 0; j < 2 * tiles; ++j) {          // halves of 64 keys
         const int half = j & 1, k0 = key0 + j * 64;
         const uint32_t at = s_at + 64 * half;
         alive = __all_sync(0xffffffffu, wait(kSFull + 2 * q + half, tiles_seen + (j >> 1)));
         if (!alive) break;
         tc_fence_after();
-        uint32_t x0[32], x1[32];
-        tmem_ld32(at, x0);
-        tmem_ld32(at + 32, x1);
-        const TileInfo& inf = info[(walked + (j >> 1)) & 3];
-        const float f = fmaxf(cq * inf.kref, 1.17549435e-38f);   // not 0: masked scores stay -inf
-        const float vref = inf.vref;
+        const uint32_t now = walked + (j >> 1);
+        const TileInfo& inf = info[now & 3];
         const uint32_t bad = inf.bad >> (4 * half);
         const bool masked = k0 < lo_max || k0 + 64 > hi_min || (bad & 15);
+        uint32_t x0[32], x1[32];
+        float f[4], d[4];                            // of the half's four groups of 16 keys: factors, octaves over the unit
+        tmem_ld32(at, x0);
+        tmem_ld32(at + 32, x1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[k] = fmaxf(cq * inf.ks[4 * half + k], 1.17549435e-38f);
+          d[k] = fmaxf(inf.lv[4 * half + k] - unit, -60.f);
+        }
         tmem_ld_wait();
         if (masked) {
-          hide(x0, lo - k0, hi - k0, bad);
-          hide(x1, lo - k0 - 32, hi - k0 - 32, bad >> 2);
+          hide(x0, seen(lo - k0, hi - k0, bad));
+          hide(x1, seen(lo - k0 - 32, hi - k0 - 32, bad >> 2));
         }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float top[4];
+        bool rise = false;
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          top[0] = fmaxf(top[0], fmaxf(__uint_as_float(x0[e]), __uint_as_float(x0[e + 1])));
-          top[1] = fmaxf(top[1], fmaxf(__uint_as_float(x0[e + 2]), __uint_as_float(x0[e + 3])));
-          top[2] = fmaxf(top[2], fmaxf(__uint_as_float(x1[e]), __uint_as_float(x1[e + 1])));
-          top[3] = fmaxf(top[3], fmaxf(__uint_as_float(x1[e + 2]), __uint_as_float(x1[e + 3])));
+        for (int k = 0; k < 4; ++k) {
+          top[k] = top16(k < 2 ? x0 : x1, 16 * (k & 1)) * f[k];
+          rise |= top[k] > __fadd_rd(unit == kNoUnit ? -INFINITY : m + kSlack, fminf(-d[k], 0.f));
         }
-        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
-        if (__any_sync(0xffffffffu, mt > m + kSlack || vref != vrun)) {
-          // The maximum is too low by more than kSlack octaves, or the values' reference has grown: what has been
-          // summed up, in l and in O, is scaled to the new ones.
-          const float mn = fmaxf(m, mt);
-          const float fm = mn == m ? 1.f : fast_exp2(m - mn);
-          m = mn;
-          l *= fm;
+        if (__any_sync(0xffffffffu, (rise || steep) && !again)) {
+          // A score is too high for m, or an addend for the unit: both are moved, and what has been summed up, in l and
+          // in O, with them.
+          const float all = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), mn = fmaxf(m, rintf(all));
+          float low = unit == kNoUnit ? INFINITY : unit, high = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (top[k] > -INFINITY) {
+              const float lv = inf.lv[4 * half + k];
+              high = fmaxf(high, lv);
+              if (unit == kNoUnit) low = fminf(low, lv);
+            }
+          const bool odd = __any_sync(0xffffffffu, steep || high > low + kJump || (fabsf(mn) > kSteep && fabsf(mn) < INFINITY));
+          float fo;
+          if (odd) {
+            Row row{m, unit == kNoUnit ? -INFINITY : unit, l, from, 1.f, steep};
+            Half h{at, cq, inf.ks + 4 * half, inf.lv + 4 * half, 0xffffffffu, 0xffffffffu,
+                   base + L::kOffV + (now & 1) * L::kTileBytes + half * 64 * 128, bar + kVFull + (now & 1), (now >> 1) & 1, a.wait_ns};
+            if (masked) {
+              h.see0 = seen(lo - k0, hi - k0, bad);
+              h.see1 = seen(lo - k0 - 32, hi - k0 - 32, bad >> 2);
+            }
+            alive = move_row<D>(&row, h, all);
+            if (!alive) {
+              if (a.d_status) atomicOr(a.d_status, TQ_DEV_TIMEOUT);
+              break;
+            }
+            steep = row.steep;
+            from = row.from;
+            l = row.l;
+            m = row.m;
+            unit = unit_of(row.unit);
+            fo = row.by;
+          } else {
+            const float by = below(m, mn);
+            float en = unit == kNoUnit ? -INFINITY : unit + by;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (top[k] > -INFINITY) en = fmaxf(en, rintf(below(top[k], mn) + inf.lv[4 * half + k]));
+            fo = unit == kNoUnit ? 1.f : fast_exp2(by + (unit - en));
+            l *= fast_exp2(by);
+            m = mn;
+            unit = unit_of(en);
+          }
           if (j > 0) {
             // O holds the half before, and with it all others: the products end in order.
             alive = __all_sync(0xffffffffu, wait(kPvDone + 2 * q + (half ^ 1), tiles_seen + ((j - 1) >> 1)));
             if (!alive) break;
             tc_fence_after();
-            const float fo = fm * (vrun / vref);
 #pragma unroll 1
             for (int k = 0; k < D / 16; ++k) {
               uint32_t o[16];
@@ -363,15 +500,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
               tmem_st16(o_at + 16 * k, o);
             }
           }
-          vrun = vref;
+          if (odd) {                                 // read the scores again
+            again = true;
+            --j;
+            continue;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) d[k] = fmaxf(inf.lv[4 * half + k] - unit, -60.f);
         }
-        // p = 2^(s f - m + kLift); a row that has seen no key yet has m = -inf, and every s is -inf too.
-        const float off = m == -INFINITY ? 0.f : kLift - m;
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-        weights(x0, f, off, sum0, at);
-        weights(x1, f, off, sum1, at + 16);
-        sum0 = add2(sum0, sum1);
-        l += sum0.x + sum0.y;
+        again = false;
+        const float off0 = kLift - base_of(m);
+        weights(x0, f, d, off0, 0, l, at);
+        weights(x1, f, d, off0, 2, l, at + 16);
         tmem_st_wait();
         tc_fence_before();
         arrive(kPFull + 2 * q + half);
@@ -383,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
       tc_fence_after();
       float* rec = a.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.head && u != u0 ? 1 : 0)) * kChunkRows * (kRecHead + D) +
                    static_cast<int64_t>(128 * q + wr) * (kRecHead + D);
-      const float by = sg.whole ? (l == 0.f ? 0.f : vrun / l) : vrun;
+      m += from;
+      const float by = sg.whole ? (l == 0.f ? 0.f : 1.f / l * pow2_whole(unit)) : 1.f;
       const int64_t at = (a.first_seq + sg.b) * a.o_bs + hq * a.o_hs + i * a.o_rs;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -417,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         if (!sg.whole) {
           rec[0] = m;
           rec[1] = l;
-          rec[2] = 0.f;
+          rec[2] = unit;
         } else if (a.lse) {
           a.lse[((a.first_seq + sg.b) * a.heads * a.group + hq) * a.nq + i] =
               l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2;
@@ -452,12 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         for (int kv = 0; kv < 2; ++kv) {
           alive = __all_sync(0xffffffffu, wait(kRawFull + kv, it) && wait((kv ? kVEmpty : kKEmpty) + st, parity ^ 1));
           if (!alive) break;
-          const TileInfo& inf = info[it & 3];
-          const float* ratios = kv ? inf.rv : inf.rk;
-          const uint32_t loaded = inf.loaded;
-          bool scaled = false;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) scaled |= ((loaded >> x) & 1) && ratios[x] != 1.f;
+          const uint32_t loaded = info[it & 3].loaded;
           const uint4* raw = reinterpret_cast<const uint4*>(smem + (kv ? L::kOffRawV : L::kOffRawK)) + ct;
           const uint32_t tile = base + (kv ? L::kOffV : L::kOffK) + st * L::kTileBytes;
           const bool clean = left >= kTile && loaded == 0xffu;
@@ -470,8 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
             uint4 y = codes[x];
             if (!clean && (!((loaded >> group) & 1) || x * kStepRows + row >= left)) y = make_uint4(0u, 0u, 0u, 0u);
             const uint32_t words[4] = {odd ? y.z : y.x, odd ? y.w : y.y, odd ? y.x : y.z, odd ? y.y : y.w};
-            put_codes<INT8>(tile + at0 + x * kStepRows * 128, tile + at1 + x * kStepRows * 128, words, scaled,
-                            scaled ? ratios[group] : 1.f);
+            put_codes<INT8>(tile + at0 + x * kStepRows * 128, tile + at1 + x * kStepRows * 128, words);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -581,7 +716,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
         }
         if (lane == 0 && sg.head && !sg.whole) a.cuts[blockIdx.x] = cut_of(a, sg, u != u0, per);
         const int key0 = sg.t0 / kTile * kTile, tiles = (sg.t1 - key0 + kTile - 1) / kTile;
-        float vref = 0.f;
         // -1: keys the segment does not reach, -2: a page outside the cache.
         const auto load_page = [&](int j) {
           const int key = key0 + j * kTile + 16 * lane;
@@ -599,10 +733,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           const float ks1 = load_scale(a.ks, page1), vs1 = load_scale(a.vs, page1);
           const uint32_t loaded = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -2);
           if (bad && lane == 0 && a.d_status) atomicOr(a.d_status, TQ_DEV_BAD_BLOCK);
-          float kref = dev::warp_max(ks);
-          if (!(kref > 0.f)) kref = 1.f;             // no page at all
-          vref = fmaxf(vref, dev::warp_max(vs));
-          const float vr = vref > 0.f ? vref : 1.17549435e-38f;
           const int64_t at = ((static_cast<int64_t>(page) * a.heads + sg.kv) * a.block + ((key0 + j * kTile + 16 * lane) & (a.block - 1))) * D;
           const uint32_t sum = __popc(loaded) * bytes;
 #pragma unroll 1
@@ -612,14 +742,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
             if (kv == 0) {
               TileInfo& inf = info[it & 3];
               if (lane == 0) {
-                inf.kref = kref;
-                inf.vref = vr;
                 inf.loaded = loaded;
                 inf.bad = bad;
               }
               if (lane < 8) {
-                inf.rk[lane] = ks / kref;
-                inf.rv[lane] = vs / vr;
+                inf.ks[lane] = ks;
+                inf.lv[lane] = octaves(vs);
               }
             }
             __syncwarp();

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
     const int hi_min = any_row ? row_hi(a, sg.n, a.group_div.of(r0)) : 0, hi_max = any_row ? row_hi(a, sg.n, last) : 0;
     const int lo_min = row_lo(a, hi_min), lo_max = row_lo(a, hi_max);
     float acc[D / 8][4];
-    float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[2] = {-INFINITY, -INFINITY}, unit[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < D / 8; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
     float cq[2] = {0.f, 0.f};
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          rise |= fmaxf(s[nt][2 * x], s[nt][2 * x + 1]) > weigh(m[x], mv[x], octaves(scale[4 + (nt >> 1)])).lim;
+          rise |= fmaxf(s[nt][2 * x], s[nt][2 * x + 1]) > weigh(m[x], unit[x], octaves(scale[4 + (nt >> 1)])).lim;
       }
       if (__any_sync(0xffffffffu, rise)) {
         float f[2];
@@ -313,22 +313,23 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
         for (int x = 0; x < 2; ++x) {
           float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
+          for (int nt = 0; nt < 8; ++nt) top = fmaxf(top, fmaxf(s[nt][2 * x], s[nt][2 * x + 1]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float mn = fmaxf(m[x], rintf(top)), by = below(m[x], mn);
+#pragma unroll
           for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              top = fmaxf(top, s[nt][2 * x + e]);
-              if (sm_some[8 * nt + 2 * t + e]) topv = fmaxf(topv, s[nt][2 * x + e] + octaves(scale[4 + (nt >> 1)]));
-            }
-#pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
-          }
-          const float mn = fmaxf(m[x], rintf(top)), mvn = fmaxf(mv[x], rintf(topv));
-          f[x] = unit_step(m[x], mv[x], mn, mvn);
-          if (mn != m[x]) l[x] *= fast_exp2(m[x] - mn);
+            for (int e = 0; e < 2; ++e)
+              if (sm_some[8 * nt + 2 * t + e] && s[nt][2 * x + e] > -INFINITY)
+                topv = fmaxf(topv, below(s[nt][2 * x + e], mn) + octaves(scale[4 + (nt >> 1)]));
+          topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 1));
+          topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 2));
+          const float en = fmaxf(unit[x] + by, rintf(topv));
+          f[x] = unit_step(m[x], unit[x], mn, en);
+          l[x] *= fast_exp2(by);
           m[x] = mn;
-          mv[x] = mvn;
+          unit[x] = en;
           // Keys without a value: counted here, then left out.
 #pragma unroll
           for (int nt = 0; nt < 8; ++nt)
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
             for (int e = 0; e < 2; ++e) {
               float& y = s[nt][2 * x + e];
               if (sm_some[8 * nt + 2 * t + e] || y == -INFINITY) continue;
-              l[x] += fast_exp2((y - mn) + kLift);
+              l[x] += fast_exp2((y - base_of(mn)) + kLift);
               y = -INFINITY;
             }
         }
@@ -353,10 +354,11 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
         float p[4];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const Weigh y = weigh(m[x], mv[x], lv);
+          const Weigh y = weigh(m[x], unit[x], lv);
+          const float base = base_of(m[x]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            p[2 * x + e] = fast_exp2(s[nt][2 * x + e] + y.off);
+            p[2 * x + e] = fast_exp2((s[nt][2 * x + e] - base) + y.lift);
             l[x] = fmaf(p[2 * x + e], y.inv, l[x]);
           }
         }
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
       if (r >= a.rows) continue;
       const int i = a.group_div.of(r), hq = sg.kv * a.group + r - i * a.group;
       const int64_t at = (a.first_seq + sg.b) * a.o_bs + hq * a.o_hs + i * a.o_rs + 2 * t;
-      const float unit = unit_of(m[x], mv[x]), by = sg.whole ? (l[x] == 0.f ? 0.f : 1.f / l[x] * pow2_whole(unit)) : 1.f;
+      const float e = unit_of(unit[x]), by = sg.whole ? (l[x] == 0.f ? 0.f : 1.f / l[x] * pow2_whole(e)) : 1.f;
       float* to = rec + row * (kRecHead + D);
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
         if (!sg.whole) {
           to[0] = m[x];
           to[1] = l[x];
-          to[2] = unit;
+          to[2] = e;
         } else if (a.lse) {
           a.lse[((a.first_seq + sg.b) * a.heads * a.group + hq) * a.nq + i] =
               l[x] == 0.f ? -INFINITY : (m[x] - kLift + log2f(l[x])) * kLn2;

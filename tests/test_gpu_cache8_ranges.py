@@ -4,8 +4,8 @@ by their weights, whatever the scales of others.
 Tolerances, per element, from the arithmetic of tests/test_gpu_cache8.py taken key by key, so that a key of small weight
 or one that the row does not see grants nothing. With p the softmax weights, B_k = scale * sum |q_i k_i| of key k and u =
 2^-24: a weight errs by ew_k = (2 d/16 + 8) 2^-23 B_k + 2^-22 B_k (score) + 2^-22 (ex2) + 2 u (2 B_k + 20 + D) (roundings
-of the exponent, |s - m| plus D octaves between the smallest and the largest value scale, 60 at most) + 2^-12 (one half;
-2^-21 for the two of an fp32 output) + (n/16 + 40) 2^-23 (sums, of a matrix unit that cuts). The output errs by the sum of
+of the exponent, |s - m| plus D octaves between the smallest and the largest value scale, 60 at most) + 2^-11 (one half:
+10 fraction bits, so steps of 2^-10 and roundings of 2^-11 of a value; 2^-21 for the two of an fp32 output) + (n/16 + 40) 2^-23 (sums, of a matrix unit that cuts). The output errs by the sum of
 p_k ew_k (|v_k| + |out|), plus half a step of its type, plus what lies below a half: 2^-25 (2^-36 with a second half kept
 times 2^11) of a weight in units where the largest addend of a code that is not zero, T = max p_k scale_k, is at least
 2^5.5, for each key, with codes of at most M: n M T 2^-30 (n M T 2^-41).
@@ -22,9 +22,9 @@ tq = pytest.importorskip("kv_cache_vector_rope_b200")
 HEADS, BLOCK = 2, 16
 
 
-def _make(rg, lens, d, code, shape):
+def _make(rg, lens, d, code, shape, key=None):
     """A cache whose value scales are set by `shape(position, length)` (octaves), suppressed keys (negative score) by the
-    first coordinate, which every query holds as 8. Returns the setup."""
+    first coordinate, which every query holds as 8; `key(position, length)` sets the keys' octaves. Returns the setup."""
     s = Setup(int(rg.integers(1 << 30)), lens, HEADS, d, BLOCK, code)
     for b, n in enumerate(lens):
         if n == 0:
@@ -33,6 +33,8 @@ def _make(rg, lens, d, code, shape):
         k, v = rg.standard_normal((n, HEADS, d)), rg.standard_normal((n, HEADS, d))
         k[..., 0] = (score * np.sqrt(d) / 8)[:, None]
         v *= 2.0 ** octaves[:, None, None]
+        if key is not None:
+            k *= 2.0 ** key(np.arange(n), n)[:, None, None]
         row = s.dtable[b:b + 1].contiguous()
         tq.tq_cache8_write(s.cache, torch.from_numpy(k).float().cuda(), torch.from_numpy(v).float().cuda(), _i32([0, n]),
                            _i32([0]), block_table=row, d_status=s.status)
@@ -80,7 +82,7 @@ def _check(s, q, lens, out, lse, od, causal=True, window=0):
             ref = p @ v
             B = x.abs() @ k.abs().T / d ** 0.5
             ew = ((2 * d / 16 + 8) * 2.0 ** -23 + 2.0 ** -22) * B + 2.0 ** -22 + 2 * 2.0 ** -24 * (2 * B + 20 + D)
-            ew = ew + (2.0 ** -21 if od == "f32" else 2.0 ** -12) + (n / 16 + 40) * 2.0 ** -23
+            ew = ew + (2.0 ** -21 if od == "f32" else 2.0 ** -11) + (n / 16 + 40) * 2.0 ** -23
             pe = p * ew
             T = (p * sv * some).amax(-1, keepdim=True)
             tol = HALF[od] * ref.abs() + pe @ v.abs() + ref.abs() * pe.sum(-1, keepdim=True)
@@ -111,7 +113,9 @@ FEW = [("int8", 64, 4, 1, "bf16", "bf16"), ("int8", 64, 1, 4, "f32", "f32"), ("i
        ("int8", 256, 1, 3, "bf16", "bf16"), ("e4m3", 64, 2, 4, "bf16", "bf16"), ("e4m3", 64, 1, 4, "f32", "f32"),
        ("e4m3", 128, 4, 1, "bf16", "bf16"), ("e4m3", 128, 1, 7, "f32", "f32"), ("e4m3", 128, 3, 4, "bf16", "bf16"),
        ("int8", 64, 4, 4, "bf16", "bf16"), ("e4m3", 256, 2, 3, "f32", "f32"), ("e4m3", 128, 2, 4, "bf16", "f32")]
-MANY = [("int8", 64, 2, 40, "f32", "f32"), ("e4m3", 64, 1, 70, "f32", "f32"), ("e4m3", 128, 2, 35, "f32", "f32"),
+CHUNK = [("int8", 64, 2, 40, "bf16", "bf16"), ("e4m3", 64, 1, 140, "bf16", "bf16"), ("e4m3", 128, 2, 35, "bf16", "bf16"),
+         ("int8", 128, 4, 70, "bf16", "bf16")]
+MANY = CHUNK + [("int8", 64, 2, 40, "f32", "f32"), ("e4m3", 64, 1, 70, "f32", "f32"), ("e4m3", 128, 2, 35, "f32", "f32"),
         ("int8", 128, 1, 70, "f32", "bf16"), ("e4m3", 256, 2, 40, "bf16", "bf16"), ("int8", 256, 1, 66, "f32", "f32")]
 
 
@@ -141,6 +145,19 @@ def test_the_newest_token_is_large(case, octaves):
     for window in (0, 50):
         out, lse = _attend(s, q, lens, od, window=window)
         _check(s, q, lens, out, lse, od, window=window)
+
+
+@pytest.mark.parametrize("octaves", [12, 18, 30])
+@pytest.mark.parametrize("case", [c for c in FEW + MANY if c[3] > 1], ids=lambda c: "-".join(map(str, c)))
+def test_the_newest_key_is_large(case, octaves):
+    # Its own row goes by that key alone; the rows in front of it go by the others, which lie far below it.
+    code, d, group, nq, qd, od = case
+    rg = np.random.default_rng(octaves + d + nq)
+    lens = [700, 90, 1]
+    s = _make(rg, lens, d, code, lambda at, n: (np.zeros(n), np.zeros(n)), lambda at, n: np.where(at == n - 1, octaves, 0))
+    q = _queries(rg, len(lens), HEADS * group, nq, d, qd)
+    out, lse = _attend(s, q, lens, od)
+    _check(s, q, lens, out, lse, od)
 
 
 @pytest.mark.parametrize("case", FEW + MANY, ids=lambda c: "-".join(map(str, c)))
