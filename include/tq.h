@@ -405,7 +405,10 @@ size_t tq_search_workspace_bytes(const tq_layout* layout, int32_t n_queries, int
  *   y      = x * rsqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
  *   (y_i, y_{i+r/2}) turned by positions[t] * rope_base^(-2i/r), i < r/2,
  *            r = rot_dim; elements r..d-1 are not turned (positions NULL: none)
- * Arithmetic in fp32, the angle in fp64; one rounding to dtype.
+ * Arithmetic in fp32, the angle in fp64; one rounding to dtype. A value that is
+ * not finite reaches what the formula takes it into: its pair where both are
+ * turned, with a norm its row (the factor of a row whose squares leave fp32,
+ * values from 2^63 / sqrt(d) on, is 0).
  *
  *  d            multiple of 8 in [8, 256];  rot_dim multiple of 8 in [0, d]
  *  q, k         device, head h of token t at q + t*token_stride + h*head_stride

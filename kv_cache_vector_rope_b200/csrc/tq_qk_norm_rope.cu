@@ -96,10 +96,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // Rows [r0, r1) of one side (q or k) of a token. LPR: lanes per row, the power
 // of two >= d / 8; a lane's values start at e0 and e1. With w0, w1 the weights
 // and (c, s) the angle of a pair (u, v) and f the row's norm factor:
-//   f (u w0 c - v w1 s),  f (u w0 s + v w1 c).
+//   f (u w0 c - v w1 s),  f (u w0 s + v w1 c),
+// and f u w0, f v w1 where the pair is not turned: not by an angle of 0, whose sine would carry an infinity or NaN of one
+// into the other.
 template <typename T, int LPR>
 __device__ __forceinline__ void side_rows(const T* src, int hs, T* dst, int ohs, int r0, int r1, const float* w,
-                                          float eps, float inv_d, int e0, int e1, bool on, const float2 (&c)[2],
+                                          float eps, float inv_d, int e0, int e1, bool on, bool turned, const float2 (&c)[2],
                                           const float2 (&sn)[2]) {
   constexpr int kRows = 32 / LPR;                    // rows of a warp side by side
   // bf16: two sets of rows while the next two are on their way; fp32, with twice the registers a set: four at once.
@@ -171,8 +173,10 @@ __device__ __forceinline__ void side_rows(const T* src, int hs, T* dst, int ohs,
         float2 y0[2], y1[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          y0[k] = mul2(ff, fma2(u[k], uc[k], mul2(v[k], vs[k])));
-          y1[k] = mul2(ff, fma2(u[k], us[k], mul2(v[k], vc[k])));
+          y0[k] = turned ? fma2(u[k], uc[k], mul2(v[k], vs[k])) : mul2(u[k], uc[k]);
+          y1[k] = turned ? fma2(u[k], us[k], mul2(v[k], vc[k])) : mul2(v[k], vc[k]);
+          y0[k] = mul2(ff, y0[k]);
+          y1[k] = mul2(ff, y1[k]);
         }
         T* p = dst + row * ohs;
         Vec<T>::store(p, y0);
@@ -203,7 +207,6 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) qk_norm_rope_kernel(NormR
        u += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
     const int64_t tok = a.parts == 1 ? u : u / a.parts;
     const int r0 = static_cast<int>(u - tok * a.parts) * a.rows_per_part, r1 = min(a.hq + a.hkv, r0 + a.rows_per_part);
-    // Elements that are not turned go by the angle 0.
     float2 c[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     if (rope) {
       const int p = a.pos[tok];
@@ -228,10 +231,10 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) qk_norm_rope_kernel(NormR
     }
     if (r0 < a.hq)
       side_rows<T, LPR>(static_cast<const T*>(a.q) + tok * a.q_ts, a.q_hs, static_cast<T*>(a.qo) + tok * a.qo_ts,
-                           a.qo_hs, r0, min(r1, a.hq), a.qw, a.eps, inv_d, e0, e1, on, c, sn);
+                           a.qo_hs, r0, min(r1, a.hq), a.qw, a.eps, inv_d, e0, e1, on, turned, c, sn);
     if (r1 > a.hq)
       side_rows<T, LPR>(static_cast<const T*>(a.k) + tok * a.k_ts, a.k_hs, static_cast<T*>(a.ko) + tok * a.ko_ts,
-                           a.ko_hs, max(r0 - a.hq, 0), r1 - a.hq, a.kw, a.eps, inv_d, e0, e1, on, c, sn);
+                           a.ko_hs, max(r0 - a.hq, 0), r1 - a.hq, a.kw, a.eps, inv_d, e0, e1, on, turned, c, sn);
   }
 }
 
