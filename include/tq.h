@@ -407,8 +407,8 @@ size_t tq_search_workspace_bytes(const tq_layout* layout, int32_t n_queries, int
  *            r = rot_dim; elements r..d-1 are not turned (positions NULL: none)
  * Arithmetic in fp32, the angle in fp64; one rounding to dtype. A value that is
  * not finite reaches what the formula takes it into: its pair where both are
- * turned, with a norm its row (the factor of a row whose squares leave fp32,
- * values from 2^63 / sqrt(d) on, is 0).
+ * turned, with a norm its row (the factor of a row whose sum of squares
+ * leaves fp32 is 0).
  *
  *  d            multiple of 8 in [8, 256];  rot_dim multiple of 8 in [0, d]
  *  q, k         device, head h of token t at q + t*token_stride + h*head_stride
@@ -537,7 +537,8 @@ tq_status tq_cache8_read(const tq_cache8* cache, tq_dtype dtype,
  *  seq_lens      device int32 [batch], keys in the cache (0 is fine); one that
  *                is negative or beyond table_stride * block is cut and sets
  *                TQ_DEV_BAD_LENGTH
- *  out           device, as q, of out_dtype; rows must not overlap
+ *  out           device, as q, of out_dtype; rows must not overlap: from the
+ *                smallest stride up, each is at least what lies below it
  *  lse_out       device float [batch][hq][nq] or NULL
  *  workspace     device scratch of tq_cache8_attention_workspace_bytes()
  *                bytes, 256-byte aligned; needs no initialisation. Calls that

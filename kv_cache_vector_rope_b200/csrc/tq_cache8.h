@@ -24,15 +24,31 @@ tq_status check_table8(const tq_cache8* c, int32_t batch, int64_t table_stride, 
 // A stride's check passes where its dimension has one index: it is never used.
 inline bool stride_ok(int64_t n, int64_t stride, int64_t unit) { return n <= 1 || (stride >= 0 && stride % unit == 0); }
 
-// Whether rows of d elements at i * si + j * sj (i < ni, j < nj) can overlap: the
-// smaller stride's rows must fit within the larger stride.
-inline bool rows_overlap(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t d) {
-  if (ni > 1 && nj > 1) {
-    const bool i_in = si <= sj;
-    const int64_t n = i_in ? ni : nj, s = i_in ? si : sj, S = i_in ? sj : si;
-    return s < d || S - d < 0 || (n - 1) > (S - d) / s;
+// Whether rows of d elements at sum i_k * stride_k (i_k < n_k) can overlap: from the smallest stride up, what lies below a
+// stride must fit within it. (Strides that interleave without that, 2 d beside 3 d, count as overlapping.)
+struct RowDim {
+  int64_t n, stride;
+};
+template <int K>
+inline bool rows_overlap(RowDim (&dim)[K], int64_t d) {
+  for (int i = 1; i < K; ++i)                        // by stride; a dimension of one index has none that matters
+    for (int j = i; j > 0 && dim[j].stride < dim[j - 1].stride; --j) {
+      const RowDim x = dim[j];
+      dim[j] = dim[j - 1];
+      dim[j - 1] = x;
+    }
+  int64_t extent = d;
+  for (const RowDim& x : dim) {
+    if (x.n <= 1) continue;
+    if (x.stride < extent) return true;
+    if (x.n - 1 > (INT64_MAX - extent) / x.stride) return true;
+    extent += (x.n - 1) * x.stride;
   }
-  return (ni > 1 && si < d) || (nj > 1 && sj < d);
+  return false;
+}
+inline bool rows_overlap(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t d) {
+  RowDim dim[2] = {{ni, si}, {nj, sj}};
+  return rows_overlap(dim, d);
 }
 
 // The driver's tensor-map encoder, looked up once; NULL where the driver lacks it.

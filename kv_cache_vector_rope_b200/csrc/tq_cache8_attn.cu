@@ -990,7 +990,8 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
       !stride_ok(nq, out_row_stride, 8))
     return fail(TQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned, strides multiples of 8 elements, not negative",
                 what);
-  if ((batch > 1 && out_batch_stride < d) || rows_overlap(hq, out_head_stride, nq, out_row_stride, d))
+  RowDim out_dims[3] = {{batch, out_batch_stride}, {hq, out_head_stride}, {nq, out_row_stride}};
+  if (rows_overlap(out_dims, d))
     return fail(TQ_ERR_INVALID_ARG, "%s: the strides of out make rows overlap", what);
   if (d != 64 && d != 128 && d != 256)
     return fail(TQ_ERR_UNSUPPORTED, "%s: d=%d not built (64, 128, 256)", what, d);
