@@ -134,32 +134,32 @@ __device__ __forceinline__ int find_seq(const int* cum, int n, int u) {
   return lo;
 }
 
-// cum[0..n] = exclusive prefix sums of count(b), b < n <= kC8Slice, by a CTA of
-// T threads (T a multiple of 32, T <= 1024). `part` holds T / 32 ints. A count
-// is below 2^26, so that a warp's 32 stay below 2^31.
+// cum[0..n] = exclusive prefix sums of count(b) >= 0, b < n <= kC8Slice, by a CTA of T threads (T a multiple of 32, T <=
+// 1024). `part` holds T / 32 ints. Lengths that fall and overlap may add up to any number: sums stay at kMostUnits, so
+// that cum never falls and a walk over the units in steps below 2^20 stays within 32 bits.
+constexpr int kMostUnits = 0x7fffffff - (1 << 20);
 template <int T, typename F>
 __device__ __forceinline__ void scan_counts(int* cum, int* part, int n, F count) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   int base = 0;
   for (int at = 0; at < n; at += T) {
     const int b = at + tid;
-    int v = b < n ? count(b) : 0;
+    uint32_t v = b < n ? count(b) : 0;               // two sums below 2^31 are below 2^32
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += x;
+      const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = min(v + x, static_cast<uint32_t>(kMostUnits));
     }
-    if (lane == 31) part[w] = v;
+    if (lane == 31) part[w] = static_cast<int>(v);
     __syncthreads();
-    long long before = base, all = base;
+    int64_t before = base, all = base;
     for (int k = 0; k < T / 32; ++k) {
       const int x = part[k];
       if (k < w) before += x;
       all += x;
     }
-    // Sums beyond int32 (malformed lengths only) stay at its top, so that cum never falls.
-    if (b < n) cum[b + 1] = static_cast<int>(min(before + v, 0x7fffffffll));
-    base = static_cast<int>(min(all, 0x7fffffffll));
+    if (b < n) cum[b + 1] = static_cast<int>(min(before + v, static_cast<int64_t>(kMostUnits)));
+    base = static_cast<int>(min(all, static_cast<int64_t>(kMostUnits)));
     __syncthreads();
   }
   if (tid == 0) cum[0] = 0;
