@@ -454,7 +454,7 @@ typedef enum { TQ_E4M3 = 0, TQ_INT8 = 1 } tq_code8;
 
 typedef struct {
   int32_t d;          /* head dim, a multiple of 16 in [16, 256]              */
-  int32_t heads;      /* KV heads                                              */
+  int32_t heads;      /* KV heads, at most 65535                               */
   int32_t block;      /* tokens per block: 16, 32, 64 or 128                   */
   int32_t code;       /* tq_code8                                              */
   int64_t n_blocks;   /* pages, below 2^31                                     */
@@ -464,7 +464,8 @@ typedef struct {
   float* v_scale;
 } tq_cache8;
 
-/* Bytes of a cache of n_blocks pages (codes and scales); -1 on invalid sizes. */
+/* Bytes of a cache of n_blocks pages (codes and scales; 0 blocks are fine);
+ * -1 on sizes that a tq_cache8 cannot have, or 2^63 bytes and more. */
 int64_t tq_cache8_bytes(int32_t d, int32_t heads, int32_t block, int64_t n_blocks);
 
 /* ------------------------------------------------------------------------

@@ -499,17 +499,24 @@ EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
+// The sizes of a cache; a code array stays below 2^62 bytes.
+static tq_status check_sizes8(int32_t d, int32_t heads, int32_t block, int64_t n_blocks, int64_t least, const char* what) {
+  if (d < 16 || d > kMaxD || d % 16 != 0)
+    return fail(TQ_ERR_INVALID_ARG, "%s: d must be a multiple of 16 in [16, %d] (got %d)", what, kMaxD, d);
+  if (block != 16 && block != 32 && block != 64 && block != 128)
+    return fail(TQ_ERR_INVALID_ARG, "%s: block must be 16, 32, 64 or 128 tokens (got %d)", what, block);
+  if (heads < 1 || heads > 65535) return fail(TQ_ERR_INVALID_ARG, "%s: heads must be in [1, 65535]", what);
+  if (n_blocks < least || n_blocks > 0x7fffffff)
+    return fail(TQ_ERR_INVALID_ARG, "%s: n_blocks must be in [%d, 2^31)", what, static_cast<int>(least));
+  return TQ_OK;
+}
+
 tq_status check_cache8(const tq_cache8* c, const char* what) {
   if (!c) return fail(TQ_ERR_INVALID_ARG, "%s: cache is NULL", what);
-  if (c->d < 16 || c->d > kMaxD || c->d % 16 != 0)
-    return fail(TQ_ERR_INVALID_ARG, "%s: d must be a multiple of 16 in [16, %d] (got %d)", what, kMaxD, c->d);
-  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)
-    return fail(TQ_ERR_INVALID_ARG, "%s: block must be 16, 32, 64 or 128 tokens (got %d)", what, c->block);
+  const tq_status st = check_sizes8(c->d, c->heads, c->block, c->n_blocks, 1, what);
+  if (st != TQ_OK) return st;
   if (c->code != TQ_E4M3 && c->code != TQ_INT8)
     return fail(TQ_ERR_INVALID_ARG, "%s: code must be TQ_E4M3 or TQ_INT8", what);
-  if (c->heads < 1 || c->heads > 65535) return fail(TQ_ERR_INVALID_ARG, "%s: heads must be in [1, 65535]", what);
-  if (c->n_blocks < 1 || c->n_blocks > 0x7fffffff)
-    return fail(TQ_ERR_INVALID_ARG, "%s: n_blocks must be in [1, 2^31)", what);
   if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(TQ_ERR_INVALID_ARG, "%s: NULL cache pointer", what);
   if (!aligned(c->k, 128) || !aligned(c->v, 128) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
     return fail(TQ_ERR_INVALID_ARG, "%s: code arrays must be 128-byte aligned", what);
@@ -528,8 +535,14 @@ tq_status check_table8(const tq_cache8* c, int32_t batch, int64_t table_stride, 
 extern "C" {
 
 int64_t tq_cache8_bytes(int32_t d, int32_t heads, int32_t block, int64_t n_blocks) {
-  if (d < 16 || d > tq::kMaxD || d % 16 != 0 || heads < 1 || block < 1 || n_blocks < 0) return -1;
-  return 2 * n_blocks * heads * (static_cast<int64_t>(block) * d + static_cast<int64_t>(sizeof(float)));
+  tq::clear_error();
+  if (tq::check_sizes8(d, heads, block, n_blocks, 0, "tq_cache8_bytes") != TQ_OK) return -1;
+  const int64_t page = 2 * static_cast<int64_t>(heads) * (static_cast<int64_t>(block) * d + static_cast<int64_t>(sizeof(float)));
+  if (n_blocks > INT64_MAX / page) {
+    tq::fail(TQ_ERR_INVALID_ARG, "tq_cache8_bytes: 2^63 bytes or more");
+    return -1;
+  }
+  return n_blocks * page;
 }
 
 tq_status tq_cache8_write(const tq_cache8* cache, tq_dtype dtype, const void* k, int64_t k_token_stride,

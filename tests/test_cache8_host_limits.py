@@ -38,3 +38,16 @@ def test_rows_read_that_overlap(n, kts, khs, overlaps):
     # The launch itself is kept away by rows of v that are not aligned, which are looked at behind those of k.
     st = _rows(tq._lib.tq_cache8_read, _cache(), n=n, kts=kts, khs=khs, v=0x2008)
     assert st == INVALID and (b"overlap" in tq._lib.tq_last_error_string()) == overlaps
+
+
+def test_bytes_of_sizes_that_no_call_takes():
+    f = tq.tq_cache8_bytes
+    assert f(128, 8, 64, 10) == 2 * 10 * 8 * (64 * 128 + 4) and f(16, 1, 16, 0) == 0
+    most = 2 * 65000 * ((1 << 31) - 1) * (128 * 256 + 4)
+    assert most < 1 << 63 < 2 * 65535 * ((1 << 31) - 1) * (128 * 256 + 4)
+    assert f(256, 65000, 128, (1 << 31) - 1) == most and f(256, 65535, 128, (1 << 31) - 1) == -1
+    for bad in ((128, 8, 48, 10), (128, 8, 0, 10), (128, 8, -16, 10), (128, 8, 256, 10), (128, 70000, 64, 10), (128, 65536, 64, 1),
+                (128, 0, 64, 10), (128, -1, 64, 10), (128, 8, 64, 1 << 60), (128, 8, 64, 1 << 31), (128, 8, 64, -1),
+                (100, 8, 64, 10), (272, 8, 64, 10), (0, 8, 64, 10)):
+        assert f(*bad) == -1, bad
+        assert b"tq_cache8_bytes" in tq._lib.tq_last_error_string()
