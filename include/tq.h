@@ -555,9 +555,10 @@ tq_status tq_cache8_read(const tq_cache8* cache, tq_dtype dtype,
  * that the row sees and whose value codes are not all zero: scales of other
  * keys do not touch a row. (With more than 64 bf16 rows per KV head, keys with
  * codes that are all zero count too, unless their scale is 2^5 times the row's.)
- * Supported d: 64, 128, 256, table_stride * block up to 2^30 (others:
- * TQ_ERR_UNSUPPORTED). Errors:
- * TQ_ERR_INVALID_ARG, TQ_ERR_WORKSPACE, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA.
+ * Supported (else TQ_ERR_UNSUPPORTED): d 64, 128, 256; C = table_stride * block
+ * up to 2^30; and heads * T * (C / 64 + 18) up to 2^30, T being the query rows
+ * of a KV head (hq / heads * nq), up to 64 of them by fours, more by 128. Both go
+ * by the width of the table, not by the lengths in it. Errors: TQ_ERR_INVALID_ARG, TQ_ERR_WORKSPACE, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA.
  * ---------------------------------------------------------------------- */
 tq_status tq_cache8_attention(const tq_cache8* cache,
                               const void* q, tq_dtype q_dtype, int64_t q_batch_stride, int64_t q_head_stride,

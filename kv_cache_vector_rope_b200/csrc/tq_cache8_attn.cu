@@ -996,19 +996,19 @@ extern "C" tq_status tq_cache8_attention(const tq_cache8* cache, const void* q, 
   if (d != 64 && d != 128 && d != 256)
     return fail(TQ_ERR_UNSUPPORTED, "%s: d=%d not built (64, 128, 256)", what, d);
   const int group = hq / cache->heads, rows = group * nq;
-  if (!workspace || workspace_bytes < attn_workspace(d, rows))
-    return fail(TQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, workspace_bytes, attn_workspace(d, rows));
-  if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
   const bool qf = q_dtype == TQ_F32, of = out_dtype == TQ_F32;
   const bool chunk = chunk_supported(d, qf || of, rows), wide = rows_supported(d, qf || of, rows);
   const int tile = chunk ? kChunkRows : wide ? kRowsTile : rows_of(d, rows, qf, of, cache->code == TQ_INT8);
   const int row_tiles = (rows + tile - 1) / tile;
   const int unit = chunk ? kChunkUnit : wide ? kRowsUnit : kUnit, lead = chunk ? kChunkLead : wide ? kRowsLead : lead_of(d);
   const int most = chunk ? kChunkSlice : wide ? kRowsSlice : kSlice;
-  // Units of one launch stay below 2^30: batches are cut into slices.
-  const int64_t per_seq = ((table_stride * cache->block + unit - 1) / unit + 1 + lead) * cache->heads * row_tiles;
-  if (per_seq > (1 << 25))
-    return fail(TQ_ERR_UNSUPPORTED, "%s: heads x query rows x capacity of one sequence too large", what);
+  // Units of one launch stay within 2^30: batches are cut into slices.
+  const int64_t per_head = ((table_stride * cache->block + unit - 1) / unit + 1 + lead) * row_tiles, per_seq = per_head * cache->heads;
+  if (per_head > (1 << 30) || per_seq > (1 << 30))
+    return fail(TQ_ERR_UNSUPPORTED, "%s: KV heads x query rows x capacity of one sequence too large", what);
+  if (!workspace || workspace_bytes < attn_workspace(d, rows))
+    return fail(TQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, workspace_bytes, attn_workspace(d, rows));
+  if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
   int64_t slice = (1 << 30) / per_seq;
   if (slice > most) slice = most;
   const int64_t streams = static_cast<int64_t>(batch) * cache->heads * row_tiles;

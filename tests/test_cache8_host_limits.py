@@ -51,3 +51,35 @@ def test_bytes_of_sizes_that_no_call_takes():
                 (100, 8, 64, 10), (272, 8, 64, 10), (0, 8, 64, 10)):
         assert f(*bad) == -1, bad
         assert b"tq_cache8_bytes" in tq._lib.tq_last_error_string()
+
+
+def _size(heads, group, nq, tokens, d=128, dtype=1, code=0):
+    """The status of a call over a table of that many tokens that has no workspace: TQ_ERR_WORKSPACE where its sizes are fine."""
+    hq = heads * group
+    c = _cache(d=d, heads=heads, block=128, code=code, n=1 << 24)
+    return _attend(c, hq=hq, nq=nq, qd=dtype, od=dtype, qbs=hq * nq * d, qhs=d, qrs=hq * d, obs=hq * nq * d, ohs=d, ors=hq * d,
+                   stride=tokens // 128, ws=0)
+
+
+@pytest.mark.parametrize("heads,group,nq,tokens,kw,fine", [
+    (63, 1, 1, 1 << 30, {}, True), (64, 1, 1, 1 << 30, {}, False),
+    (8, 4, 1, 1 << 30, {}, True), (32, 8, 1, 1 << 20, {}, True),
+    (8, 4, 262144, 262144, {}, True),                             # a prompt of 262144 tokens in one call
+    (8, 4, 1 << 20, 1 << 20, {}, False), (8, 4, 1 << 20, 1 << 16, {}, True),
+    (1, 1, 1 << 29, 128, {}, True), (1, 1, 1 << 29, 1 << 20, {}, False),
+    (8, 4, 65536, 262144, dict(d=256), True), (8, 4, 1 << 20, 262144, dict(d=256, dtype=0), False),
+    (65535, 1, 1, 1 << 19, {}, True), (65535, 1, 1, 1 << 20, {}, False),
+    (1, 1, 1, (1 << 30) + 128, {}, False)])
+def test_sizes_on_each_side_of_the_limit(heads, group, nq, tokens, kw, fine):
+    assert _size(heads, group, nq, tokens, **kw) == (WORKSPACE if fine else UNSUPPORTED)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("code", [0, 1])
+def test_what_the_header_names_as_supported_is_taken(d, dtype, code):
+    for heads, group, nq in ((1, 1, 1), (8, 4, 1), (3, 5, 7), (2, 8, 8), (4, 13, 5), (8, 4, 2048), (16, 1, 9999)):
+        rows = group * nq
+        t = -(-rows // (4 if rows <= 64 else 128))
+        tokens = min(1 << 30, 64 * ((1 << 30) // (heads * t) - 18)) // 128 * 128
+        assert _size(heads, group, nq, tokens, d=d, dtype=dtype, code=code) == WORKSPACE
