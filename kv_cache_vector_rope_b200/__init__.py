@@ -115,10 +115,23 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+
+
+class _NoBinding:
+    """Stands where _tq_torch.so is missing or made for another torch: the calls that go through it say so, the others run."""
+
+    def __init__(self, cause: ImportError):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs _tq_torch.so, which is not built or does not load; run "
+                          "`python kv_cache_vector_rope_b200/build.py`") from self._cause
+
+
 try:
     from . import _tq_torch as _bind            # checks and marshalling of the short calls (binding/tq_torch.cpp)
 except ImportError as e:
-    raise ImportError("_tq_torch.so is not built or does not load; run `python kv_cache_vector_rope_b200/build.py`") from e
+    _bind = _NoBinding(e)
 
 
 def exported_symbols() -> list[str]:

@@ -23,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtq.so")
 BINDING_SRC = os.path.join(PKG, "binding", "tq_torch.cpp")
 BINDING = os.path.join(PKG, "_tq_torch.so")
+BINDING_FOR = os.path.join(PKG, "_tq_torch.for")      # the Python and torch that the binding was built for
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -54,6 +55,13 @@ def nvcc() -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    """Both libraries, where they are stale; returns the path of libtq.so."""
+    build_lib(force, verbose, extra)
+    build_binding(force, verbose)
+    return LIB
+
+
+def build_lib(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     if not force and not _stale():
         return LIB
     tmp = LIB + ".tmp"
@@ -65,15 +73,26 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return LIB
 
 
+def _binding_stale(made_for: str) -> bool:
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_FOR):
+        return True
+    with open(BINDING_FOR) as f:
+        if f.read() != made_for:
+            return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(p) > t for p in (BINDING_SRC, os.path.join(INCLUDE, "tq.h")))
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """The Python extension, by the host compiler against torch's headers; links libtq.so next to it."""
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "tq.h")]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
-        return BINDING
+    """The Python extension, by the host compiler against torch's headers; links libtq.so next to it. Its ABI is that of
+    one Python and one torch: it is stale for others too."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
+    made_for = f"python {sysconfig.get_config_var('SOABI')}, torch {torch.__version__}\n"
+    if not force and not _binding_stale(made_for):
+        return BINDING
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include") if os.path.isabs(nvcc()) else None
     includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], INCLUDE, *([cuda] if cuda else [])]
@@ -85,11 +104,13 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(made_for)
     return BINDING
 
 
 if __name__ == "__main__":
     force = "--force" in sys.argv
     extra = ["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else None
-    print(build(force=force or bool(extra), verbose=True, extra=extra))
+    print(build_lib(force=force or bool(extra), verbose=True, extra=extra))
     print(build_binding(force=force, verbose=True))
