@@ -553,8 +553,7 @@ tq_status tq_cache8_read(const tq_cache8* cache, tq_dtype dtype,
  * What a key adds is beside that off by 2^-30 (2^-41) of the row's largest
  * product of a weight and a value scale times the largest code, over the keys
  * that the row sees and whose value codes are not all zero: scales of other
- * keys do not touch a row. (With more than 64 bf16 rows per KV head, keys with
- * codes that are all zero count too, unless their scale is 2^5 times the row's.)
+ * keys do not touch a row.
  * Supported (else TQ_ERR_UNSUPPORTED): d 64, 128, 256; C = table_stride * block
  * up to 2^30; and heads * T * (C / 64 + 18) up to 2^30, T being the query rows
  * of a KV head (hq / heads * nq), up to 64 of them by fours, more by 128. Both go

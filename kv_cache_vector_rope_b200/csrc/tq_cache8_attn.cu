@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
             }
-            const float en = fmaxf(e + by, rintf(topv));
+            const float en = next_unit(e, by, topv);
             f[j] = unit_step(m, e, mn, en);
             l[nt][j] *= fast_exp2(by);
             if (!kHold) __syncwarp();

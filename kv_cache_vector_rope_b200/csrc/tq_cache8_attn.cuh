@@ -243,6 +243,11 @@ __device__ __forceinline__ Weigh weigh(float m, float e, float lv) {
 }
 // m as it is taken from scores: of a row that has seen no key all are -inf.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+// The unit of sums in units of 2^e whose m has moved by `by`, with further addends of up to 2^top: at least 2^-126, which
+// outputs cannot tell from less.
+__device__ __forceinline__ float next_unit(float e, float by, float top) {
+  return fmaxf(e, top) == -INFINITY ? -INFINITY : fmaxf(fmaxf(e + by, rintf(top)), -126.f);
+}
 // a - b of two maxima, the first at most the second (which may be -inf too).
 __device__ __forceinline__ float below(float a, float b) { return a == b ? 0.f : a - b; }
 // Factor of the value sums where (m, e) become (mn, en).

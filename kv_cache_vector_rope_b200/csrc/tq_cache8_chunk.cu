@@ -191,12 +191,6 @@ __device__ __forceinline__ float top16(const uint32_t (&x)[32], int at) {
 }
 
 constexpr float kSteep = 4194304.f;
-// Keys without a value take no part in a row's unit (Weigh). Which they are is known only with the tile's values, long
-// after its scores, so it is looked up only where a scale lies more than this many octaves above the unit (above another
-// of the half's, before the first addend): short of that they cost a row no more than as many of a half's 25 octaves.
-// (Looked for in every tile, by the converting warps or two idle ones, a prompt of 4 x 2048 tokens took 258 and 245 us
-// against 234.)
-constexpr float kJump = 5.f;
 // A query row's maximum of scores, unit of its value sums (Weigh) and sum of weights. Weights are 2^(s f + (lift - m)),
 // one rounding each, while scores are below 2^22 octaves. Beyond (steep, for the warp) the product, which is not rounded
 // before the sum, may differ from m by more than halves have room for: the scores are made to count from `from` first. by:
@@ -211,43 +205,41 @@ struct Half {
   float cq;
   const float *ks, *lv;                              // of the four groups of 16 keys
   uint32_t see0, see1;
-  uint32_t v;                                        // its values in shared memory: D / 64 times [64 keys][128 bytes], 16 KB apart
-  uint64_t* v_full;                                  // where they are waited for
-  uint32_t parity;
-  uint64_t wait_ns;
+  uint2 some;                                        // the keys with a value code that is not zero
 };
-// The common move's counterpart for a half whose keys without a value count apart, or of steep scores: their weights go
-// into l here and their scores become -inf in tensor memory, where the others count from `from` then, as m does. top: the
-// half's largest score as it comes from the products. Returns whether the values came. A call, so that the hot path stays
-// short.
+// Which of 64 keys have a value code that is not zero: their halves lie at `at` in shared memory, D / 64 times [64 keys]
+// [128 bytes], 16 KB apart. A lane takes two keys, 16 bytes at a time, lanes side by side in different banks.
 template <int D>
-__device__ __noinline__ bool move_row(Row* row, const Half& h, float top) {
-  if (!__all_sync(0xffffffffu, mbar_wait(h.v_full, h.parity, h.wait_ns))) return false;
-  Row r = *row;
-  uint32_t has[2];                                   // the keys with a value code that is not zero
+__device__ __noinline__ uint2 keys_with_values(uint32_t at) {
+  const int lane = threadIdx.x & 31;
+  uint32_t any[2] = {0u, 0u};
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    uint32_t any = 0u;
-#pragma unroll 1
-    for (int c = 0; c < D / 8; ++c) {
+  for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
       uint32_t y[4];
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                   : "r"(h.v + (c >> 3) * (128 * 128) + (32 * x + (threadIdx.x & 31)) * 128 + (c & 7) * 16)
+                   : "r"(at + (c >> 3) * (128 * 128) + (32 * x + lane) * 128 + ((c ^ lane) & 7) * 16)
                    : "memory");
-      any |= y[0] | y[1] | y[2] | y[3];
+      any[x] |= (y[0] | y[1]) | (y[2] | y[3]);
     }
-    has[x] = __ballot_sync(0xffffffffu, (any & 0x7fff7fffu) != 0u);
-  }
+  return make_uint2(__ballot_sync(0xffffffffu, (any[0] & 0x7fff7fffu) != 0u), __ballot_sync(0xffffffffu, (any[1] & 0x7fff7fffu) != 0u));
+}
+// The common move's counterpart for a half in which rows see keys without a value, or for steep scores: the weights of such
+// keys go into l here and their scores become -inf in tensor memory, where the others count from `from` then, as m does.
+// top: the half's largest score as it comes from the products. A call, so that the hot path stays short.
+__device__ __noinline__ void move_row(Row* row, const Half& h, float top) {
+  Row r = *row;
   const float mn = fmaxf(r.m, rintf(top - r.from)), by = below(r.m, mn);
   const bool far = fabsf(mn) > kSteep && fabsf(mn) < INFINITY;
   const bool steep = __any_sync(0xffffffffu, r.steep || far);
   const float shift = steep && fabsf(mn) < INFINITY ? mn : 0.f;
-  float en = r.unit + by;
+  float topv = -INFINITY;
   r.l *= fast_exp2(by);
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
-    const uint32_t see = (k < 2 ? h.see0 : h.see1) >> (16 * (k & 1)), some = (k < 2 ? has[0] : has[1]) >> (16 * (k & 1));
+    const uint32_t see = (k < 2 ? h.see0 : h.see1) >> (16 * (k & 1)), some = (k < 2 ? h.some.x : h.some.y) >> (16 * (k & 1));
     const float f = fmaxf(h.cq * h.ks[k], 1.17549435e-38f);
     uint32_t y[16];
     tmem_ld16(h.at + 16 * k, y);
@@ -266,16 +258,16 @@ __device__ __noinline__ bool move_row(Row* row, const Half& h, float top) {
       }
     }
     tmem_st16(h.at + 16 * k, y);
-    if (top16 > -INFINITY) en = fmaxf(en, rintf(below(top16, mn) + h.lv[k]));
+    if (top16 > -INFINITY) topv = fmaxf(topv, below(top16, mn) + h.lv[k]);
   }
   tmem_st_wait();
+  const float en = next_unit(r.unit, by, topv);
   r.by = r.unit == -INFINITY ? 1.f : fast_exp2(by + (r.unit - en));
   r.from += shift;
   r.m = mn - shift;
   r.unit = en;
   r.steep = steep;
   *row = r;
-  return true;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -445,29 +437,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
           // A score is too high for m, or an addend for the unit: both are moved, and what has been summed up, in l and
           // in O, with them.
           const float all = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), mn = fmaxf(m, rintf(all));
-          float low = unit == kNoUnit ? INFINITY : unit, high = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (top[k] > -INFINITY) {
-              const float lv = inf.lv[4 * half + k];
-              high = fmaxf(high, lv);
-              if (unit == kNoUnit) low = fminf(low, lv);
-            }
-          const bool odd = __any_sync(0xffffffffu, steep || high > low + kJump || (fabsf(mn) > kSteep && fabsf(mn) < INFINITY));
+          alive = __all_sync(0xffffffffu, wait(kVFull + (now & 1), now >> 1));
+          if (!alive) break;
+          Half h{at, cq, inf.ks + 4 * half, inf.lv + 4 * half, 0xffffffffu, 0xffffffffu,
+                 keys_with_values<D>(base + L::kOffV + (now & 1) * L::kTileBytes + half * 64 * 128)};
+          if (masked) {
+            h.see0 = seen(lo - k0, hi - k0, bad);
+            h.see1 = seen(lo - k0 - 32, hi - k0 - 32, bad >> 2);
+          }
+          const bool odd = __any_sync(0xffffffffu, steep || (h.see0 & ~h.some.x) || (h.see1 & ~h.some.y) || (fabsf(mn) > kSteep && fabsf(mn) < INFINITY));
           float fo;
           if (odd) {
             Row row{m, unit == kNoUnit ? -INFINITY : unit, l, from, 1.f, steep};
-            Half h{at, cq, inf.ks + 4 * half, inf.lv + 4 * half, 0xffffffffu, 0xffffffffu,
-                   base + L::kOffV + (now & 1) * L::kTileBytes + half * 64 * 128, bar + kVFull + (now & 1), (now >> 1) & 1, a.wait_ns};
-            if (masked) {
-              h.see0 = seen(lo - k0, hi - k0, bad);
-              h.see1 = seen(lo - k0 - 32, hi - k0 - 32, bad >> 2);
-            }
-            alive = move_row<D>(&row, h, all);
-            if (!alive) {
-              if (a.d_status) atomicOr(a.d_status, TQ_DEV_TIMEOUT);
-              break;
-            }
+            move_row(&row, h, all);
             steep = row.steep;
             from = row.from;
             l = row.l;
@@ -476,10 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
             fo = row.by;
           } else {
             const float by = below(m, mn);
-            float en = unit == kNoUnit ? -INFINITY : unit + by;
+            float topv = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (top[k] > -INFINITY) en = fmaxf(en, rintf(below(top[k], mn) + inf.lv[4 * half + k]));
+              if (top[k] > -INFINITY) topv = fmaxf(topv, below(top[k], mn) + inf.lv[4 * half + k]);
+            const float en = next_unit(unit == kNoUnit ? -INFINITY : unit, by, topv);
             fo = unit == kNoUnit ? 1.f : fast_exp2(by + (unit - en));
             l *= fast_exp2(by);
             m = mn;

@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D)) cache8_rows_kernel(Att
                 topv = fmaxf(topv, below(s[nt][2 * x + e], mn) + octaves(scale[4 + (nt >> 1)]));
           topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 1));
           topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 2));
-          const float en = fmaxf(unit[x] + by, rintf(topv));
+          const float en = next_unit(unit[x], by, topv);
           f[x] = unit_step(m[x], unit[x], mn, en);
           l[x] *= fast_exp2(by);
           m[x] = mn;

@@ -191,3 +191,61 @@ def test_values_near_the_largest(case):
     out, lse = _attend(s, q, lens, od)
     assert bool(torch.isfinite(out).all())
     _check(s, q, lens, out, lse, od)
+
+
+LONG = [("int8", 64, 1, 2, "f32", "f32"), ("e4m3", 128, 4, 1, "bf16", "bf16"), ("e4m3", 64, 4, 3, "bf16", "bf16"),
+        ("int8", 64, 2, 40, "bf16", "bf16"), ("e4m3", 128, 2, 150, "bf16", "bf16"), ("e4m3", 128, 1, 70, "f32", "f32"),
+        ("int8", 256, 1, 66, "bf16", "bf16")]
+
+
+@pytest.mark.parametrize("octaves", [-70, 30, 90])
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(map(str, c)))
+def test_sequences_cut_between_many_ctas(case, octaves):
+    # Their records meet with units that lie far apart, some without an addend: the first third of the values is zero, the
+    # next one lies `octaves` above the last and weighs e^-40 of it.
+    code, d, group, nq, qd, od = case
+    rg = np.random.default_rng(abs(octaves) + d + nq)
+    lens = [9001, 700]
+
+    def shape(at, n):
+        third = 3 * at // n
+        return np.choose(third, [-1000, octaves, 0]), np.choose(third, [1.0, -40.0, 0.0])
+    s = _make(rg, lens, d, code, shape)
+    q = _queries(rg, len(lens), HEADS * group, nq, d, qd)
+    for kw in ({}, dict(window=6500)):
+        out, lse = _attend(s, q, lens, od, **kw)
+        _check(s, q, lens, out, lse, od, **kw)
+
+
+@pytest.mark.parametrize("power", [22, 40, 70])
+@pytest.mark.parametrize("case", FEW + MANY + LONG, ids=lambda c: "-".join(map(str, c)))
+def test_scores_of_any_size(case, power):
+    # Queries times 2^power: a row is the value of its largest score, where that is ahead by more than the scores' errors.
+    code, d, group, nq, qd, od = case
+    rg = np.random.default_rng(power + d + nq)
+    lens = [2500, 200, 3]
+    s = _make(rg, lens, d, code, lambda at, n: (10 * np.sin(at // BLOCK), np.zeros(n)), lambda at, n: 3 * at / n)
+    q = _queries(rg, len(lens), HEADS * group, nq, d, qd) * 2.0 ** power
+    out, lse = _attend(s, q, lens, od)
+    assert not bool(torch.isnan(out).any()) and not bool(torch.isnan(lse).any())
+    checked = 0
+    for i, n in enumerate(lens):
+        pages = s.dtable[i, :-(-n // BLOCK)].long()
+        see = torch.arange(n, device="cuda")[None] <= n - nq + torch.arange(nq, device="cuda")[:, None]
+        for j in range(HEADS):
+            k, v = ((getattr(s.cache, m)[pages, j].view(torch.float8_e4m3fn if code == "e4m3" else torch.int8).float().double() *
+                     getattr(s.cache, m + "_scale")[pages, j].double()[:, None, None]).reshape(-1, d)[:n] for m in ("k", "v"))
+            x = q[i, j * group:j * group + group].double()
+            score = (x @ k.T / d ** 0.5).masked_fill(~see, -torch.inf)
+            size = (x.abs() @ k.abs().T / d ** 0.5).masked_fill(~see, 0.0).amax(-1)
+            two = score.topk(2, -1)
+            top, at = two.values[..., 0], two.indices[..., 0]
+            some = ~torch.isinf(top)
+            es = ((2 * d / 16 + 8) * 2.0 ** -23 + 2.0 ** -21) * size
+            got, have = out[i, j * group:j * group + group].double(), lse[i, j * group:j * group + group].double()
+            assert bool(((have - top).abs() <= es + 10.0)[some].all())        # the sum of weights adds ln n at most
+            ahead = some & (top - two.values[..., 1] > 2 * es + 60.0)
+            ref = v[at]
+            assert bool(((got - ref).abs() <= (HALF[od] + 2.0 ** -11) * ref.abs() + 1e-20)[ahead].all())
+            checked += int(ahead.sum())
+    assert checked > 0
