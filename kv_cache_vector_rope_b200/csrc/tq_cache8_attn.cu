@@ -897,14 +897,15 @@ cudaError_t launch_types(bool qf, bool of, const Maps& m, const AttnArgs& a, cud
 
 // Query rows a CTA takes together: 16 where a KV head has more than 8 and their
 // sums fit the registers (d up to 128, not fp32; twelve rows over 8 x 32768 keys,
-// d = 128: 143 us, by eights 2 x 98). Over int8 codes up to four rows are one
-// tile of byte products with two of q's limbs a column: one step of a decode of
-// 8 x 32768 keys took, against the half products' eight columns, 66 against 75 us
-// (d = 64), 100 against 102 (d = 256), and with fp32 queries 101 against 116 (d =
-// 128); with bf16 queries at d = 128 102 against 96, so there they stay away, as
-// they do from 5 to 8 rows (two such tiles: 125 against 98 us).
+// d = 128: 141 us, by eights 190; d = 64 98, 116). Over int8 codes up to four rows
+// are one tile of byte products with two of q's limbs a column where that is the
+// faster: one step of a decode of 8 x 32768 keys took, against the half products'
+// eight columns, 62 against 71 us (d = 64), and with fp32 queries 64 against 84 (d =
+// 64), 104 against 117 (d = 128), 108 against 112 (d = 256); with bf16 queries 102
+// against 97 (d = 128) and 109 against 98 (d = 256), so there they stay away, as they
+// do from 5 to 8 rows (two such tiles: 125 against 98 us).
 int rows_of(int d, int rows, bool qf, bool of, bool int8) {
-  if (int8 && rows <= 4 && (qf || d != 128)) return 4;
+  if (int8 && rows <= 4 && (qf || d == 64)) return 4;
   return rows > 8 && d <= 128 && !qf && !of ? 16 : 8;
 }
 
@@ -920,7 +921,7 @@ bool streams_alone(int d, int64_t streams, int64_t most_keys) {
 template <int D>
 cudaError_t launch_few(bool int8, int tile, bool qf, bool of, const Maps& m, const AttnArgs& a, cudaStream_t st) {
   if (tile == 4) {
-    if constexpr (D != 128) return launch_types<D, true, true, 1>(qf, of, m, a, st);
+    if constexpr (D == 64) return launch_types<D, true, true, 1>(qf, of, m, a, st);
     else return of ? launch_attn<D, true, true, 1, true, true>(m, a, st) : launch_attn<D, true, true, 1, true, false>(m, a, st);
   }
   if constexpr (D <= 128)
