@@ -448,7 +448,8 @@ tq_status tq_qk_norm_rope(int32_t d, int32_t rot_dim, int64_t n_tokens, int32_t 
  * A scale is 2^e with the smallest e >= -100 such that the block's largest
  * magnitude is at most 448 * 2^e (e4m3) or 127 * 2^e (int8). Being a power of
  * two it divides exactly, so a code is its value's one rounding (nearest, ties
- * to even), and reading back is exact in fp32 and bf16.
+ * to even), and reading back is exact in fp32 and bf16. (Attention takes a value
+ * scale by its exponent alone.)
  * ---------------------------------------------------------------------- */
 typedef enum { TQ_E4M3 = 0, TQ_INT8 = 1 } tq_code8;
 

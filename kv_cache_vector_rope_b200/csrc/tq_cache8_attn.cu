@@ -10,10 +10,11 @@
 //
 // A decode step is bound by the cache's bytes (2 d per key and KV head), so the
 // work is cut along the keys: all (sequence, KV head, row tile, 64-key tile)
-// units in that order are dealt in equal contiguous ranges to the CTAs, however
-// long or ragged the sequences are. A range that ends inside a sequence leaves
-// a partial record (m, l, sum) that cache8_combine_kernel merges; a CTA writes
-// at most two of them.
+// units in that order are dealt to the CTAs in contiguous ranges of equal cost,
+// a stream's start counting as several units, however long or ragged the
+// sequences are. A range that ends inside a sequence leaves a partial record
+// (m, l, unit, sum) that cache8_combine_kernel merges; a CTA writes at most two of
+// them.
 //
 // Each warp takes groups of 16 keys of its CTA's range and keeps its own
 // running (m, l, sum). A group lies in one page; its keys and values come by two
@@ -34,11 +35,11 @@
 // score costs a quarter of the keys' conversions and half the instructions.
 //
 // Bound by instruction issue beside the memory: unpacking 8-bit codes for the
-// matrix unit, softmax and the two products fill 56% of the issue slots and 47%
-// of the integer pipe where streams are short. Measured, floor of the cache's bytes in brackets: a step of
-// 8 sequences of 32768 keys, 8 KV heads, 4 rows each, d = 128, 98 us (82); one
-// sequence of 131072 keys 54 us (41); four drafted fp32 rows of 32 ragged
-// sequences, 20 KV heads, d = 64, 71 us (40).
+// matrix unit, softmax and the two products fill 52% of the issue slots and 50%
+// of the integer pipe at d = 128. Measured, floor of the cache's bytes in brackets: a
+// step of 8 sequences of 32768 keys, 8 KV heads, 4 rows each, d = 128, 101 us (82),
+// d = 64 64 us (41); one sequence of 131072 keys 56 us (41); four drafted fp32 rows
+// of 32 ragged sequences, 20 KV heads, d = 64, 77 us (40).
 #include <cuda.h>
 
 #include "tq_cache8_attn.cuh"
@@ -55,8 +56,9 @@ constexpr int kAtGrid = kMaxRecs;                    // at most two CTAs per SM
 constexpr int kUnit = 64;                            // keys per unit of the split
 constexpr int kMinUnits = 2;                         // a CTA takes at least this many units
 // What a segment's start and merge cost a CTA beside its keys, in units. Four drafted fp32 rows of 32 ragged sequences,
-// 20 KV heads, d = 64: 94 us at 8, 86 at 12, 82 at 16, 83 at 24; 8 heads of d = 128: 54.0 at 8, 53.3 at 12, 57 at 24;
-// 4 heads of d = 256: 72 at 4, 65 at 8, 60 at 14.
+// 20 KV heads, d = 64: 79 us at 8, 77 at 12 and 16, 78 at 24; d = 128: one sequence of 131072 keys 56.4 at 8 and 12, 55.8
+// at 24, 16 rows of 32 ragged sequences 105, 102 and 110; 4 heads of d = 256, 32 ragged sequences: 66 at 4, 62 at 8, 60
+// at 14, 66 at 24.
 constexpr int lead_of(int d) { return d == 64 ? 16 : d == 128 ? 8 : 14; }
 constexpr int kSlice = 512;                          // sequences of one launch
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -910,9 +912,9 @@ int rows_of(int d, int rows, bool qf, bool of, bool int8) {
 }
 
 // Whether each CTA takes one stream by itself, without the lengths' sums before it and the merge behind: where there are
-// a few streams per CTA at most and none can be long. One token, d = 128, 8 streams of 100 keys: 5.6 us against 8.6 split
-// over the CTAs, of 400 8.4 against 9.5, of 777 11.4 against 9.7; 240 streams of 1000 keys 19 against 25; 512 of 100 12
-// against 16, of 1000 35 against 38; 2048 streams of 60 keys 41 against 40.
+// a few streams per CTA at most and none can be long. One token, d = 128, 8 streams of 100 keys: 6.9 us against 9.6 split
+// over the CTAs, of 400 9.7 against 10.6, of 777 13.0 against 10.8; 240 streams of 1000 keys 21 against 27; 512 of 100 14
+// against 18, of 1000 39 against 42; 2048 streams of 60 keys 46 against 44.
 bool streams_alone(int d, int64_t streams, int64_t most_keys) {
   const int ctas = kSms * (d == 256 ? Plan<256>::kCtas : Plan<128>::kCtas);
   return streams <= 4 * ctas && most_keys * d <= (2 * streams > ctas ? 1024 : 512) * 128;

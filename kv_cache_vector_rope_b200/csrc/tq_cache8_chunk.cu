@@ -23,8 +23,8 @@
 // two looks at barriers: about 2100 cycles, of which the other half's weights
 // cover 1400) beside shared memory (about 3000 of 4700 cycles a step). Measured:
 // 1024 tokens of two sequences of 8192, 8 KV heads of 4 query heads, d = 128,
-// 294 us (the products alone 158 at the library's rate), d = 64 246 us; a prompt
-// of 4 x 2048 tokens, d = 128, 250 us.
+// 296 us (the products alone 158 at the library's rate), d = 64 260 us; a prompt
+// of 4 x 2048 tokens, d = 128, 248 us.
 #include "tq_cache8_attn.cuh"
 
 namespace tq {
@@ -776,6 +776,10 @@ cudaError_t launch_one(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// Up to 64 rows go to the few-row kernel, which a short sequence wants: one of 1000 keys, 8 KV heads, 64 rows, 21.6 us
+// against 23.4 here (d = 64: 16.6 against 21.2). Over long ones this kernel would be the faster from 17 rows on, d = 128 (8 x
+// 32768 keys: 16 rows 143 there, 205 here, 24 rows 257 and 207, 64 rows 500 and 212; 8 x 2048 keys, 24 rows 42 and 34),
+// and from 33 on, d = 64 (32 rows 181 and 189, 48 rows 260 and 190).
 bool chunk_supported(int d, bool f32, int rows) { return (d == 64 || d == 128) && !f32 && rows > 64; }
 
 size_t chunk_record_bytes(int d) { return sizeof(float) * kSms * 2 * kChunkRows * static_cast<size_t>(kRecHead + d); }

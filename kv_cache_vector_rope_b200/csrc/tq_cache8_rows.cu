@@ -15,8 +15,8 @@
 // Bound by the matrix instructions: 2 x 128 of them a warp and tile at d = 128,
 // fp32, or at d = 256, 1.23 ns each per SM, half of the time; the rest is the
 // conversion, the weights and the barriers between them. Measured, 512 rows of
-// two sequences of 8192 tokens: 8 KV heads of 4 fp32 heads, d = 128, 1058 us (by
-// eights of rows 2040); 4 KV heads, d = 256, bf16 615 us, fp32 977 us.
+// two sequences of 8192 tokens: 8 KV heads of 4 fp32 heads, d = 128, 1118 us (by
+// eights of rows 2040), d = 64 568 us; 4 KV heads, d = 256, bf16 641 us, fp32 989 us.
 #include "tq_cache8_attn.cuh"
 
 namespace tq {
@@ -29,7 +29,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kTile = kRowsUnit;                     // keys at a time
 static_assert(kTile == 64 && kRowsTile == 16 * kWarps, "four groups of 16 keys, 16 rows a warp");
 
-// CTAs per SM: at d = 64 two, whose barriers and products overlap (512 fp32 rows of 2 x 8192 tokens 657 -> 559 us,
+// CTAs per SM: at d = 64 two, whose barriers and products overlap (512 fp32 rows of 2 x 8192 tokens 657 -> 559 us when it was chosen,
 // though 128 registers spill 200 bytes); at d = 128 two do not fit shared memory.
 constexpr int rows_ctas(int d) { return d <= 64 ? 2 : 1; }
 
@@ -454,8 +454,10 @@ cudaError_t launch_code(bool int8, const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Up to 64 rows the few-row kernel is the faster: two sequences of 8192 tokens, 8 KV heads, d = 128, fp32: 61 us with 64
-// rows against 75 here, and 86 with 68 rows there. d = 256, 4 KV heads: 52 against 64.
+// Up to 64 rows the few-row kernel is the faster: two sequences of 8192 tokens, 8 KV heads, d = 128, fp32: 64 us with 64
+// rows against 79 here, d = 64 50 against 54; 4 KV heads of d = 256, bf16 54 against 82. From 256 rows on this one is: 168
+// us against 202, 102 against 150, 122 against 162. Between them they cross twice, a tile of 128 rows costing the same
+// however full (128 rows 103 against 111, 132 rows 167 against 116).
 constexpr int kRowsFrom = 64;
 bool rows_supported(int d, bool f32, int rows) { return (f32 || d == 256) && rows > kRowsFrom; }
 

@@ -16,7 +16,7 @@
 // through sincospif: far positions lose whole turns only) and stay in registers
 // as products with the weights while the warp walks the token's heads.
 //
-// Bound by memory: 16384 tokens of 40 bf16 heads of 128 64.2 us (51.3 at the
+// Bound by memory: 16384 tokens of 40 bf16 heads of 128 64.9 us (51.3 at the
 // copy's rate; more CTAs per SM 72 to 91 us), 1021
 // tokens of 40 fp32 heads of 64 6.0 us (3.2), 8 tokens 2.9 us, which is launch,
 // one load, the angles and one store, each waiting for the last.
