@@ -26,7 +26,8 @@
 // eight query rows as the columns, which suits the few rows of a step: every
 // 8-bit code is exactly a half, and a query row is scaled by a power of two
 // into half's range (exact for bf16; fp32 queries and fp32 outputs use two
-// half limbs for q and for p). Weights carry the octaves of the value scale over a unit of the row's own (Weigh). The contraction index of both products is
+// half limbs for q and for p). Weights carry the octaves of the value scale over a
+// unit of the row's own (Weigh). The contraction index of both products is
 // permuted so that a lane's operands are 16 contiguous bytes of the cache.
 //
 // Up to four rows over int8 codes multiply the bytes as they are (16x8x32): q in
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
     // The rows' m and e, and what follows from them: two tiles' do not fit the registers and lie where the warp's maxima
     // and sums go at the end (twelve rows over 8 x 32768 keys: 149 us in registers).
     constexpr bool kHold = NT == 1;
-    float mh[kHold ? NT : 1][kHold ? NJ : 1], eh[kHold ? NT : 1][kHold ? NJ : 1];
+    float mh[kHold ? NT : 1][kHold ? NJ : 1] = {}, eh[kHold ? NT : 1][kHold ? NJ : 1] = {};
     const auto m_of = [&](int nt, int j) { return kHold ? mh[kHold ? nt : 0][kHold ? j : 0] : sm_m[w * kRows + row_of(nt, j)]; };
     const auto e_of = [&](int nt, int j) { return kHold ? eh[kHold ? nt : 0][kHold ? j : 0] : sm_l[w * kRows + row_of(nt, j)]; };
     const auto set_m = [&](int nt, int j, float x, float y) {
@@ -392,17 +393,18 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
         sm_l[w * kRows + row_of(nt, j)] = y;
       }
     };
-    Weigh wg[kHold ? G : 1][kHold ? NT : 1][kHold ? NJ : 1];     // for value scales of 2^lv
-    float lv[G];
-    const auto weigh_of = [&](int x, int nt, int j) { return kHold ? wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] : weigh(m_of(nt, j), e_of(nt, j), lv[x]); };
+    Weigh wg[kHold ? G : 1][kHold ? NT : 1][kHold ? NJ : 1] = {};        // for value scales of 2^lv
+    float lv[G] = {};
+    const auto weigh_of = [&](int x, int nt, int j) {
+      return kHold ? wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] : weigh(m_of(nt, j), e_of(nt, j), lv[x]);
+    };
     const auto weigh_all = [&] {
-      if (!kHold) return;
+      if constexpr (kHold) {
 #pragma unroll
-      for (int x = 0; x < G; ++x)
+        for (int x = 0; x < G; ++x)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) wg[kHold ? x : 0][kHold ? nt : 0][kHold ? j : 0] = weigh(m_of(nt, j), e_of(nt, j), lv[x]);
+          for (int j = 0; j < NJ; ++j) wg[x][0][j] = weigh(m_of(0, j), e_of(0, j), lv[x]);
+      }
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -415,8 +417,6 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
       for (int x = 0; x < MT; ++x) acc[nt][x][0] = acc[nt][x][1] = acc[nt][x][2] = acc[nt][x][3] = 0.f;
     }
     if (!kHold) __syncwarp();
-#pragma unroll
-    for (int x = 0; x < G; ++x) lv[x] = 0.f;
     weigh_all();
     for (int i = 0; i < turns; ++i) {
       constexpr int kBatch = 32 / G;                 // turns of a batch of pages
@@ -654,8 +654,8 @@ __global__ void __launch_bounds__(kAtThreads, Plan<D>::kCtas)
             for (int e = 0; e < 4; ++e) acc[nt][x][e] *= f[e % NJ];
           }
         }
-        if (kHold) weigh_all();
-        else __syncwarp();
+        weigh_all();
+        if (!kHold) __syncwarp();
       }
       uint32_t ph0[G][NT][2], ph1[G][NT][2];
 #pragma unroll

@@ -445,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_chunk_kernel(AttnArgs a) {
             h.see0 = seen(lo - k0, hi - k0, bad);
             h.see1 = seen(lo - k0 - 32, hi - k0 - 32, bad >> 2);
           }
-          const bool odd = __any_sync(0xffffffffu, steep || (h.see0 & ~h.some.x) || (h.see1 & ~h.some.y) || (fabsf(mn) > kSteep && fabsf(mn) < INFINITY));
+          const bool odd = __any_sync(0xffffffffu, steep || (h.see0 & ~h.some.x) || (h.see1 & ~h.some.y) ||
+                                                       (fabsf(mn) > kSteep && fabsf(mn) < INFINITY));
           float fo;
           if (odd) {
             Row row{m, unit == kNoUnit ? -INFINITY : unit, l, from, 1.f, steep};
